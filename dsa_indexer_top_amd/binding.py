@@ -13,7 +13,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libecho.so")
 
 ECHO_OK, ECHO_EINVAL, ECHO_EUNSUPPORTED, ECHO_EHIP, ECHO_EWORKSPACE = 0, -1, -2, -3, -4
-ST_EXHAUSTED, ST_BAD_HOST, ST_DUP_HOST, ST_CACHE_FULL = 1, 2, 4, 8
+ST_EXHAUSTED, ST_BAD_HOST, ST_DUP_HOST, ST_CACHE_FULL, ST_NO_PAGES, ST_BAD_LEN = 1, 2, 4, 8, 16, 32
+BF16, FP16, FP32 = 0, 1, 2
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 RECALL_GATHER, RECALL_MEMCPY = 0, 1
 PREFETCH_OFF, PREFETCH_RANGED, PREFETCH_FUSED = 0, 1, 2
 FUSED_MAX_RANGE, FUSED_MAX_PER_RANGE = 8192, 128
@@ -55,6 +57,22 @@ class AppendArgs(C.Structure):
                 ("new_kv", P), ("new_host", P), ("k", P), ("k_scale", P), ("key_begin", P),
                 ("key_len", P), ("req_to_host", P), ("host_kv_w", P), ("step_id", I32),
                 ("step_dev", P)]
+
+
+class PageArgs(C.Structure):
+    _fields_ = [("n_rows", I32), ("page_size", I32), ("max_pages", I32), ("n_pages", I32),
+                ("max_new", I32), ("len_in", P), ("new_len", P), ("done", P), ("page_table", P),
+                ("free_list", P), ("count_in", P), ("len_out", P), ("count_out", P),
+                ("row_begin", P), ("slot", P), ("row", P), ("pos", P), ("status", P)]
+
+
+class QkArgs(C.Structure):
+    _fields_ = [("n_tok", I32), ("n_q_heads", I32), ("n_k_heads", I32), ("head_dim", I32),
+                ("type", I32), ("q_norm", I32), ("k_norm", I32), ("rot_begin", I32),
+                ("rot_dim", I32), ("interleaved", I32), ("n_pos", I32), ("eps", F32), ("q", P),
+                ("k", P), ("q_tok_stride", I64), ("q_head_stride", I64), ("k_tok_stride", I64),
+                ("k_head_stride", I64), ("q_weight", P), ("q_bias", P), ("k_weight", P),
+                ("k_bias", P), ("pos", P), ("cos_sin", P)]
 
 
 _SIGS = {
@@ -99,6 +117,13 @@ _SIGS = {
     "echo_graph_end": (C.c_int, [P, C.POINTER(P)]),
     "echo_graph_launch": (C.c_int, [P, P]),
     "echo_graph_destroy": (C.c_int, [P]),
+    "echo_page_workspace_bytes": (SZ, [I32, I32]),
+    "echo_page_step": (C.c_int, [C.POINTER(PageArgs), P, SZ, P]),
+    "echo_quant_fp8": (C.c_int, [P, I32, I64, I32, I64, P, I64, P, I64, I64, P]),
+    "echo_matmul_fp8": (C.c_int, [P, I64, P, I64, I64, P, I64, P, I64, I64, I32, I32, I32, P, I64,
+                                  I32, P]),
+    "echo_qk_norm_rope": (C.c_int, [C.POINTER(QkArgs), P, I64, I64, P, I64, I64, P]),
+    "echo_indexer_qk": (C.c_int, [C.POINTER(QkArgs), P, I64, F32, P, P, P, P, P, I64, P]),
     "echo_host_alloc": (C.c_int, [SZ, C.c_int, C.POINTER(P), C.POINTER(P)]),
     "echo_host_free": (C.c_int, [P]),
 }
@@ -325,6 +350,212 @@ def decode_append(args, pool, new_slot, ws, stream=None):
 
 def step_advance(step_dev, stream=None):
     _call("echo_step_advance", ptr(step_dev), stream_handle(stream))
+
+
+# ---------------------------------------------------------------- before the scores
+# The calls below take tensors whole, so their types, shapes, strides and device are checked here
+# before anything is enqueued (ECHO_EINVAL); the rest of the checks are the library's.
+DEVICE_TYPE = "cuda"
+
+
+def _refuse(fn, what):
+    raise EchoError(fn, ECHO_EINVAL, what)
+
+
+def _on_device(fn, stream, *tensors):
+    """The stream handle; every tensor given is on the current device."""
+    import torch
+    if DEVICE_TYPE == "cuda":
+        cur = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != cur:
+                _refuse(fn, "a tensor on %s; the current device is cuda:%d" % (t.device, cur))
+    return stream_handle(stream)
+
+
+def _want(fn, name, t, dtype, shape=None):
+    """t is a contiguous tensor of that type (and shape)."""
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(fn, "%s is not a contiguous %s tensor%s" % (
+            name, dtype, "" if shape is None else " of shape %s" % (tuple(shape),)))
+
+
+def _float_type(fn, name, t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return FP16
+    if t.dtype == torch.float32:
+        return FP32
+    return _refuse(fn, "%s is %s, not bf16, fp16 or fp32" % (name, t.dtype))
+
+
+def _row_stride(fn, name, t):
+    """Row stride of a matrix whose rows are contiguous."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        _refuse(fn, "the rows of %s are not contiguous" % name)
+    return max(t.stride(0), cols) if rows < 2 else t.stride(0)
+
+
+def _codes(fn, name, t):
+    """Row stride of a matrix of FP8 codes (uint8 or float8_e4m3fn)."""
+    import torch
+    if t.dtype != torch.uint8 and t.dtype != torch.float8_e4m3fn:
+        _refuse(fn, "%s is %s, not FP8 codes" % (name, t.dtype))
+    return _row_stride(fn, name, t)
+
+
+def _heads_strides(fn, name, t):
+    """Strides of tokens and heads; the stride of a dimension of one means nothing."""
+    if t.numel() and t.stride(2) != 1 and t.shape[2] > 1:
+        _refuse(fn, "the heads of %s are not contiguous" % name)
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def page_workspace_bytes(n_rows, max_new):
+    return lib().echo_page_workspace_bytes(n_rows, max_new)
+
+
+def page_step(len_in, new_len, page_table, page_size, free_list, count_in, len_out, count_out,
+              row_begin, slot, row, pos, status, ws, done=None, stream=None):
+    """One step of a paged cache's tables and maps (echo_page_step); ws may be None for a step
+    that needs no workspace, done and row may be None."""
+    import torch
+    fn, i32 = "echo_page_step", torch.int32
+    st = _on_device(fn, stream, len_in, new_len, page_table, free_list, count_in, len_out, count_out,
+                    row_begin, slot, row, pos, status, ws, done)
+    n, cap = len_in.shape[0], slot.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        _refuse(fn, "page_table has no row for each request")
+    _want(fn, "page_table", page_table, i32)
+    for name, t, shape in (("len_in", len_in, (n,)), ("new_len", new_len, (n,)),
+                           ("len_out", len_out, (n,)), ("row_begin", row_begin, (n + 1,)),
+                           ("pos", pos, (cap,)), ("count_in", count_in, (1,)),
+                           ("count_out", count_out, (1,)), ("status", status, (1,))):
+        _want(fn, name, t, i32, shape)
+    _want(fn, "free_list", free_list, i32)
+    _want(fn, "slot", slot, torch.int64)
+    if row is not None:
+        _want(fn, "row", row, i32, (cap,))
+    if done is not None and done.dtype != torch.bool:
+        _want(fn, "done", done, torch.uint8, (n,))
+    elif done is not None:
+        _want(fn, "done", done, torch.bool, (n,))
+    a = PageArgs(n, page_size, page_table.shape[1], free_list.numel(), cap, ptr(len_in), ptr(new_len),
+                 ptr(done), ptr(page_table), ptr(free_list), ptr(count_in), ptr(len_out),
+                 ptr(count_out), ptr(row_begin), ptr(slot), ptr(row), ptr(pos), ptr(status))
+    _call(fn, C.byref(a), ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), st)
+
+
+def quant_fp8(x, y, scale, stream=None):
+    """FP8 codes y and scales [rows, ceil(cols / 128)] (any strides) of a matrix x."""
+    fn = "echo_quant_fp8"
+    st = _on_device(fn, stream, x, y, scale)
+    if x.dim() != 2 or y.shape != x.shape or scale.shape != (x.shape[0], -(-x.shape[1] // 128)):
+        _refuse(fn, "shapes %s, %s, %s" % (tuple(x.shape), tuple(y.shape), tuple(scale.shape)))
+    if _float_type(fn, "scale", scale) != FP32:
+        _refuse(fn, "scale is not fp32")
+    _call(fn, ptr(x), _float_type(fn, "x", x), x.shape[0], x.shape[1], _row_stride(fn, "x", x), ptr(y),
+          _codes(fn, "y", y), ptr(scale), scale.stride(0), scale.stride(1), st)
+
+
+def matmul_fp8(a, a_scale, b, b_scale, c, stream=None):
+    """c [m, n] = a [m, k] times b [n, k] transposed, FP8 codes with fp32 scales: a_scale [m,
+    ceil(k / 128)] and b_scale [ceil(n / 128), ceil(k / 128)], any strides."""
+    fn = "echo_matmul_fp8"
+    st = _on_device(fn, stream, a, a_scale, b, b_scale, c)
+    if a.dim() != 2 or b.dim() != 2 or c.dim() != 2:
+        _refuse(fn, "a, b and c are matrices")
+    (m, k), n = a.shape, b.shape[0]
+    nb = -(-k // 128)
+    if b.shape[1] != k or c.shape != (m, n) or a_scale.shape != (m, nb) or b_scale.shape != (-(-n // 128), nb):
+        _refuse(fn, "shapes %s" % (tuple(tuple(t.shape) for t in (a, a_scale, b, b_scale, c)),))
+    if _float_type(fn, "a_scale", a_scale) != FP32 or _float_type(fn, "b_scale", b_scale) != FP32:
+        _refuse(fn, "a scale is not fp32")
+    lda, ldb = _codes(fn, "a", a), _codes(fn, "b", b)
+    for name, t, rows, ld in (("a", a, m, lda), ("b", b, n, ldb)):
+        # the last row is read in 16-byte pieces as well
+        if rows and k % 16 and t.untyped_storage().nbytes() - t.storage_offset() < (rows - 1) * ld + -(-k // 16) * 16:
+            _refuse(fn, "the last row of %s ends inside a 16-byte piece" % name)
+    _call(fn, ptr(a), -(-lda // 16) * 16 if m < 2 else lda, ptr(a_scale), a_scale.stride(0),
+          a_scale.stride(1), ptr(b), -(-ldb // 16) * 16 if n < 2 else ldb, ptr(b_scale),
+          b_scale.stride(0), b_scale.stride(1), m, n, k, ptr(c), _row_stride(fn, "c", c),
+          _float_type(fn, "c", c), st)
+
+
+def _qk_args(fn, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias, k_norm,
+             k_weight, k_bias):
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        _refuse(fn, "q and k are [tokens, heads, head_dim]")
+    n, dim = q.shape[0], q.shape[2]
+    kind = _float_type(fn, "q", q)
+    if k.dtype != q.dtype:
+        _refuse(fn, "q and k have different types")
+    qt, qh = _heads_strides(fn, "q", q)
+    kt, kh = _heads_strides(fn, "k", k)
+    _want(fn, "pos", pos, torch.int32, (n,))
+    rot = n_pos = 0
+    if cos_sin is not None:
+        _want(fn, "cos_sin", cos_sin, torch.float32)
+        if cos_sin.dim() != 2:
+            _refuse(fn, "cos_sin is [positions, rotated values]")
+        n_pos, rot = cos_sin.shape
+    else:
+        n_pos = INF
+    for name, t in (("q_weight", q_weight), ("q_bias", q_bias), ("k_weight", k_weight), ("k_bias", k_bias)):
+        if t is not None:
+            _want(fn, name, t, torch.float32, (dim,))
+    return QkArgs(n, q.shape[1], k.shape[1], dim, kind, q_norm, k_norm, rot_begin, rot,
+                  1 if interleaved else 0, n_pos, eps, ptr(q), ptr(k), qt, qh, kt, kh, ptr(q_weight), ptr(q_bias), ptr(k_weight), ptr(k_bias),
+                  ptr(pos), ptr(cos_sin))
+
+
+def qk_norm_rope(q, k, q_out, k_out, pos, cos_sin, rot_begin=0, interleaved=False, q_norm=NORM_NONE,
+                 q_weight=None, q_bias=None, k_norm=NORM_NONE, k_weight=None, k_bias=None, eps=1e-6,
+                 stream=None):
+    """Norms and rotation of query and key heads [tokens, heads, head_dim], any strides of tokens
+    and heads; the rotated part has cos_sin's width.  q_out / k_out may be q / k."""
+    fn = "echo_qk_norm_rope"
+    st = _on_device(fn, stream, q, k, q_out, k_out, pos, cos_sin, q_weight, q_bias, k_weight, k_bias)
+    a = _qk_args(fn, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias,
+                 k_norm, k_weight, k_bias)
+    for name, t, x in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t.shape != x.shape or t.dtype != x.dtype:
+            _refuse(fn, "%s does not match its input" % name)
+    _call(fn, C.byref(a), ptr(q_out), *_heads_strides(fn, "q_out", q_out), ptr(k_out),
+          *_heads_strides(fn, "k_out", k_out), st)
+
+
+def indexer_qk(q, k, w, q8, w_out, k_cache, k_scale, slot, pos, cos_sin, w_mul=1.0, rot_begin=0,
+               interleaved=False, q_norm=NORM_NONE, q_weight=None, q_bias=None, k_norm=NORM_NONE,
+               k_weight=None, k_bias=None, eps=1e-6, stream=None):
+    """The indexer's inputs from query heads q [tokens, heads, 128], keys k [tokens, 1, 128] and
+    head weights w [tokens, heads]: FP8 queries q8, weights w_out with the queries' scales folded
+    in, and the keys as rows slot[t] of k_cache [slots, 128] / k_scale [slots]."""
+    import torch
+    fn = "echo_indexer_qk"
+    st = _on_device(fn, stream, q, k, w, q8, w_out, k_cache, k_scale, slot, pos, cos_sin, q_weight,
+                    q_bias, k_weight, k_bias)
+    a = _qk_args(fn, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias,
+                 k_norm, k_weight, k_bias)
+    n, heads, dim = q.shape
+    if w.dtype != torch.float32 or w.shape != (n, heads) or (heads > 1 and w.stride(1) != 1):
+        _refuse(fn, "w is not fp32 [tokens, heads] with contiguous rows")
+    _want(fn, "q8", q8, q8.dtype, (n, heads, dim))
+    _want(fn, "k_cache", k_cache, k_cache.dtype)
+    for name, t in (("q8", q8), ("k_cache", k_cache)):
+        if t.dtype != torch.uint8 and t.dtype != torch.float8_e4m3fn:
+            _refuse(fn, "%s is %s, not FP8 codes" % (name, t.dtype))
+    _want(fn, "w_out", w_out, torch.float32, (n, heads))
+    _want(fn, "k_scale", k_scale, torch.float32)
+    if k_cache.numel() != k_scale.numel() * dim:
+        _refuse(fn, "k_cache and k_scale hold different numbers of keys")
+    _want(fn, "slot", slot, torch.int64, (n,))
+    _call(fn, C.byref(a), ptr(w), w.stride(0), w_mul, ptr(q8), ptr(w_out), ptr(k_cache), ptr(k_scale),
+          ptr(slot), k_scale.numel(), st)
 
 
 class CapturedGraph:

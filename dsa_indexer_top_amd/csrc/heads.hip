@@ -1,0 +1,304 @@
+// Norms of query and key heads with the position rotation in the same pass, written back in the
+// inputs' type (echo_qk_norm_rope) or as FP8 queries, folded score weights and rows of the
+// indexer's key cache (echo_indexer_qk).
+//
+// One head of one token is a row of D values.  With the row's 32-bit values x_i:
+//   RMS norm     n_i = x_i / sqrt(mean(x^2) + eps) * w_i
+//   layer norm   n_i = (x_i - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * w_i + b_i
+//   rotation     the pair (u, v) at angle index p becomes (u c_p - v s_p, v c_p + u s_p),
+//                c and s from row pos of the table; pairs are (i, i + R/2) or (2i, 2i + 1) of
+//                the R rotated values, which start at rot_begin
+//   FP8          scale = max(amax(n) / 448, 2^-126), codes n / scale
+//
+// A row is held by G lanes of 8 values (G the power of two that covers D), so a wave reads 64/G
+// rows with 16-byte loads, the sums are butterflies over those lanes, and the partner of a
+// rotated half comes from another lane of the row.  Everything is read once and written once:
+// the kernel is bound by HBM at many tokens and by launch latency at few.  Query rows and key
+// rows are separate workgroups, so a wave loads the norm's weights once for all its rows.
+#include "float_types.cuh"
+
+namespace echo {
+
+constexpr int HT = 256;          // threads per workgroup
+constexpr int HU = 4;            // row groups per wave
+
+struct HeadSide {                // the query or the key side
+  const void *x;
+  void *y;
+  int64_t xt, xh, yt, yh;        // strides of tokens and heads, in elements
+  const float *weight, *bias;
+  int32_t heads, norm;
+};
+struct Fp8Side {                 // what the FP8 form writes
+  const float *w;
+  int64_t wt;
+  float w_mul;
+  uint8_t *q8;
+  float *w_out;
+  uint8_t *k_cache;
+  float *k_scale;
+  const int64_t *slot;
+  int64_t n_slots;
+};
+struct HeadArgs {
+  HeadSide side[2];
+  Fp8Side f;
+  const int32_t *pos;
+  const float *cos_sin;
+  int32_t n_tok, dim, rot_begin, rot, n_pos;
+  uint32_t q_groups;             // workgroups of the query side
+  float eps;
+};
+
+// Eight floats; the table's and the weights' rows are 16-byte aligned (checked by the host).
+ECHO_DEV void load_f8(const float *__restrict__ p, float (&v)[VEC]) {
+  const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+}
+
+template <typename T, int G, bool FP8, bool NEXT>
+__global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
+  constexpr int ROWS = 64 / G;                       // rows of one wave-wide load
+  const int l = lane_id(), sub = l / G, j = l % G;
+  const bool is_k = blockIdx.x >= a.q_groups;
+  const HeadSide &s = a.side[is_k ? 1 : 0];
+  const uint32_t blk = is_k ? blockIdx.x - a.q_groups : blockIdx.x;
+  const uint32_t first = (blk * (HT / 64) + (threadIdx.x >> 6)) * (HU * ROWS);
+  const uint32_t heads = static_cast<uint32_t>(s.heads);
+  const uint32_t n_rows = static_cast<uint32_t>(a.n_tok) * heads;
+  const bool in_row = j * VEC < a.dim;
+
+  // this lane's place in the rotation
+  const int e = j * VEC - a.rot_begin, half = a.rot >> 1;
+  const bool turns = in_row && e >= 0 && e < a.rot;
+  const bool second = !NEXT && e >= half;
+  const int angle = NEXT ? e >> 1 : (second ? e - half : e);
+  const int mate = turns && !NEXT ? l + (second ? -(half / VEC) : half / VEC) : l;
+
+  float wt[VEC], bi[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) { wt[i] = 1.f; bi[i] = 0.f; }
+  if (s.norm != ECHO_NORM_NONE && in_row) {
+    if (s.weight) load_f8(s.weight + j * VEC, wt);
+    if (s.bias) load_f8(s.bias + j * VEC, bi);
+  }
+
+  Raw8<T> raw[HU];
+  int32_t pos[HU];
+  uint32_t tok[HU], head[HU];
+#pragma unroll
+  for (int u = 0; u < HU; ++u) {
+    const uint32_t row = first + u * ROWS + sub;
+    const bool in = row < n_rows;
+    tok[u] = in ? row / heads : 0u;
+    head[u] = in ? row - tok[u] * heads : 0u;
+    pos[u] = in ? a.pos[tok[u]] : -1;                // -1: nothing is written
+    raw[u] = in && in_row ? load8(static_cast<const T *>(s.x) + tok[u] * s.xt + head[u] * s.xh + j * VEC)
+                          : zero8<T>();
+  }
+#pragma unroll
+  for (int u = 0; u < HU; ++u) {
+    const bool live = pos[u] >= 0 && pos[u] < a.n_pos;
+    float c[VEC], d[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) { c[i] = 1.f; d[i] = 0.f; }
+    if (turns && live) {
+      const float *cs = a.cos_sin + static_cast<int64_t>(pos[u]) * a.rot + angle;
+      if (NEXT) {
+        const f32x4 cv = *reinterpret_cast<const f32x4 *>(cs), sv = *reinterpret_cast<const f32x4 *>(cs + half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { c[i] = cv[i]; d[i] = sv[i]; }
+      } else {
+        load_f8(cs, c);
+        load_f8(cs + half, d);
+      }
+    }
+    float x[VEC];
+    unpack8(raw[u], x);
+    if (s.norm != ECHO_NORM_NONE) {                  // uniform over the workgroup
+      float mean = 0.f;
+      if (s.norm == ECHO_NORM_LAYER) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) t += x[i];
+        mean = group_sum<G>(t) / static_cast<float>(a.dim);
+      }
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        x[i] = in_row ? x[i] - mean : 0.f;
+        t = fmaf(x[i], x[i], t);
+      }
+      const float r = 1.f / sqrtf(group_sum<G>(t) / static_cast<float>(a.dim) + a.eps);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[i] = fmaf(x[i] * r, wt[i], bi[i]);
+    }
+    if (NEXT) {
+      if (turns) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          const float p = x[i], q = x[i + 1];
+          x[i] = p * c[i / 2] - q * d[i / 2];
+          x[i + 1] = q * c[i / 2] + p * d[i / 2];
+        }
+      }
+    } else if (a.rot) {                              // uniform: the lanes exchange
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float p = __shfl(x[i], mate, 64);
+        if (turns) x[i] = x[i] * c[i] + (second ? p : -p) * d[i];
+      }
+    }
+    const float amax = FP8 ? group_amax<G>(x) : 0.f;
+    if (!live) continue;
+    if (!FP8) {
+      if (in_row) store8(static_cast<T *>(s.y) + tok[u] * s.yt + head[u] * s.yh + j * VEC, x);
+      continue;
+    }
+    const Fp8Scale sc = fp8_scale(amax);
+    const u32x2 code = quantise8(x, sc.inv);
+    if (!is_k) {
+      const int64_t row = static_cast<int64_t>(tok[u]) * heads + head[u];
+      *reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC) = code;
+      if (j == 0) a.f.w_out[row] = a.f.w[tok[u] * a.f.wt + head[u]] * sc.scale * a.f.w_mul;
+    } else {
+      const int64_t slot = a.f.slot[tok[u]];
+      if (slot < 0 || slot >= a.f.n_slots) continue;
+      *reinterpret_cast<u32x2 *>(a.f.k_cache + slot * D + j * VEC) = code;
+      if (j == 0) a.f.k_scale[slot] = sc.scale;
+    }
+  }
+}
+
+template <typename T, int G, bool FP8>
+static void launch_heads_g(const HeadArgs &a, bool next, uint32_t grid, hipStream_t st) {
+  if (next)
+    heads_kernel<T, G, FP8, true><<<grid, HT, 0, st>>>(a);
+  else
+    heads_kernel<T, G, FP8, false><<<grid, HT, 0, st>>>(a);
+}
+
+static uint32_t row_groups(int64_t rows, int g) {
+  const int64_t per = static_cast<int64_t>(HT / 64) * HU * (64 / g);
+  return static_cast<uint32_t>((rows + per - 1) / per);
+}
+
+template <typename T, bool FP8>
+static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
+  int g = 2;
+  while (g * VEC < a.dim) g *= 2;
+  a.q_groups = row_groups(static_cast<int64_t>(a.n_tok) * a.side[0].heads, g);
+  const uint32_t grid = a.q_groups + row_groups(static_cast<int64_t>(a.n_tok) * a.side[1].heads, g);
+  if (FP8) {
+    launch_heads_g<T, 16, FP8>(a, next, grid, st);
+  } else {
+    switch (g) {
+      case 2: launch_heads_g<T, 2, false>(a, next, grid, st); break;
+      case 4: launch_heads_g<T, 4, false>(a, next, grid, st); break;
+      case 8: launch_heads_g<T, 8, false>(a, next, grid, st); break;
+      case 16: launch_heads_g<T, 16, false>(a, next, grid, st); break;
+      default: launch_heads_g<T, 32, false>(a, next, grid, st); break;
+    }
+  }
+  return check_launch("qk heads");
+}
+
+template <bool FP8>
+static int launch_typed(const echo_qk_args *q, HeadArgs &a, hipStream_t st) {
+  const bool next = q->interleaved != 0;
+  switch (q->type) {
+    case ECHO_BF16: return launch_heads<bf16_t, FP8>(a, next, st);
+    case ECHO_FP16: return launch_heads<fp16_t, FP8>(a, next, st);
+    default: return launch_heads<float, FP8>(a, next, st);
+  }
+}
+
+static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+// The checks both entry points share; *empty is set for a call with nothing to do.
+static int check_heads(const char *fn, const echo_qk_args *q, bool *empty) {
+  *empty = false;
+  if (!q) return fail(ECHO_EINVAL, "%s: NULL args", fn);
+  if (q->n_tok < 0 || q->n_q_heads < 0 || q->n_k_heads < 0 || q->n_pos < 0 || q->rot_begin < 0 || q->rot_dim < 0)
+    return fail(ECHO_EINVAL, "%s: negative size", fn);
+  if (q->type != ECHO_BF16 && q->type != ECHO_FP16 && q->type != ECHO_FP32)
+    return fail(ECHO_EINVAL, "%s: type %d", fn, q->type);
+  for (int32_t n : {q->q_norm, q->k_norm})
+    if (n != ECHO_NORM_NONE && n != ECHO_NORM_RMS && n != ECHO_NORM_LAYER)
+      return fail(ECHO_EINVAL, "%s: norm %d", fn, n);
+  if (q->head_dim < 8 || q->head_dim > 256 || q->head_dim % 8)
+    return fail(ECHO_EUNSUPPORTED, "%s: head_dim %d is not a multiple of 8 in [8, 256]", fn, q->head_dim);
+  if (q->rot_dim % 16 || q->rot_begin % 8)
+    return fail(ECHO_EUNSUPPORTED, "%s: rot_dim %d / rot_begin %d are not multiples of 16 / 8", fn, q->rot_dim, q->rot_begin);
+  if (q->rot_dim > q->head_dim || q->rot_begin > q->head_dim - q->rot_dim)
+    return fail(ECHO_EINVAL, "%s: the rotated part ends behind the head", fn);
+  if (!(q->eps >= 0.f)) return fail(ECHO_EINVAL, "%s: eps below 0", fn);
+  if (q->n_tok == 0 || (q->n_q_heads == 0 && q->n_k_heads == 0)) { *empty = true; return ECHO_OK; }
+  if (!q->pos || (q->n_q_heads && !q->q) || (q->n_k_heads && !q->k) || (q->rot_dim && !q->cos_sin))
+    return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
+  const int64_t most = 0x7FFFFFFF - 65536;
+  if (static_cast<int64_t>(q->n_tok) * q->n_q_heads > most || static_cast<int64_t>(q->n_tok) * q->n_k_heads > most)
+    return fail(ECHO_EUNSUPPORTED, "%s: more than 2^31 - 2^16 heads in all", fn);
+  const int64_t vec = q->type == ECHO_FP32 ? 4 : 8;                 // elements in 16 bytes
+  if (misaligned(q->q_weight, 16) || misaligned(q->q_bias, 16) || misaligned(q->k_weight, 16) ||
+      misaligned(q->k_bias, 16) || misaligned(q->cos_sin, 16) ||
+      (q->n_q_heads && (misaligned(q->q, 16) || q->q_tok_stride % vec || q->q_head_stride % vec)) ||
+      (q->n_k_heads && (misaligned(q->k, 16) || q->k_tok_stride % vec || q->k_head_stride % vec)))
+    return fail(ECHO_EUNSUPPORTED, "%s: a pointer or stride is not a multiple of 16 bytes", fn);
+  return ECHO_OK;
+}
+
+static HeadArgs head_args(const echo_qk_args *q) {
+  HeadArgs a = {};
+  a.side[0] = HeadSide{q->q, nullptr, q->q_tok_stride, q->q_head_stride, 0, 0, q->q_weight, q->q_bias, q->n_q_heads, q->q_norm};
+  a.side[1] = HeadSide{q->k, nullptr, q->k_tok_stride, q->k_head_stride, 0, 0, q->k_weight, q->k_bias, q->n_k_heads, q->k_norm};
+  a.pos = q->pos;
+  a.cos_sin = q->cos_sin;
+  a.n_tok = q->n_tok;
+  a.dim = q->head_dim;
+  a.rot_begin = q->rot_begin;
+  a.rot = q->rot_dim;
+  a.n_pos = q->n_pos;
+  a.eps = q->eps;
+  return a;
+}
+
+}  // namespace echo
+
+using namespace echo;
+
+extern "C" int echo_qk_norm_rope(const echo_qk_args *q, void *q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
+                                 void *k_out, int64_t ko_tok_stride, int64_t ko_head_stride, void *stream) {
+  bool empty;
+  const int rc = check_heads("echo_qk_norm_rope", q, &empty);
+  if (rc != ECHO_OK || empty) return rc;
+  if ((q->n_q_heads && !q_out) || (q->n_k_heads && !k_out)) return fail(ECHO_EINVAL, "echo_qk_norm_rope: NULL output");
+  const int64_t vec = q->type == ECHO_FP32 ? 4 : 8;
+  if ((q->n_q_heads && (misaligned(q_out, 16) || qo_tok_stride % vec || qo_head_stride % vec)) ||
+      (q->n_k_heads && (misaligned(k_out, 16) || ko_tok_stride % vec || ko_head_stride % vec)))
+    return fail(ECHO_EUNSUPPORTED, "echo_qk_norm_rope: an output or its stride is not a multiple of 16 bytes");
+  HeadArgs a = head_args(q);
+  a.side[0].y = q_out; a.side[0].yt = qo_tok_stride; a.side[0].yh = qo_head_stride;
+  a.side[1].y = k_out; a.side[1].yt = ko_tok_stride; a.side[1].yh = ko_head_stride;
+  return launch_typed<false>(q, a, S(stream));
+}
+
+extern "C" int echo_indexer_qk(const echo_qk_args *q, const float *w, int64_t w_tok_stride, float w_mul, uint8_t *q8,
+                               float *w_out, uint8_t *k_cache, float *k_scale, const int64_t *slot, int64_t n_slots,
+                               void *stream) {
+  bool empty;
+  const int rc = check_heads("echo_indexer_qk", q, &empty);
+  if (rc != ECHO_OK) return rc;
+  if (q->head_dim != D) return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: head_dim %d is not %d", q->head_dim, D);
+  if (q->n_k_heads > 1) return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: %d key heads; a token has one key", q->n_k_heads);
+  if (n_slots < 0) return fail(ECHO_EINVAL, "echo_indexer_qk: negative size");
+  if (empty) return ECHO_OK;
+  if ((q->n_q_heads && (!w || !q8 || !w_out)) || (q->n_k_heads && (!k_cache || !k_scale || !slot)))
+    return fail(ECHO_EINVAL, "echo_indexer_qk: NULL pointer");
+  if (misaligned(q8, 8) || misaligned(k_cache, 8))
+    return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: q8 or k_cache is not 8-byte aligned");
+  HeadArgs a = head_args(q);
+  a.f = Fp8Side{w, w_tok_stride, w_mul, q8, w_out, k_cache, k_scale, slot, n_slots};
+  return launch_typed<true>(q, a, S(stream));
+}

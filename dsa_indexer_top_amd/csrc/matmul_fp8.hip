@@ -1,0 +1,327 @@
+// Block-scaled FP8 product on gfx950 (echo_matmul_fp8):
+//   c[i][j] = sum_t sa(i, t) * sb(j / 128, t) * sum_{p in block t} a[i][p] * b[j][p]
+//
+// v_mfma_f32_16x16x128_f8f6f4 multiplies 16 x 16 x 128, exactly one scale block, so its result is
+// one term of the sum over t.  The weights are its first operand (result rows), the activations
+// its second (result columns): lane l then holds c[i = l%16][j = 4 (l/16) .. + 3], four
+// consecutive outputs of one row, and one activation scale for all of them, while the weight
+// scale is the same for the whole tile.  Folding a term in is one FMA per element with
+// s = sa * sb; those FMAs run on the VALU while the matrix core multiplies the next tile.
+#include "float_types.cuh"
+#include "score_tile.cuh"
+
+namespace echo {
+
+struct MatArgs {
+  const uint8_t *a, *b;
+  const float *sa, *sb;
+  int64_t lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc;
+  int32_t m, n, k;
+  void *c;
+  bool wide;                      // rows of c allow four elements per store
+};
+
+ECHO_DEV v8i operand(const u32x4 &x, const u32x4 &y) {
+  return v8i{static_cast<int>(x[0]), static_cast<int>(x[1]), static_cast<int>(x[2]), static_cast<int>(x[3]),
+             static_cast<int>(y[0]), static_cast<int>(y[1]), static_cast<int>(y[2]), static_cast<int>(y[3])};
+}
+
+// Bytes [32 g, 32 g + 32) of a row's 128-byte block that holds `left` bytes, zeros behind them.
+// Pieces that start behind the end are read from the block's first piece, which every row has.
+ECHO_DEV v8i load_operand(const uint8_t *__restrict__ blk, int g, int left) {
+  const int o0 = 32 * g, o1 = o0 + 16;
+  u32x4 p[2] = {*reinterpret_cast<const u32x4 *>(blk + (o0 < left ? o0 : 0)),
+                *reinterpret_cast<const u32x4 *>(blk + (o1 < left ? o1 : 0))};
+  if (left < 128) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int keep = left - (o0 + 16 * h + 4 * i);       // valid bytes of this word
+        const uint32_t mask = keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
+        p[h][i] &= mask;
+      }
+  }
+  return operand(p[0], p[1]);
+}
+
+// One 16 x 16 x 128 term on the FP8 matrix core, or exactly (EXACT) on the bf16 one.
+//
+// The FP8 core adds products in groups of eight neighbours: within a group it cuts every product
+// at 2^-13 of the largest one's power of two (measured: a product survives next to one 2^13 times
+// larger and is gone at 2^14, the groups are then summed in fp32).  For normally distributed
+// operands a sum is off by 1.6e-5 of its size, far below the half step of a bf16 (2^-9) or fp16
+// (2^-12) result, so those use it.  Results in fp32 convert the codes to bf16, which holds every
+// E4M3FN number and multiplies exactly into fp32, and take four bf16 MFMAs at half the rate.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <bool EXACT> struct Operand;
+template <> struct Operand<false> {
+  v8i v;
+  ECHO_DEV void set(const v8i &x) { v = x; }
+};
+template <> struct Operand<true> {
+  bf16x8 v[4];
+  ECHO_DEV void set(const v8i &x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned word = static_cast<unsigned>(x[2 * i + h]);
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, 1.f, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, 1.f, true);
+        v[i][4 * h] = lo[0]; v[i][4 * h + 1] = lo[1]; v[i][4 * h + 2] = hi[0]; v[i][4 * h + 3] = hi[1];
+      }
+  }
+};
+ECHO_DEV v4f mfma128(const Operand<false> &x, const Operand<false> &y) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+ECHO_DEV v4f mfma128(const Operand<true> &x, const Operand<true> &y) {
+  v4f c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.v[i], y.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// Stores the lane's four consecutive outputs of row i, columns j .. j + 3.
+template <typename T>
+ECHO_DEV void store_c(const MatArgs &a, int64_t i, int32_t j, const v4f &v) {
+  if (i >= a.m || j >= a.n) return;
+  T *p = static_cast<T *>(a.c) + i * a.ldc + j;
+  T e[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) e[u] = from_f32<T>(v[u]);
+  if (a.wide && j + 4 <= a.n) {
+    if (sizeof(T) == 4) {
+      u32x4 w;
+      __builtin_memcpy(&w, e, sizeof(T) * 4);
+      *reinterpret_cast<u32x4 *>(p) = w;
+    } else {
+      u32x2 w;
+      __builtin_memcpy(&w, e, 8);
+      *reinterpret_cast<u32x2 *>(p) = w;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j + u < a.n) p[u] = e[u];
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// One workgroup per 16 * NT weight rows and 16 * MT activation rows; its 8 waves take the scale
+// blocks in turn and their sums are joined in LDS in wave order.  Reading the weights is what
+// costs here, so every output type gets the exact products.
+constexpr int SW = 8;
+template <typename T, int MT, int NT>
+__global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
+  __shared__ float part[SW][MT * NT][64 * 4];
+  const int wv = threadIdx.x >> 6, l = lane_id(), j = l & 15, g = l >> 4;
+  const int32_t n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
+  const int nb = (a.k + 127) >> 7;
+  const uint8_t *bp[NT], *ap[MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) bp[i] = a.b + static_cast<int64_t>(min(n0 + 16 * i + j, a.n - 1)) * a.ldb;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) ap[i] = a.a + static_cast<int64_t>(min(m0 + 16 * i + j, a.m - 1)) * a.lda;
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y) acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int t = wv; t < nb; t += SW) {
+    const int left = min(a.k - t * 128, 128);
+    const int64_t o = static_cast<int64_t>(t) * 128;
+    Operand<true> bv[NT], av[MT];
+    float s[MT];
+    const float sb = a.sb[(n0 >> 7) * a.bs_row + t * a.bs_blk];
+#pragma unroll
+    for (int y = 0; y < NT; ++y) bv[y].set(load_operand(bp[y] + o, g, left));
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      av[x].set(load_operand(ap[x] + o, g, left));
+      s[x] = a.sa[min(m0 + 16 * x + j, a.m - 1) * a.as_row + t * a.as_blk] * sb;
+    }
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int y = 0; y < NT; ++y) {
+        const v4f c = mfma128(bv[y], av[x]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[x][y][v] = fmaf(c[v], s[x], acc[x][y][v]);
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y) *reinterpret_cast<v4f *>(&part[wv][x * NT + y][l * 4]) = acc[x][y];
+  __syncthreads();
+  for (int i = wv; i < MT * NT; i += SW) {
+    v4f sum = *reinterpret_cast<const v4f *>(&part[0][i][l * 4]);
+#pragma unroll
+    for (int w = 1; w < SW; ++w) sum += *reinterpret_cast<const v4f *>(&part[w][i][l * 4]);
+    store_c<T>(a, m0 + 16 * (i / NT) + j, n0 + 16 * (i % NT) + 4 * g, sum);
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void glb_void;
+
+// A row of a stage is 128 bytes in eight 16-byte pieces; piece s of row r sits at place
+// s ^ ((r >> 1) & 7), so the 16 rows of an operand read hit different banks.
+ECHO_DEV int place(int row, int seg) { return row * 128 + ((seg ^ ((row >> 1) & 7)) << 4); }
+
+// ROWS rows of one stage from global memory straight to LDS by NW waves: a wave's load puts 64
+// consecutive 16-byte pieces (8 rows), so the exchange of pieces is made on the global side.
+template <int ROWS, int NW>
+struct StageLoad {
+  static constexpr int N = ROWS * 8 / (NW * 64);       // loads per thread
+  const uint8_t *row[N];                               // this thread's rows
+  int seg[N];                                          // and the byte of its piece
+  ECHO_DEV void init(const uint8_t *base, int64_t ld, int32_t r0, int32_t n_rows) {
+    const int wv = threadIdx.x >> 6, l = lane_id();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = (i * NW + wv) * 8 + (l >> 3);
+      row[i] = base + static_cast<int64_t>(min(r0 + r, n_rows - 1)) * ld;
+      seg[i] = ((l & 7) ^ ((r >> 1) & 7)) << 4;
+    }
+  }
+  // k0: first byte of the block; left: its bytes (pieces behind them read the first piece)
+  ECHO_DEV void load(uint8_t *__restrict__ stage, int64_t k0, int left) const {
+    const int wv = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      __builtin_amdgcn_global_load_lds((glb_void *)(row[i] + k0 + (seg[i] < left ? seg[i] : 0)),
+                                       (lds_void *)(stage + (i * NW + wv) * 1024), 16, 0, 0);
+  }
+};
+
+ECHO_DEV v8i stage_operand(const uint8_t *__restrict__ stage, int row, int g) {
+  return operand(*reinterpret_cast<const u32x4 *>(stage + place(row, 2 * g)),
+                 *reinterpret_cast<const u32x4 *>(stage + place(row, 2 * g + 1)));
+}
+ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int keep = left - (32 * g + 4 * i);
+    v[i] &= keep >= 4 ? -1 : keep <= 0 ? 0 : static_cast<int>((1u << (8 * keep)) - 1u);
+  }
+  return v;
+}
+
+// BM activation rows x BN weight rows per workgroup, WM x WN per wave.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel(MatArgs a) {
+  constexpr int NW = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
+  constexpr bool EXACT = sizeof(T) == 4;
+  static_assert(WN <= 128, "one weight scale per wave");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int l = lane_id(), j = l & 15, g = l >> 4;
+  const int32_t m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
+  const int wm = (wv % (BM / WM)) * WM, wn = (wv / (BM / WM)) * WN;
+  const int nb = (a.k + 127) >> 7;
+  StageLoad<BM, NW> la;
+  StageLoad<BN, NW> lb;
+  la.init(a.a, a.lda, m0, a.m);
+  lb.init(a.b, a.ldb, n0, a.n);
+  const float *sa[MT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x) sa[x] = a.sa + min(m0 + wm + 16 * x + j, a.m - 1) * a.as_row;
+  const float *sb = a.sb + (min(n0 + wn, a.n - 1) >> 7) * a.bs_row;
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y) acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if (nb > 0) {
+    la.load(lds[0], 0, a.k);
+    lb.load(lds[0] + BM * 128, 0, a.k);
+  }
+  for (int t = 0; t < nb; ++t) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): this block is in LDS
+    __syncthreads();
+    const uint8_t *cur = lds[t & 1];
+    uint8_t *nxt = lds[(t & 1) ^ 1];
+    if (t + 1 < nb) {
+      const int64_t k0 = static_cast<int64_t>(t + 1) * 128;
+      la.load(nxt, k0, a.k - (t + 1) * 128);
+      lb.load(nxt + BM * 128, k0, a.k - (t + 1) * 128);
+    }
+    const int left = a.k - t * 128;
+    const float sbt = sb[t * a.bs_blk];
+    float s[MT];
+    Operand<EXACT> av[MT];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      s[x] = sa[x][t * a.as_blk] * sbt;
+      v8i v = stage_operand(cur, wm + 16 * x + j, g);
+      if (left < 128) v = keep_bytes(v, g, left);
+      av[x].set(v);
+    }
+#pragma unroll
+    for (int y = 0; y < NT; ++y) {
+      v8i v = stage_operand(cur + BM * 128, wn + 16 * y + j, g);
+      if (left < 128) v = keep_bytes(v, g, left);
+      Operand<EXACT> bv;
+      bv.set(v);
+#pragma unroll
+      for (int x = 0; x < MT; ++x) {
+        const v4f c = mfma128(bv, av[x]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[x][y][v] = fmaf(c[v], s[x], acc[x][y][v]);
+      }
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < NT; ++y)
+#pragma unroll
+    for (int x = 0; x < MT; ++x) store_c<T>(a, m0 + wm + 16 * x + j, n0 + wn + 16 * y + 4 * g, acc[x][y]);
+}
+
+template <typename T>
+static int launch_matmul(const MatArgs &a, hipStream_t st) {
+  const auto cdiv = [](int32_t x, int32_t y) { return static_cast<uint32_t>((static_cast<int64_t>(x) + y - 1) / y); };
+  if (a.m <= 16) {
+    matmul_few_kernel<T, 1, 1><<<dim3(cdiv(a.n, 16), cdiv(a.m, 16)), SW * 64, 0, st>>>(a);
+  } else if (a.m <= 64) {
+    matmul_few_kernel<T, 2, 2><<<dim3(cdiv(a.n, 32), cdiv(a.m, 32)), SW * 64, 0, st>>>(a);
+  } else {
+    matmul_tile_kernel<T, 128, 128, 64, 64><<<dim3(cdiv(a.n, 128), cdiv(a.m, 128)), 256, 0, st>>>(a);
+  }
+  return check_launch("matmul_fp8");
+}
+
+}  // namespace echo
+
+using namespace echo;
+
+extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t as_row, int64_t as_blk,
+                               const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk,
+                               int32_t m, int32_t n, int32_t k, void *c, int64_t ldc, int32_t c_type, void *stream) {
+  if (m < 0 || n < 0 || k < 0) return fail(ECHO_EINVAL, "echo_matmul_fp8: negative size");
+  if (c_type != ECHO_BF16 && c_type != ECHO_FP16 && c_type != ECHO_FP32)
+    return fail(ECHO_EINVAL, "echo_matmul_fp8: type %d", c_type);
+  if (m == 0 || n == 0) return ECHO_OK;
+  if (!c || (k && (!a || !b || !a_scale || !b_scale))) return fail(ECHO_EINVAL, "echo_matmul_fp8: NULL pointer");
+  if (lda < k || ldb < k || ldc < n) return fail(ECHO_EINVAL, "echo_matmul_fp8: row stride below the row");
+  if (k == 0) a = b = nullptr, lda = ldb = 0;             // no byte of them is read
+  if (reinterpret_cast<uintptr_t>(a) % 16 || reinterpret_cast<uintptr_t>(b) % 16 || lda % 16 || ldb % 16)
+    return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: a, b, lda or ldb is not a multiple of 16");
+  if (k > 0x7FFFFFFF - 256 || n > 0x7FFFFFFF - 256 || m > 65535 * 128)
+    return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: size beyond the grid");
+  const size_t size = c_type == ECHO_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(c) % size) return fail(ECHO_EINVAL, "echo_matmul_fp8: c is not aligned to its type");
+  const MatArgs x = {a, b, a_scale, b_scale, lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc, m, n, k, c,
+                     reinterpret_cast<uintptr_t>(c) % (4 * size) == 0 && ldc % 4 == 0};
+  switch (c_type) {
+    case ECHO_BF16: return launch_matmul<bf16_t>(x, S(stream));
+    case ECHO_FP16: return launch_matmul<fp16_t>(x, S(stream));
+    default: return launch_matmul<float>(x, S(stream));
+  }
+}

@@ -69,8 +69,22 @@ enum {
   ECHO_ST_BAD_HOST = 2,  /* a selected token maps to a host index outside [0, n_host); pool untouched */
   ECHO_ST_DUP_HOST = 4,  /* two selected misses share a host index (caller precondition broken);
                             pool state afterwards is unspecified */
-  ECHO_ST_CACHE_FULL = 8 /* echo_decode_append: a request's key range is full; its token was not
+  ECHO_ST_CACHE_FULL = 8,/* echo_decode_append: a request's key range is full; its token was not
                             appended */
+  ECHO_ST_NO_PAGES = 16, /* echo_page_step: the step needs more pages than are free, or the stack of
+                            free pages does not fit its pool; nothing was handed out */
+  ECHO_ST_BAD_LEN = 32   /* echo_page_step: a negative length, one behind the page table's width, or
+                            more new tokens than the maps hold; nothing was handed out */
+};
+
+/* Types of floating-point tensors. */
+enum { ECHO_BF16 = 0, ECHO_FP16 = 1, ECHO_FP32 = 2 };
+
+/* Norms of query and key heads (echo_qk_args). */
+enum {
+  ECHO_NORM_NONE = 0,
+  ECHO_NORM_RMS = 1,   /* x / sqrt(mean(x^2) + eps) * weight + bias */
+  ECHO_NORM_LAYER = 2  /* (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias */
 };
 
 /* Recall modes for echo_recall. */
@@ -551,6 +565,135 @@ int echo_graph_end(void *stream, echo_graph *graph);
  * echo_pool.host_kv.  Free with echo_host_free. */
 int echo_host_alloc(size_t bytes, int coherent, void **host, void **dev);
 int echo_host_free(void *host);
+
+/*
+ * What a step needs before its scores: the page maps of a paged key cache, the FP8 products that
+ * give the indexer's queries and keys, and their norms, rotation and FP8 form.  In the order of a
+ * step: echo_page_step, echo_quant_fp8 and echo_matmul_fp8 (projections), echo_indexer_qk, then
+ * echo_index_scores_paged.
+ */
+
+/*
+ * Advances the page tables of n_rows requests by one step and maps its new tokens, from lengths
+ * that are on the GPU.  Pages have page_size tokens (a power of two in [16, 65536]); free pages
+ * are a stack, free_list[0 .. *count_in), its top at the end.
+ *   1. A request r with done[r] != 0 (done may be NULL: none) gives back its ceil(len_in[r] /
+ *      page_size) pages, pushed in (request, page) order, and its length becomes 0.  It may get
+ *      new tokens in the same step: a row of the batch taken over by the next request.
+ *   2. Each request gets the pages its new_len[r] further tokens need; the i-th new page of the
+ *      step in (request, page) order is the i-th from the top of the stack and is entered into
+ *      page_table[r].  len_out[r] = length + new_len[r]; *count_out = pages left.
+ *   3. New token t of the step (requests in order) gets slot[t] = page * page_size + offset, its
+ *      row of the paged cache; row[t] = r (row may be NULL); pos[t] = its position in the request.
+ *      All three are -1 for t in [row_begin[n_rows], max_new).  row_begin[r] is request r's first
+ *      new token.
+ * len_out may be len_in and count_out may be count_in (a step in place); no other arrays may
+ * overlap.  Entries of page_table that no page of step 2 takes, and the stack above *count_out
+ * except for what step 1 pushed, are left as they were.  A step that cannot be done whole is not
+ * done at all: ECHO_ST_NO_PAGES and/or ECHO_ST_BAD_LEN are ORed into *status, lengths and count
+ * are copied through, row_begin is 0 and every map entry -1.  The pages in the tables of the
+ * requests and on the stack are the caller's: all distinct and in [0, n_pages).
+ * Sizes: page_table [n_rows, max_pages], free_list [n_pages], row_begin [n_rows + 1], slot / row /
+ * pos [max_new].  Workspace: echo_page_workspace_bytes; two steps that may run at the same time
+ * (two graphs, two streams) need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes and
+ * NULL pointers, ECHO_EUNSUPPORTED for other page sizes and for more than 65535 requests,
+ * ECHO_EWORKSPACE for a short workspace.
+ */
+typedef struct {
+  int32_t n_rows;
+  int32_t page_size;
+  int32_t max_pages;         /* width of page_table */
+  int32_t n_pages;           /* pages of the pool */
+  int32_t max_new;           /* room of slot, row and pos */
+  const int32_t *len_in;     /* [n_rows] */
+  const int32_t *new_len;    /* [n_rows] */
+  const uint8_t *done;       /* [n_rows] or NULL */
+  int32_t *page_table;
+  int32_t *free_list;
+  const int32_t *count_in;   /* [1] */
+  int32_t *len_out;          /* [n_rows] */
+  int32_t *count_out;        /* [1] */
+  int32_t *row_begin;
+  int64_t *slot;
+  int32_t *row;              /* or NULL */
+  int32_t *pos;
+  int32_t *status;           /* [1], sticky */
+} echo_page_args;
+size_t echo_page_workspace_bytes(int32_t n_rows, int32_t max_new);
+int echo_page_step(const echo_page_args *a, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * FP8 codes of a matrix, with one scale per row and block of 128 columns (the last block may be
+ * short): scale = max(largest |x| of the block / 448, 2^-126), y = x / scale rounded to the nearest
+ * E4M3FN number.  x has type x_type and row stride ldx, y row stride ldy (both in elements);
+ * scale[r * scale_row + b * scale_blk].  What the codes of a block with a NaN or an infinity
+ * stand for is NaN.  Any alignment is taken; rows of x on 16 bytes and of y on 8 are faster.  ECHO_EINVAL for
+ * negative sizes, NULL pointers, an unknown type and strides that make rows overlap;
+ * ECHO_EUNSUPPORTED beyond 2^30 columns or 2^31 - 1 blocks.  No rows or columns: ECHO_OK.
+ */
+int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols, int64_t ldx, uint8_t *y,
+                   int64_t ldy, float *scale, int64_t scale_row, int64_t scale_blk, void *stream);
+
+/*
+ * Product of two FP8 matrices with fp32 scales in blocks of 128:
+ *   c[i][j] = sum over blocks t of a_scale(i, t) * b_scale(j / 128, t) *
+ *             (sum over p in block t, p < k, of a[i][p] * b[j][p])
+ * a [m, k] are activations with a scale per row and 128 columns, a_scale(i, t) =
+ * a_scale[i * as_row + t * as_blk]; b [n, k] are weights with a scale per 128 rows and 128 columns,
+ * b_scale[(j / 128) * bs_row + t * bs_blk].  Sums are kept in fp32 and rounded once to c's type
+ * c_type (ECHO_BF16, ECHO_FP16 or ECHO_FP32); c[i * ldc + j].  a, b, lda and ldb are multiples of
+ * 16 and every row, the last too, is readable up to k rounded up to 16; what stands behind k is
+ * ignored.  c must not overlap an input.  The result does not depend on what runs beside it: no
+ * atomics, no workspace.  m = 0 or n = 0: ECHO_OK; k = 0 writes zeros.  ECHO_EINVAL for negative
+ * sizes, NULL pointers, an unknown type, lda or ldb below k, ldc below n; ECHO_EUNSUPPORTED for
+ * other alignments or more than 2^31 - 1 output tiles.
+ */
+int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t as_row, int64_t as_blk,
+                    const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk, int32_t m,
+                    int32_t n, int32_t k, void *c, int64_t ldc, int32_t c_type, void *stream);
+
+/*
+ * Norms of n_q_heads query heads and n_k_heads key heads of n_tok tokens, and the rotation of
+ * rot_dim values of each head from rot_begin on by the token's angles, in one pass.  Row pos[t] of
+ * cos_sin [n_pos, rot_dim] holds the cosines of the rot_dim / 2 angles and then their sines.  The
+ * pair of angle i is (rot_begin + i, rot_begin + rot_dim / 2 + i), or with interleaved != 0
+ * (rot_begin + 2 i, rot_begin + 2 i + 1): (u, v) becomes (u cos - v sin, v cos + u sin).  Values
+ * are computed in fp32 and rounded once.  q and k are [n_tok, heads, head_dim] of type `type`
+ * with strides in elements; weights and biases are fp32 [head_dim] or NULL (1 and 0).  A token
+ * whose pos is outside [0, n_pos) is padding: nothing of it is written.  head_dim is a multiple of 8
+ * up to 256, rot_dim (0: none, cos_sin may be NULL) a multiple of 16, rot_begin of 8; pointers and
+ * strides of q, k, cos_sin, weights and outputs are multiples of 16 bytes.  Anything else is
+ * ECHO_EUNSUPPORTED.
+ */
+typedef struct {
+  int32_t n_tok, n_q_heads, n_k_heads, head_dim;
+  int32_t type;
+  int32_t q_norm, k_norm;    /* ECHO_NORM_* */
+  int32_t rot_begin, rot_dim, interleaved, n_pos;
+  float eps;
+  const void *q, *k;
+  int64_t q_tok_stride, q_head_stride, k_tok_stride, k_head_stride;
+  const float *q_weight, *q_bias, *k_weight, *k_bias;
+  const int32_t *pos;        /* [n_tok] */
+  const float *cos_sin;
+} echo_qk_args;
+
+/* q_out and k_out have the inputs' type; each may be its input (same strides) but overlap nothing
+ * else. */
+int echo_qk_norm_rope(const echo_qk_args *a, void *q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
+                      void *k_out, int64_t ko_tok_stride, int64_t ko_head_stride, void *stream);
+
+/*
+ * The same for the indexer (head_dim = 128, at most one key head), ending in what
+ * echo_index_scores_paged reads: q8 [n_tok, n_q_heads, 128] FP8 queries, each head quantised with a
+ * scale of its own as in echo_quant_fp8 and the scale folded into the head's weight, w_out[t][h] =
+ * w[t][h] * scale(t, h) * w_mul (w has token stride w_tok_stride); and the token's key as FP8 row
+ * k_cache[slot[t]] with k_scale[slot[t]].  A token whose slot is outside [0, n_slots) writes no key
+ * (its query is written); the slots of a call are distinct.  q8 and k_cache are 8-byte aligned.
+ */
+int echo_indexer_qk(const echo_qk_args *a, const float *w, int64_t w_tok_stride, float w_mul, uint8_t *q8,
+                    float *w_out, uint8_t *k_cache, float *k_scale, const int64_t *slot, int64_t n_slots,
+                    void *stream);
 
 /* Text of the last error on this thread ("" if none). */
 const char *echo_last_error(void);

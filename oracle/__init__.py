@@ -21,7 +21,9 @@ write-through, the EMA threshold), interquery (the chunked prefill's
 approximate top-k subsets under the shifted histogram, and its unions),
 prefetch (what the page fixes about the threshold prefetch: the eligible
 tokens, the bound in proportion to the context, the contract a prefetched pool
-satisfies, and one valid outcome).
+satisfies, and one valid outcome).  In front of the scores: pages (page tables
+and slot maps of a paged cache), blockfp8 (FP8 in blocks of 128 and the scaled
+product), heads (norms and rotation of query and key heads).
 
 Readings of points the page leaves open are listed in each module's docstring.
 Parity status of every function is stated in its docstring ("pinned by ...").

@@ -72,6 +72,7 @@ def _install():
     torch.Tensor.cuda = lambda self, *a, **k: self.clone()
     from dsa_indexer_top_amd import binding
     binding.LIB_PATH = os.environ["ECHO_EMU_LIB"]
+    binding.DEVICE_TYPE = "cpu"
 
 
 def pytest_configure(config):

@@ -357,6 +357,9 @@ static void op_dpp(const unsigned char *in, unsigned char *out, size_t, size_t, 
     const int row = l / 16, rl = l % 16;
     int src = -1;
     if (a.ctrl >= 0x111 && a.ctrl <= 0x11F) { const int s = a.ctrl - 0x110; if (rl >= s) src = l - s; }
+    else if (a.ctrl >= 0 && a.ctrl <= 0xFF) src = (l & ~3) + ((a.ctrl >> (2 * (l & 3))) & 3);   // quad_perm
+    else if (a.ctrl == 0x140) src = 16 * row + 15 - rl;                                          // row_mirror
+    else if (a.ctrl == 0x141) src = (l & ~7) + 7 - (l & 7);                                      // row_half_mirror
     else if (a.ctrl == 0x142) { if (row >= 1) src = 16 * row - 1; }
     else if (a.ctrl == 0x143) { if (row >= 2) src = 31; }
     else { fprintf(stderr, "EMU ERROR: DPP control 0x%x not emulated\n", a.ctrl); abort(); }
@@ -443,6 +446,37 @@ static void op_mfma(const unsigned char *in, unsigned char *out, size_t, size_t,
   }
 }
 
+// 16x16x32 bf16 MFMA: lane l supplies row l%16 of A and column l%16 of B for K elements
+// [8 (l/16), 8 (l/16) + 8); the result as above.
+static float bf16_value(const unsigned char *p) {
+  unsigned short h;
+  memcpy(&h, p, 2);
+  return __uint_as_float(static_cast<unsigned>(h) << 16);
+}
+struct MfmaBf16In { unsigned char a[16], b[16]; v4f_emu c; };
+static void op_mfma_bf16(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
+  static float A[16][32], B[32][16];
+  for (int l = 0; l < 64; ++l) {
+    MfmaBf16In x;
+    memcpy(&x, in + l * SLOT, sizeof x);
+    for (int q = 0; q < 8; ++q) {
+      A[l % 16][8 * (l / 16) + q] = bf16_value(x.a + 2 * q);
+      B[8 * (l / 16) + q][l % 16] = bf16_value(x.b + 2 * q);
+    }
+  }
+  for (int l = 0; l < 64; ++l) {
+    MfmaBf16In x;
+    memcpy(&x, in + l * SLOT, sizeof x);
+    v4f_emu r;
+    for (int v = 0; v < 4; ++v) {
+      double acc = 0;
+      for (int k = 0; k < 32; ++k) acc += static_cast<double>(A[4 * (l / 16) + v][k]) * B[k][l % 16];
+      r[v] = static_cast<float>(acc + x.c[v]);
+    }
+    memcpy(out + l * SLOT, &r, 16);
+  }
+}
+
 }  // namespace emu
 
 using namespace emu;
@@ -504,6 +538,43 @@ v4f_emu emu_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8i_emu a, v8i_emu b, v4f_emu
   MfmaIn x{a, b, c};
   v4f_emu r;
   wave_op(&x, sizeof x, &r, 16, op_mfma, nullptr);
+  return r;
+}
+
+// OCP E4M3FN from a float: nearest even on the 3-bit mantissa (subnormals in steps of 2^-9).
+static unsigned f32_to_e4m3fn(float x) {
+  const unsigned sign = __float_as_uint(x) >> 31 ? 0x80u : 0u;
+  if (std::isnan(x)) return sign | 0x7F;
+  const double a = std::fabs(static_cast<double>(x));
+  if (a >= 464.0) return sign | 0x7F;
+  int e = a > 0 ? std::ilogb(a) : -6;
+  if (e < -6) e = -6;
+  double m = std::nearbyint(std::ldexp(a, 3 - e));          // in units of 2^(e-3)
+  if (m >= 16) { m /= 2; ++e; }
+  const unsigned code = m < 8 ? static_cast<unsigned>(m) : (static_cast<unsigned>(e + 7) << 3) + static_cast<unsigned>(m) - 8;
+  return sign | code;
+}
+int emu_amdgcn_cvt_pk_fp8_f32(float a, float b, int old, bool high) {
+  const unsigned v = f32_to_e4m3fn(a) | f32_to_e4m3fn(b) << 8, o = static_cast<unsigned>(old);
+  return static_cast<int>(high ? (o & 0xFFFFu) | v << 16 : (o & 0xFFFF0000u) | v);
+}
+
+v2bf_emu emu_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned src, float scale, bool high) {
+  if (high) src >>= 16;
+  unsigned w = 0;
+  for (int i = 0; i < 2; ++i)
+    w |= (__float_as_uint(emu::e4m3fn(static_cast<unsigned char>(src >> (8 * i))) * scale) >> 16) << (16 * i);
+  v2bf_emu r;
+  memcpy(&r, &w, 4);
+  return r;
+}
+v4f_emu emu_amdgcn_mfma_f32_16x16x32_bf16(v8bf_emu a, v8bf_emu b, v4f_emu c, int, int, int) {
+  MfmaBf16In x;
+  memcpy(x.a, &a, 16);
+  memcpy(x.b, &b, 16);
+  x.c = c;
+  v4f_emu r;
+  wave_op(&x, sizeof x, &r, 16, op_mfma_bf16, nullptr);
   return r;
 }
 

@@ -127,6 +127,19 @@ v2u_emu emu_amdgcn_permlane16_swap(unsigned a, unsigned b, bool fi, bool bc);
 v2u_emu emu_amdgcn_permlane32_swap(unsigned a, unsigned b, bool fi, bool bc);
 v4f_emu emu_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8i_emu a, v8i_emu b, v4f_emu c, int, int, int, int, int, int);
 inline unsigned long long emu_amdgcn_s_memrealtime() { return 0; }
+// two floats to OCP E4M3FN (nearest even, NaN above 464), into the low or high half of `old`
+int emu_amdgcn_cvt_pk_fp8_f32(float a, float b, int old, bool high);
+// two E4M3FN codes (low or high half) times a power of two as bf16
+typedef __bf16 v2bf_emu __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf_emu __attribute__((ext_vector_type(8)));
+v2bf_emu emu_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned src, float scale, bool high);
+v4f_emu emu_amdgcn_mfma_f32_16x16x32_bf16(v8bf_emu a, v8bf_emu b, v4f_emu c, int, int, int);
+// global memory straight to LDS: the wave's base plus the lane's place (done at once here)
+inline void emu_amdgcn_global_load_lds(const void *g, void *lds, unsigned size, int, unsigned) {
+  memcpy(static_cast<char *>(lds) + emu::ctx()->lane * size, g, size);
+}
+inline void emu_amdgcn_s_waitcnt(int) {}
+inline void emu_amdgcn_s_setprio(int) {}
 
 // ---- host runtime
 typedef int hipError_t;

@@ -1,0 +1,210 @@
+"""FP8 in blocks of 128: echo_quant_fp8 and echo_matmul_fp8 against the oracle in float64.
+
+Tolerances (u = 2^-24).  Scales are one division of fp32 numbers: equal to numpy's.  A code is the
+E4M3FN number nearest to x * fl(448 / amax) rounded, within 3 roundings of x / scale (the two
+divisions and the product): it may be off the nearest number's distance by 4 u |x / scale|.  A
+product sums up to 128 terms in a block, nb blocks and 8 partial sums in fp32; should the matrix
+core cut instead of rounding, each step is off by 2 u: (128 + nb + 8 + 3) * 2 u times the sum of
+the terms' magnitudes, plus half a step of the output's type.
+
+Sums for 16-bit outputs may come from the FP8 matrix core, which is not an fp32 sum of products.
+Measured on gfx950: of eight neighbouring products with one of 2^16, another one of 2^e is in the sum
+for e >= 3 and gone for e < 3; 225 * 2^-6 * 2^e (15/8 squared) is cut to a multiple of 8 = 2^(16-13),
+towards zero, for either sign; products of other groups are kept to fp32.  So a product loses less
+than 2^-13 of the power of two of its group's largest product, which is at most that product: a
+group loses at most 7 * 2^-13 of its largest product's magnitude (the largest one's own last bits,
+2^-6 of its power of two, are kept), and an output at most that summed over the groups."""
+
+import numpy as np
+import pytest
+import torch
+
+from dsa_indexer_top_amd import binding as B
+from gpu_util import announce, dev, host
+from oracle import blockfp8 as O
+from oracle.fp8 import E4M3FN_TABLE
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF_STEP = {t: torch.finfo(d).eps / 2 for t, d in TYPES.items()}
+
+
+def f64(t):
+    torch.cuda.synchronize()
+    return t.cpu().double().numpy()
+
+
+def check_codes(codes, scale, x, what=""):
+    """Codes and scales of x (float64 of what the kernel read)."""
+    want = np.maximum(np.float32(448.0 * O.SCALE_MIN), np.stack(
+        [np.abs(x[:, b:b + 128]).max(1) for b in range(0, x.shape[1], 128)], 1).astype(np.float32)) / np.float32(448)
+    assert np.array_equal(scale, want), what
+    t = x / O.spread(scale.astype(np.float64), x.shape[1])
+    off = np.abs(E4M3FN_TABLE[codes] - t)
+    assert (off <= O.nearest_distance(t) + 4 * U * np.abs(t)).all(), (what, np.max(off - O.nearest_distance(t)))
+
+
+QUANT = [(1, 128), (1, 1), (3, 127), (5, 129), (33, 300), (2, 2047), (17, 1024), (260, 8), (1, 5000)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,cols", QUANT)
+def test_quant(rows, cols, kind):
+    announce("quant", rows, cols, kind)
+    rng = np.random.default_rng(rows * 1000 + cols)
+    x = torch.from_numpy(rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)) * 2)).to(TYPES[kind])
+    ld = -(-cols // 16) * 16
+    y = torch.full((rows, ld), 0xEE, dtype=torch.uint8, device="cuda")
+    scale = torch.full((rows, -(-cols // 128)), -1.0, device="cuda")
+    B.quant_fp8(x.cuda(), y[:, :cols], scale)
+    check_codes(host(y)[:, :cols], host(scale), x.double().numpy())
+    assert (host(y)[:, cols:] == 0xEE).all()          # what stands behind a row is left
+
+
+def test_quant_strides_and_odd_addresses():
+    rng = np.random.default_rng(2)
+    base = torch.from_numpy(rng.standard_normal((9, 701))).to(torch.bfloat16)
+    x = base.cuda()[:, 3:3 + 391]                     # rows that start on 2 bytes
+    y = torch.full((9, 400), 0xEE, dtype=torch.uint8, device="cuda")
+    scale = torch.full((4, 9), -1.0, device="cuda")   # scales with blocks as rows
+    B.quant_fp8(x, y[:, 1:392], scale.t())
+    check_codes(host(y)[:, 1:392], host(scale).T, base[:, 3:394].double().numpy())
+    assert (host(y)[:, 0] == 0xEE).all() and (host(y)[:, 392:] == 0xEE).all()
+
+
+def test_quant_values_at_the_borders():
+    """Zeros, subnormals, the largest numbers, halves between codes, infinities and NaN."""
+    rows = [np.zeros(256), np.full(256, 1e-38), np.linspace(-448, 448, 256), np.full(256, 3.0e38),
+            np.r_[448.0, np.arange(255) * 1.0625], np.full(256, 1e-45), np.r_[448.0, 2.0 ** -10 * np.arange(255)]]
+    x = np.array(rows, np.float32)
+    xt = torch.from_numpy(x)
+    y = torch.empty((len(x), 256), dtype=torch.uint8, device="cuda")
+    scale = torch.empty((len(x), 2), device="cuda")
+    B.quant_fp8(xt.cuda(), y, scale)
+    check_codes(host(y), host(scale), x.astype(np.float64))
+    assert (host(scale) > 0).all() and (host(y)[0] & 0x7F == 0).all()
+    # a block with a NaN or an infinity stands for NaN; its neighbours are as they would be
+    for bad in (np.nan, np.inf, -np.inf):
+        z = x[2:5].copy()
+        z[1, 5] = bad
+        B.quant_fp8(torch.from_numpy(z).cuda(), y[:3], scale[:3])
+        with np.errstate(invalid="ignore"):
+            v = E4M3FN_TABLE[host(y)[:3]] * O.spread(host(scale)[:3].astype(np.float64), 256)
+        assert np.isnan(v[1, :128]).all() and not np.isnan(v[1, 128:]).any() and not np.isnan(v[[0, 2]]).any()
+
+
+def product_case(rng, m, n, k, grid=False):
+    """Codes with 16-byte rows whose bytes behind k are NaN codes, and scales."""
+    ld = -(-k // 16) * 16
+    a, b = (np.full((r, ld), 0x7F, np.uint8) for r in (m, n))
+    if grid:                                          # whole numbers: every sum is exact
+        codes = np.flatnonzero(np.isin(E4M3FN_TABLE, np.arange(-4, 5)))
+        a[:, :k], b[:, :k] = (rng.choice(codes, (r, k)) for r in (m, n))
+        scales = [2.0 ** rng.integers(-3, 4, s) for s in ((m, -(-k // 128)), (-(-n // 128), -(-k // 128)))]
+    else:
+        finite = np.flatnonzero(np.isfinite(E4M3FN_TABLE))
+        a[:, :k], b[:, :k] = (rng.choice(finite, (r, k)) for r in (m, n))
+        scales = [np.exp(rng.standard_normal(s)) for s in ((m, -(-k // 128)), (-(-n // 128), -(-k // 128)))]
+    return a, b, scales[0].astype(np.float32), scales[1].astype(np.float32)
+
+
+def check_product(got, a, sa, b, sb, k, half_step, what):
+    want, T = O.matmul(a[:, :k], sa, b[:, :k], sb)
+    tol = (128 + -(-k // 128) + 11) * 2 * U * T
+    off = np.abs(got - want)
+    assert (off <= tol + half_step * (np.abs(want) + tol)).all(), (what, np.max(off / np.maximum(T, 1e-30)))
+
+
+# sizes about 16, the tiles' edges, one and several workgroups, K of part of a block
+PRODUCT = [(1, 1, 1), (1, 16, 128), (1, 300, 130), (7, 33, 129), (16, 128, 256), (17, 130, 1100), (33, 17, 300),
+           (64, 64, 128), (65, 129, 300), (100, 260, 31), (130, 128, 256), (129, 300, 400), (200, 1, 140),
+           (257, 5, 128), (270, 270, 272)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", PRODUCT)
+def test_product(m, n, k, kind):
+    announce("product", m, n, k, kind)
+    rng = np.random.default_rng(m * 7 + n * 3 + k)
+    a, b, sa, sb = product_case(rng, m, n, k)
+    if kind == "fp16":                                # keep the sums below fp16's 65504
+        sa *= np.float32(1e-4 / max(1.0, k / 128))
+    c = torch.full((m, n + 3), -77.0, dtype=TYPES[kind], device="cuda")
+    B.matmul_fp8(dev(a)[:, :k], dev(sa), dev(b)[:, :k], dev(sb), c[:, :n])
+    # fp16 below its normal numbers rounds in steps of 2^-24
+    half = HALF_STEP[kind]
+    got = f64(c)
+    want, T = O.matmul(a[:, :k], sa, b[:, :k], sb)
+    tol = (128 + -(-k // 128) + 11) * 2 * U * T
+    if kind != "fp32":
+        tol = tol + 7 * 2.0 ** -13 * O.group_maxima(a[:, :k], sa, b[:, :k], sb)
+    floor = 2.0 ** -25 if kind == "fp16" else 0.0
+    assert (np.abs(got[:, :n] - want) <= tol + half * (np.abs(want) + tol) + floor).all()
+    assert (got[:, n:] == -77.0).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 40, 300), (40, 70, 500), (140, 140, 384)])
+def test_product_exact_on_whole_numbers(m, n, k):
+    """Small whole numbers and powers of two as scales: every partial sum is exact in fp32."""
+    rng = np.random.default_rng(k)
+    a, b, sa, sb = product_case(rng, m, n, k, grid=True)
+    c = torch.empty((m, n), device="cuda")
+    B.matmul_fp8(dev(a)[:, :k], dev(sa), dev(b)[:, :k], dev(sb), c)
+    assert np.array_equal(f64(c), O.matmul(a[:, :k], sa, b[:, :k], sb)[0])
+
+
+@pytest.mark.parametrize("m", [3, 50, 150])
+def test_product_strides(m):
+    """Scales with blocks as rows, wide rows of a, b and c, columns of c that allow no wide store."""
+    rng = np.random.default_rng(m)
+    n, k = 150, 260
+    a, b, sa, sb = product_case(rng, m, n, k)
+    at, bt = torch.full((m, 320), 0x7F, dtype=torch.uint8, device="cuda"), torch.full((n, 400), 0x7F, dtype=torch.uint8, device="cuda")
+    at[:, 16:16 + k], bt[:, 32:32 + k] = dev(a)[:, :k], dev(b)[:, :k]
+    c = torch.full((m, n + 7), -77.0, device="cuda")
+    B.matmul_fp8(at[:, 16:16 + k], dev(sa.T).t(), bt[:, 32:32 + k], dev(sb.T).t(), c[:, 3:3 + n])
+    got = f64(c)
+    check_product(got[:, 3:3 + n], a, sa, b, sb, k, HALF_STEP["fp32"], m)
+    assert (got[:, :3] == -77.0).all() and (got[:, 3 + n:] == -77.0).all()
+
+
+@pytest.mark.parametrize("m", [2, 40, 140])
+def test_product_nan_stays_in_its_row_and_column(m):
+    rng = np.random.default_rng(9)
+    n, k = 70, 200
+    a, b, sa, sb = product_case(rng, m, n, k)
+    a[1, 130] = 0x7F
+    b[69, 5] = 0xFF
+    c = torch.empty((m, n), device="cuda")
+    B.matmul_fp8(dev(a)[:, :k], dev(sa), dev(b)[:, :k], dev(sb), c)
+    nan = np.isnan(f64(c))
+    assert nan[1].all() and nan[:, 69].all() and nan.sum() == n + m - 1
+
+
+@pytest.mark.parametrize("m", [3, 200])
+def test_product_of_nothing(m):
+    c = torch.full((m, 20), 5.0, device="cuda")
+    z = lambda r, w, t: torch.zeros((r, w), dtype=t, device="cuda")
+    B.matmul_fp8(z(m, 0, torch.uint8), z(m, 0, torch.float32), z(20, 0, torch.uint8), z(1, 0, torch.float32), c)
+    assert (f64(c) == 0).all()
+    B.matmul_fp8(z(0, 64, torch.uint8), z(0, 1, torch.float32), z(20, 64, torch.uint8), z(1, 1, torch.float32), c[:0])
+
+
+def test_quant_then_product_of_hidden_states():
+    """bf16 states to FP8 and through a projection: within the quantiser's half steps of the
+    product of the unquantised states (an E4M3FN code is off by at most 2^-4 of its value, or half
+    a subnormal step, 2^-10 of the scale)."""
+    rng = np.random.default_rng(4)
+    m, n, k = 21, 130, 520
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(torch.bfloat16)
+    _, b, _, sb = product_case(rng, 1, n, k)
+    y = torch.empty((m, 528), dtype=torch.uint8, device="cuda")[:, :k]
+    sa = torch.empty((5, m), device="cuda").t()
+    c = torch.empty((m, n), device="cuda")
+    B.quant_fp8(x.cuda(), y, sa)
+    B.matmul_fp8(y, sa, dev(b)[:, :k], dev(sb), c)
+    bv = E4M3FN_TABLE[b[:, :k]] * O.spread(np.repeat(sb.astype(np.float64), 128, 0)[:n], k)
+    xv, s = x.double().numpy(), O.spread(host(sa).astype(np.float64), k)
+    bound = (np.abs(xv) * 2.0 ** -4 + s * 2.0 ** -10) @ np.abs(bv).T * 1.001
+    assert (np.abs(f64(c) - xv @ bv.T) <= bound).all()
