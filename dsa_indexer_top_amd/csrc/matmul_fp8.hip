@@ -175,35 +175,44 @@ typedef __attribute__((address_space(1))) const void glb_void;
 ECHO_DEV int place(int row, int seg) { return row * 128 + ((seg ^ ((row >> 1) & 7)) << 4); }
 
 // ROWS rows of one stage from global memory straight to LDS by NW waves: a wave's load puts 64
-// consecutive 16-byte pieces (8 rows), so the exchange of pieces is made on the global side.
+// consecutive 16-byte pieces (8 rows), so the exchange of pieces is made on the global side.  A
+// thread's piece is the same byte of every row it loads (NW is even), and rows are 32-bit
+// offsets from the tile's first one.
 template <int ROWS, int NW>
 struct StageLoad {
+  static_assert(NW % 2 == 0, "the exchange repeats every 16 rows");
   static constexpr int N = ROWS * 8 / (NW * 64);       // loads per thread
-  const uint8_t *row[N];                               // this thread's rows
-  int seg[N];                                          // and the byte of its piece
-  ECHO_DEV void init(const uint8_t *base, int64_t ld, int32_t r0, int32_t n_rows) {
-    const int wv = threadIdx.x >> 6, l = lane_id();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = (i * NW + wv) * 8 + (l >> 3);
-      row[i] = base + static_cast<int64_t>(min(r0 + r, n_rows - 1)) * ld;
-      seg[i] = ((l & 7) ^ ((r >> 1) & 7)) << 4;
-    }
-  }
-  // k0: first byte of the block; left: its bytes (pieces behind them read the first piece)
-  ECHO_DEV void load(uint8_t *__restrict__ stage, int64_t k0, int left) const {
-    const int wv = threadIdx.x >> 6;
+  const uint8_t *tile;                                 // uniform
+  uint32_t off[N];
+  ECHO_DEV void init(const uint8_t *base, int64_t ld, int32_t r0, int32_t n_rows, int wv, int seg) {
+    tile = base + static_cast<int64_t>(r0) * ld;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void *)(row[i] + k0 + (seg[i] < left ? seg[i] : 0)),
-                                       (lds_void *)(stage + (i * NW + wv) * 1024), 16, 0, 0);
+      off[i] = static_cast<uint32_t>(min((i * NW + wv) * 8 + (lane_id() >> 3), n_rows - 1 - r0)) * static_cast<uint32_t>(ld) + seg;
+  }
+  // t: block; seg: this thread's byte of it, or, behind a short block's end, back: the distance to
+  // its first piece
+  ECHO_DEV void load(uint8_t *__restrict__ stage, int t, int wv, uint32_t back) const {
+    const uint8_t *p = tile + static_cast<int64_t>(t) * 128;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      __builtin_amdgcn_global_load_lds((glb_void *)(p + (off[i] - back)), (lds_void *)(stage + (i * NW + wv) * 1024),
+                                       16, 0, 0);
   }
 };
 
-ECHO_DEV v8i stage_operand(const uint8_t *__restrict__ stage, int row, int g) {
-  return operand(*reinterpret_cast<const u32x4 *>(stage + place(row, 2 * g)),
-                 *reinterpret_cast<const u32x4 *>(stage + place(row, 2 * g + 1)));
-}
+template <bool V> struct Const { static constexpr bool value = V; };
+
+// The lane's 32 bytes of row `row` of a stage: the places of its two pieces, which repeat every 16
+// rows (2048 bytes).
+struct Pieces {
+  int32_t p0, p1;
+  ECHO_DEV void init(int row, int g) { p0 = place(row, 2 * g); p1 = place(row, 2 * g + 1); }
+  ECHO_DEV v8i read(const uint8_t *__restrict__ stage, int rows16) const {
+    return operand(*reinterpret_cast<const u32x4 *>(stage + p0 + rows16 * 2048),
+                   *reinterpret_cast<const u32x4 *>(stage + p1 + rows16 * 2048));
+  }
+};
 ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -213,75 +222,155 @@ ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
   return v;
 }
 
-// BM activation rows x BN weight rows per workgroup, WM x WN per wave.
+// BM activation rows x BN weight rows per workgroup, WM x WN per wave; two stages in LDS, the next
+// block's loads issued before this block's products.
+//
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own, so consecutive tiles of one XCD
+// are neighbours: it gets one eighth of the tiles, taken in bands of BAND tile rows.
+constexpr int BAND = 8;
+ECHO_DEV void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t &tm, uint32_t &tn) {
+  const uint32_t total = mt * nt, xcd = id & 7u, i = id >> 3;
+  const uint32_t each = total >> 3, more = total & 7u;         // the first `more` XCDs take one more
+  uint32_t t = xcd * each + (xcd < more ? xcd : more) + i;
+  const uint32_t band = t / (BAND * nt), in = t - band * BAND * nt;
+  const uint32_t rows = min(static_cast<uint32_t>(BAND), mt - band * BAND);
+  tn = in / rows;
+  tm = band * BAND + in - tn * rows;
+}
+
+// Empty asm statements stay in program order and emit nothing: each product takes its operand from
+// one and hands its result to the next, so the compiler keeps AHEAD products in flight and no more.
+ECHO_DEV void pin(Operand<false> &o, v4f &c) { asm volatile("" : "+v"(o.v), "+v"(c)); }
+ECHO_DEV void pin(Operand<true> &, v4f &c) { asm volatile("" : "+v"(c)); }
+ECHO_DEV void pin(v4f &n, v4f &c) { asm volatile("" : "+v"(n), "+v"(c)); }
+ECHO_DEV void pin(Pieces &p) { asm volatile("" : "+v"(p.p0), "+v"(p.p1)); }
+
 template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel(MatArgs a) {
-  constexpr int NW = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
-  constexpr bool EXACT = sizeof(T) == 4;
+struct Tile {
+  static constexpr int NW = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
+  static constexpr int AHEAD = 2;                        // products in flight ahead of their FMAs
+  static constexpr bool EXACT = sizeof(T) == 4;
   static_assert(WN <= 128, "one weight scale per wave");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
-  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int l = lane_id(), j = l & 15, g = l >> 4;
-  const int32_t m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
-  const int wm = (wv % (BM / WM)) * WM, wn = (wv / (BM / WM)) * WN;
-  const int nb = (a.k + 127) >> 7;
+  static_assert(MT >= AHEAD, "the products ahead are of this or the next operand");
   StageLoad<BM, NW> la;
   StageLoad<BN, NW> lb;
-  la.init(a.a, a.lda, m0, a.m);
-  lb.init(a.b, a.ldb, n0, a.n);
-  const float *sa[MT];
-#pragma unroll
-  for (int x = 0; x < MT; ++x) sa[x] = a.sa + min(m0 + wm + 16 * x + j, a.m - 1) * a.as_row;
-  const float *sb = a.sb + (min(n0 + wn, a.n - 1) >> 7) * a.bs_row;
+  const float *sa[MT], *sb;
+  int64_t as_blk, bs_blk;
+  int nb, k, wv, wm, wn, j, g, seg;
+  Pieces pa, pb;
   v4f acc[MT][NT];
-#pragma unroll
-  for (int x = 0; x < MT; ++x)
-#pragma unroll
-    for (int y = 0; y < NT; ++y) acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
+  float ns[MT], nsb;                                     // the next block's scales
 
-  if (nb > 0) {
-    la.load(lds[0], 0, a.k);
-    lb.load(lds[0] + BM * 128, 0, a.k);
+  ECHO_DEV void load(int t, uint8_t *__restrict__ stage) const {
+    const uint32_t back = seg < k - t * 128 ? 0u : static_cast<uint32_t>(seg);
+    la.load(stage, t, wv, back);
+    lb.load(stage + BM * 128, t, wv, back);
   }
-  for (int t = 0; t < nb; ++t) {
+  ECHO_DEV void load_scales(int t) {
+#pragma unroll
+    for (int x = 0; x < MT; ++x) ns[x] = sa[x][t * as_blk];
+    nsb = sb[t * bs_blk];
+  }
+  template <bool TAIL>
+  ECHO_DEV void operand_of(Operand<EXACT> &o, const uint8_t *__restrict__ stage, const Pieces &p, int rows16, int left) const {
+    v8i v = p.read(stage, rows16);
+    if (TAIL) v = keep_bytes(v, g, left);
+    o.set(v);
+  }
+  // Block t from `cur`; block t + 1's loads go to `nxt`.
+  template <bool TAIL>
+  ECHO_DEV void block(int t, uint8_t *__restrict__ cur, uint8_t *__restrict__ nxt) {
+    float s[MT];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) s[x] = ns[x] * nsb;
+    if (t + 1 < nb) {
+      load(t + 1, nxt);
+      load_scales(t + 1);
+    }
+    const int left = k - t * 128;
+    Operand<EXACT> av[MT], bv[2];
+    operand_of<TAIL>(bv[0], cur + BM * 128, pb, 0, left);
+#pragma unroll
+    for (int x = 0; x < MT; ++x) operand_of<TAIL>(av[x], cur, pa, x, left);
+    v4f c[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) c[u] = mfma128(bv[0], av[u]);
+#pragma unroll
+    for (int u = 0; u < MT * NT; ++u) {
+      const int x = u % MT, y = u / MT, nx = (u + AHEAD) % MT, ny = (u + AHEAD) / MT;
+      if (x == 0 && y + 1 < NT) {
+        pin(pb);
+        operand_of<TAIL>(bv[(y + 1) & 1], cur + BM * 128, pb, y + 1, left);
+      }
+      v4f co = c[u % AHEAD];
+      if (ny < NT) {
+        pin(bv[ny & 1], co);
+        v4f cn = mfma128(bv[ny & 1], av[nx]);
+        pin(cn, co);
+        c[u % AHEAD] = cn;
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[x][y][v] = fmaf(co[v], s[x], acc[x][y][v]);
+    }
+  }
+};
+
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel(MatArgs a) {
+  typedef Tile<T, BM, BN, WM, WN> K;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
+  K w;
+  w.wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int l = lane_id();
+  w.j = l & 15;
+  w.g = l >> 4;
+  w.seg = ((l & 7) ^ ((w.wv * 4 + (l >> 4)) & 7)) << 4;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, (a.m + BM - 1) / BM, (a.n + BN - 1) / BN, tm, tn);
+  const int32_t m0 = tm * BM, n0 = tn * BN;
+  w.wm = (w.wv % (BM / WM)) * WM;
+  w.wn = (w.wv / (BM / WM)) * WN;
+  w.pa.init(w.wm + w.j, w.g);
+  w.pb.init(w.wn + w.j, w.g);
+  w.k = a.k;
+  w.nb = (a.k + 127) >> 7;
+  w.la.init(a.a, a.lda, m0, a.m, w.wv, w.seg);
+  w.lb.init(a.b, a.ldb, n0, a.n, w.wv, w.seg);
+  w.as_blk = a.as_blk;
+  w.bs_blk = a.bs_blk;
+#pragma unroll
+  for (int x = 0; x < K::MT; ++x) w.sa[x] = a.sa + min(m0 + w.wm + 16 * x + w.j, a.m - 1) * a.as_row;
+  w.sb = a.sb + (min(n0 + w.wn, a.n - 1) >> 7) * a.bs_row;
+#pragma unroll
+  for (int x = 0; x < K::MT; ++x)
+#pragma unroll
+    for (int y = 0; y < K::NT; ++y) w.acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (w.nb > 0) {
+    w.load(0, lds[0]);
+    w.load_scales(0);
+  }
+  const int whole = a.k >> 7;
+  for (int t = 0; t < whole; ++t) {
     __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): this block is in LDS
     __syncthreads();
-    const uint8_t *cur = lds[t & 1];
-    uint8_t *nxt = lds[(t & 1) ^ 1];
-    if (t + 1 < nb) {
-      const int64_t k0 = static_cast<int64_t>(t + 1) * 128;
-      la.load(nxt, k0, a.k - (t + 1) * 128);
-      lb.load(nxt + BM * 128, k0, a.k - (t + 1) * 128);
-    }
-    const int left = a.k - t * 128;
-    const float sbt = sb[t * a.bs_blk];
-    float s[MT];
-    Operand<EXACT> av[MT];
-#pragma unroll
-    for (int x = 0; x < MT; ++x) {
-      s[x] = sa[x][t * a.as_blk] * sbt;
-      v8i v = stage_operand(cur, wm + 16 * x + j, g);
-      if (left < 128) v = keep_bytes(v, g, left);
-      av[x].set(v);
-    }
-#pragma unroll
-    for (int y = 0; y < NT; ++y) {
-      v8i v = stage_operand(cur + BM * 128, wn + 16 * y + j, g);
-      if (left < 128) v = keep_bytes(v, g, left);
-      Operand<EXACT> bv;
-      bv.set(v);
-#pragma unroll
-      for (int x = 0; x < MT; ++x) {
-        const v4f c = mfma128(bv, av[x]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[x][y][v] = fmaf(c[v], s[x], acc[x][y][v]);
-      }
-    }
+    w.template block<false>(t, lds[t & 1], lds[(t & 1) ^ 1]);
+  }
+  if (whole < w.nb) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    __syncthreads();
+    w.template block<true>(whole, lds[whole & 1], lds[(whole & 1) ^ 1]);
   }
 #pragma unroll
-  for (int y = 0; y < NT; ++y)
+  for (int y = 0; y < K::NT; ++y)
 #pragma unroll
-    for (int x = 0; x < MT; ++x) store_c<T>(a, m0 + wm + 16 * x + j, n0 + wn + 16 * y + 4 * g, acc[x][y]);
+    for (int x = 0; x < K::MT; ++x)
+      store_c<T>(a, m0 + w.wm + 16 * x + w.j, n0 + w.wn + 16 * y + 4 * w.g, w.acc[x][y]);
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+static void launch_tiles(const MatArgs &a, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>((static_cast<int64_t>(a.m) + BM - 1) / BM * ((static_cast<int64_t>(a.n) + BN - 1) / BN));
+  matmul_tile_kernel<T, BM, BN, WM, WN><<<tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
 }
 
 template <typename T>
@@ -292,7 +381,14 @@ static int launch_matmul(const MatArgs &a, hipStream_t st) {
   } else if (a.m <= 64) {
     matmul_few_kernel<T, 2, 2><<<dim3(cdiv(a.n, 32), cdiv(a.m, 32)), SW * 64, 0, st>>>(a);
   } else {
-    matmul_tile_kernel<T, 128, 128, 64, 64><<<dim3(cdiv(a.n, 128), cdiv(a.m, 128)), 256, 0, st>>>(a);
+    const int64_t big = static_cast<int64_t>(cdiv(a.m, 256)) * cdiv(a.n, 256);
+    if constexpr (sizeof(T) == 2) {
+      if (big >= 256) {
+        launch_tiles<T, 256, 256, 64, 128>(a, st);
+        return check_launch("matmul_fp8");
+      }
+    }
+    launch_tiles<T, 128, 128, 64, 64>(a, st);
   }
   return check_launch("matmul_fp8");
 }
@@ -313,7 +409,9 @@ extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_sca
   if (k == 0) a = b = nullptr, lda = ldb = 0;             // no byte of them is read
   if (reinterpret_cast<uintptr_t>(a) % 16 || reinterpret_cast<uintptr_t>(b) % 16 || lda % 16 || ldb % 16)
     return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: a, b, lda or ldb is not a multiple of 16");
-  if (k > 0x7FFFFFFF - 256 || n > 0x7FFFFFFF - 256 || m > 65535 * 128)
+  const int64_t tiles = ((static_cast<int64_t>(m) + 127) / 128) * ((static_cast<int64_t>(n) + 127) / 128);
+  if (lda > (1 << 22) || ldb > (1 << 22)) return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: rows of more than 2^22 bytes");
+  if (k > 0x7FFFFFFF - 256 || n > 0x7FFFFFFF - 256 || m > 0x7FFFFFFF - 256 || tiles > 0x7FFFFFFF / 8)
     return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: size beyond the grid");
   const size_t size = c_type == ECHO_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(c) % size) return fail(ECHO_EINVAL, "echo_matmul_fp8: c is not aligned to its type");
