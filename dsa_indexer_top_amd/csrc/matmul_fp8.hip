@@ -18,7 +18,7 @@ struct MatArgs {
   int64_t lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc;
   int32_t m, n, k;
   void *c;
-  bool wide;                      // rows of c allow four elements per store
+  bool wide;                      // rows of c allow 16 bytes per store
 };
 
 ECHO_DEV v8i operand(const u32x4 &x, const u32x4 &y) {
@@ -85,28 +85,27 @@ ECHO_DEV v4f mfma128(const Operand<true> &x, const Operand<true> &y) {
   return c;
 }
 
+template <typename T>
+ECHO_DEV u32x2 pack4(const v4f &v) {
+  T e[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) e[u] = from_f32<T>(v[u]);
+  u32x2 w;
+  __builtin_memcpy(&w, e, 8);
+  return w;
+}
 // Stores the lane's four consecutive outputs of row i, columns j .. j + 3.
 template <typename T>
 ECHO_DEV void store_c(const MatArgs &a, int64_t i, int32_t j, const v4f &v) {
   if (i >= a.m || j >= a.n) return;
   T *p = static_cast<T *>(a.c) + i * a.ldc + j;
-  T e[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) e[u] = from_f32<T>(v[u]);
   if (a.wide && j + 4 <= a.n) {
-    if (sizeof(T) == 4) {
-      u32x4 w;
-      __builtin_memcpy(&w, e, sizeof(T) * 4);
-      *reinterpret_cast<u32x4 *>(p) = w;
-    } else {
-      u32x2 w;
-      __builtin_memcpy(&w, e, 8);
-      *reinterpret_cast<u32x2 *>(p) = w;
-    }
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<v4f *>(p) = v;
+    else *reinterpret_cast<u32x2 *>(p) = pack4<T>(v);
   } else {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (j + u < a.n) p[u] = e[u];
+      if (j + u < a.n) p[u] = from_f32<T>(v[u]);
   }
 }
 
@@ -190,24 +189,22 @@ struct StageLoad {
     for (int i = 0; i < N; ++i)
       off[i] = static_cast<uint32_t>(min((i * NW + wv) * 8 + (lane_id() >> 3), n_rows - 1 - r0)) * static_cast<uint32_t>(ld) + seg;
   }
-  // t: block; seg: this thread's byte of it, or, behind a short block's end, back: the distance to
-  // its first piece
-  ECHO_DEV void load(uint8_t *__restrict__ stage, int t, int wv, uint32_t back) const {
-    const uint8_t *p = tile + static_cast<int64_t>(t) * 128;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void *)(p + (off[i] - back)), (lds_void *)(stage + (i * NW + wv) * 1024),
-                                       16, 0, 0);
+  // Load i of block t; back: 0, or, behind a short block's end, the distance to the row's first
+  // piece.
+  ECHO_DEV void load(uint8_t *__restrict__ stage, int t, int i, int wv, uint32_t back) const {
+    __builtin_amdgcn_global_load_lds((glb_void *)(tile + static_cast<int64_t>(t) * 128 + (off[i] - back)),
+                                     (lds_void *)(stage + (i * NW + wv) * 1024), 16, 0, 0);
   }
 };
 
-template <bool V> struct Const { static constexpr bool value = V; };
-
-// The lane's 32 bytes of row `row` of a stage: the places of its two pieces, which repeat every 16
-// rows (2048 bytes).
+// The lane's 32 bytes of row `row` of a stage, pieces g and g + 4; their places repeat every 16 rows
+// (2048 bytes).  Which bytes of a row a lane group multiplies does not matter as long as both
+// operands agree; with these two no read has a bank conflict, while pieces 2g and 2g + 1 had one
+// in every read (the sixteen lanes served together come from rows of two neighbouring lane groups:
+// SQ_LDS_BANK_CONFLICT half of the LDS cycles, 8192^3 2078 against 2105 TFLOP/s).
 struct Pieces {
   int32_t p0, p1;
-  ECHO_DEV void init(int row, int g) { p0 = place(row, 2 * g); p1 = place(row, 2 * g + 1); }
+  ECHO_DEV void init(int row, int g) { p0 = place(row, g); p1 = place(row, g + 4); }
   ECHO_DEV v8i read(const uint8_t *__restrict__ stage, int rows16) const {
     return operand(*reinterpret_cast<const u32x4 *>(stage + p0 + rows16 * 2048),
                    *reinterpret_cast<const u32x4 *>(stage + p1 + rows16 * 2048));
@@ -216,14 +213,23 @@ struct Pieces {
 ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int keep = left - (32 * g + 4 * i);
+    const int keep = left - ((i < 4 ? 16 * g : 16 * g + 48) + 4 * i);
     v[i] &= keep >= 4 ? -1 : keep <= 0 ? 0 : static_cast<int>((1u << (8 * keep)) - 1u);
   }
   return v;
 }
 
-// BM activation rows x BN weight rows per workgroup, WM x WN per wave; two stages in LDS, the next
-// block's loads issued before this block's products.
+// BM activation rows x BN weight rows per workgroup, WM x WN per wave; two stages in LDS.  While a
+// block is multiplied the next one's loads are issued one by one between the products: issued
+// together at the start of the block they held up its first operand reads (8192^3 on MI355X: 2105
+// against 2188 TFLOP/s).
+//
+// What bounds the 256 x 256 tile: an MFMA takes 32 cycles of its SIMD's matrix core and its result
+// four FMAs of 4 cycles, so the products can hide everything else; counters give 58% of cycles
+// multiplying at 8192^3 at the 1.81 GHz the chip then ran (1.98 GHz at 50% before the loads were
+// spread): the clock falls as the cores fill.  Without any loads the same code reaches 2650
+// TFLOP/s, without the FMAs 2200.  A wave's accumulators are 128 registers, the most that two
+// waves per SIMD allow beside the operands: 64 x 128 outputs per wave.
 //
 // Workgroups go to the 8 XCDs in turn, each with an L2 of its own, so consecutive tiles of one XCD
 // are neighbours: it gets one eighth of the tiles, taken in bands of BAND tile rows.
@@ -249,6 +255,7 @@ template <typename T, int BM, int BN, int WM, int WN>
 struct Tile {
   static constexpr int NW = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
   static constexpr int AHEAD = 2;                        // products in flight ahead of their FMAs
+  static constexpr int EVERY = 2;                        // products between two loads
   static constexpr bool EXACT = sizeof(T) == 4;
   static_assert(WN <= 128, "one weight scale per wave");
   static_assert(MT >= AHEAD, "the products ahead are of this or the next operand");
@@ -261,10 +268,15 @@ struct Tile {
   v4f acc[MT][NT];
   float ns[MT], nsb;                                     // the next block's scales
 
-  ECHO_DEV void load(int t, uint8_t *__restrict__ stage) const {
+  static constexpr int LOADS = StageLoad<BM, NW>::N + StageLoad<BN, NW>::N;
+  ECHO_DEV void load_one(int t, int i, uint8_t *__restrict__ stage) const {
     const uint32_t back = seg < k - t * 128 ? 0u : static_cast<uint32_t>(seg);
-    la.load(stage, t, wv, back);
-    lb.load(stage + BM * 128, t, wv, back);
+    if (i < StageLoad<BM, NW>::N) la.load(stage, t, i, wv, back);
+    else lb.load(stage + BM * 128, t, i - StageLoad<BM, NW>::N, wv, back);
+  }
+  ECHO_DEV void load(int t, uint8_t *__restrict__ stage) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load_one(t, i, stage);
   }
   ECHO_DEV void load_scales(int t) {
 #pragma unroll
@@ -277,16 +289,14 @@ struct Tile {
     if (TAIL) v = keep_bytes(v, g, left);
     o.set(v);
   }
-  // Block t from `cur`; block t + 1's loads go to `nxt`.
-  template <bool TAIL>
+  // Block t from `cur`; with NEXT block t + 1's loads go to `nxt`.  Product i is issued before the
+  // FMAs of product i - AHEAD; a weight operand is read once the one before the last has been used.
+  template <bool TAIL, bool NEXT>
   ECHO_DEV void block(int t, uint8_t *__restrict__ cur, uint8_t *__restrict__ nxt) {
     float s[MT];
 #pragma unroll
     for (int x = 0; x < MT; ++x) s[x] = ns[x] * nsb;
-    if (t + 1 < nb) {
-      load(t + 1, nxt);
-      load_scales(t + 1);
-    }
+    if (NEXT) load_scales(t + 1);
     const int left = k - t * 128;
     Operand<EXACT> av[MT], bv[2];
     operand_of<TAIL>(bv[0], cur + BM * 128, pb, 0, left);
@@ -294,23 +304,25 @@ struct Tile {
     for (int x = 0; x < MT; ++x) operand_of<TAIL>(av[x], cur, pa, x, left);
     v4f c[AHEAD];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) c[u] = mfma128(bv[0], av[u]);
-#pragma unroll
-    for (int u = 0; u < MT * NT; ++u) {
-      const int x = u % MT, y = u / MT, nx = (u + AHEAD) % MT, ny = (u + AHEAD) / MT;
+    for (int i = 0; i < MT * NT + AHEAD; ++i) {
+      const int x = i % MT, y = i / MT, e = i - AHEAD;
       if (x == 0 && y + 1 < NT) {
         pin(pb);
         operand_of<TAIL>(bv[(y + 1) & 1], cur + BM * 128, pb, y + 1, left);
       }
-      v4f co = c[u % AHEAD];
-      if (ny < NT) {
-        pin(bv[ny & 1], co);
-        v4f cn = mfma128(bv[ny & 1], av[nx]);
+      if (NEXT && i % EVERY == 1 && i / EVERY < LOADS) load_one(t + 1, i / EVERY, nxt);
+      v4f co = {0.f, 0.f, 0.f, 0.f};
+      if (e >= 0) co = c[e % AHEAD];
+      if (i < MT * NT) {
+        pin(bv[y & 1], co);
+        v4f cn = mfma128(bv[y & 1], av[x]);
         pin(cn, co);
-        c[u % AHEAD] = cn;
+        c[i % AHEAD] = cn;
       }
+      if (e >= 0) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[x][y][v] = fmaf(co[v], s[x], acc[x][y][v]);
+        for (int v = 0; v < 4; ++v) acc[e % MT][e / MT][v] = fmaf(co[v], s[e % MT], acc[e % MT][e / MT][v]);
+      }
     }
   }
 };
@@ -349,16 +361,40 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
     w.load(0, lds[0]);
     w.load_scales(0);
   }
-  const int whole = a.k >> 7;
-  for (int t = 0; t < whole; ++t) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): this block is in LDS
+  auto arrive = [&] {
+    __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): the block's loads, issued one block ago
     __syncthreads();
-    w.template block<false>(t, lds[t & 1], lds[(t & 1) ^ 1]);
+  };
+  int t = 0;
+  for (; t + 1 < w.nb; ++t) {
+    arrive();
+    w.template block<false, true>(t, lds[t & 1], lds[(t & 1) ^ 1]);
   }
-  if (whole < w.nb) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-    __syncthreads();
-    w.template block<true>(whole, lds[whole & 1], lds[(whole & 1) ^ 1]);
+  if (w.nb > 0) {
+    arrive();
+    w.template block<true, false>(t, lds[t & 1], lds[(t & 1) ^ 1]);   // the last one may be short
+  }
+  if (a.wide && m0 + BM <= a.m && n0 + BN <= a.n) {      // a whole tile: no bounds, 16 bytes a store
+#pragma unroll
+    for (int x = 0; x < K::MT; ++x) {
+      T *row = static_cast<T *>(a.c) + static_cast<int64_t>(m0 + w.wm + 16 * x + w.j) * a.ldc + n0 + w.wn;
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int y = 0; y < K::NT; ++y) *reinterpret_cast<v4f *>(row + 16 * y + 4 * w.g) = w.acc[x][y];
+      } else {
+        // Two neighbouring tiles: lane rows of 16 exchange halves, so that a lane holds eight
+        // consecutive outputs, lane groups 0 and 2 those of the first tile.
+        row += 16 * (w.g & 1) + 8 * (w.g >> 1);
+#pragma unroll
+        for (int y = 0; y < K::NT; y += 2) {
+          const u32x2 p = pack4<T>(w.acc[x][y]), q = pack4<T>(w.acc[x][y + 1]);
+          const v2u lo = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+          const v2u hi = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+          *reinterpret_cast<u32x4 *>(row + 16 * y) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+      }
+    }
+    return;
   }
 #pragma unroll
   for (int y = 0; y < K::NT; ++y)
@@ -416,7 +452,7 @@ extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_sca
   const size_t size = c_type == ECHO_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(c) % size) return fail(ECHO_EINVAL, "echo_matmul_fp8: c is not aligned to its type");
   const MatArgs x = {a, b, a_scale, b_scale, lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc, m, n, k, c,
-                     reinterpret_cast<uintptr_t>(c) % (4 * size) == 0 && ldc % 4 == 0};
+                     reinterpret_cast<uintptr_t>(c) % 16 == 0 && ldc * size % 16 == 0};
   switch (c_type) {
     case ECHO_BF16: return launch_matmul<bf16_t>(x, S(stream));
     case ECHO_FP16: return launch_matmul<fp16_t>(x, S(stream));
