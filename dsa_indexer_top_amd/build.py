@@ -19,6 +19,10 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(ROOT, "include")]
+# The block-scaled product adds every MFMA's result to vector registers at once: left to itself the
+# compiler sends the results of workgroups with few waves through accumulation registers, one move
+# and a wait per value.
+EXTRA = {"matmul_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 DEVICE = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
@@ -30,7 +34,7 @@ def _compile(src):
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     cmd = [HIPCC] + COMMON
     if src.endswith(".hip"):
-        cmd += DEVICE
+        cmd += DEVICE + EXTRA.get(src, [])
     cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:

@@ -110,15 +110,16 @@ ECHO_DEV void store_c(const MatArgs &a, int64_t i, int32_t j, const v4f &v) {
 }
 
 // ---------------------------------------------------------------- few rows
-// One workgroup per 16 * NT weight rows and 16 * MT activation rows; its 8 waves take the scale
-// blocks in turn and their sums are joined in LDS in wave order.  Reading the weights is what
-// costs here, so every output type gets the exact products.
+// One workgroup per 16 * NT weight rows and all (at most 16 * MT) activation rows; its 8 waves take
+// the scale blocks in turn and their sums are joined in LDS in wave order.  Reading the weights is
+// what costs here (1 x 8192 x 8192 on MI355X: 13.6 us = 4.9 TB/s; 1 x 8192 x 2048: 5.1 us, mostly
+// the launch and one round trip), so every output type gets the exact products.
 constexpr int SW = 8;
 template <typename T, int MT, int NT>
 __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
   __shared__ float part[SW][MT * NT][64 * 4];
   const int wv = threadIdx.x >> 6, l = lane_id(), j = l & 15, g = l >> 4;
-  const int32_t n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
+  const int32_t n0 = blockIdx.x * (16 * NT), m0 = 0;
   const int nb = (a.k + 127) >> 7;
   const uint8_t *bp[NT], *ap[MT];
 #pragma unroll
@@ -130,19 +131,33 @@ __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
   for (int x = 0; x < MT; ++x)
 #pragma unroll
     for (int y = 0; y < NT; ++y) acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int t = wv; t < nb; t += SW) {
+  // The next block's loads are under way while a block is converted and multiplied.
+  v8i nbv[NT], nav[MT];
+  float nsa[MT], nsb = 0.f;
+  auto fetch = [&](int t) {
     const int left = min(a.k - t * 128, 128);
     const int64_t o = static_cast<int64_t>(t) * 128;
-    Operand<true> bv[NT], av[MT];
-    float s[MT];
-    const float sb = a.sb[(n0 >> 7) * a.bs_row + t * a.bs_blk];
 #pragma unroll
-    for (int y = 0; y < NT; ++y) bv[y].set(load_operand(bp[y] + o, g, left));
+    for (int y = 0; y < NT; ++y) nbv[y] = load_operand(bp[y] + o, g, left);
 #pragma unroll
     for (int x = 0; x < MT; ++x) {
-      av[x].set(load_operand(ap[x] + o, g, left));
-      s[x] = a.sa[min(m0 + 16 * x + j, a.m - 1) * a.as_row + t * a.as_blk] * sb;
+      nav[x] = load_operand(ap[x] + o, g, left);
+      nsa[x] = a.sa[min(m0 + 16 * x + j, a.m - 1) * a.as_row + t * a.as_blk];
     }
+    nsb = a.sb[(n0 >> 7) * a.bs_row + t * a.bs_blk];
+  };
+  if (wv < nb) fetch(wv);
+  for (int t = wv; t < nb; t += SW) {
+    Operand<true> bv[NT], av[MT];
+    float s[MT];
+#pragma unroll
+    for (int y = 0; y < NT; ++y) bv[y].set(nbv[y]);
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      av[x].set(nav[x]);
+      s[x] = nsa[x] * nsb;
+    }
+    if (t + SW < nb) fetch(t + SW);
 #pragma unroll
     for (int x = 0; x < MT; ++x)
 #pragma unroll
@@ -166,6 +181,9 @@ __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
 }
 
 // ---------------------------------------------------------------- tiles
+// s_waitcnt's operand for "at most n vector memory operations outstanding" and nothing else.
+constexpr int vmcnt(int n) { return (n & 15) | 0x0F70 | (n >> 4) << 14; }
+
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void glb_void;
 
@@ -251,52 +269,70 @@ ECHO_DEV void pin(Operand<true> &, v4f &c) { asm volatile("" : "+v"(c)); }
 ECHO_DEV void pin(v4f &n, v4f &c) { asm volatile("" : "+v"(n), "+v"(c)); }
 ECHO_DEV void pin(Pieces &p) { asm volatile("" : "+v"(p.p0), "+v"(p.p1)); }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, int STAGES>
 struct Tile {
   static constexpr int NW = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
   static constexpr int AHEAD = 2;                        // products in flight ahead of their FMAs
-  static constexpr int EVERY = 2;                        // products between two loads
+  static constexpr int LOADS = StageLoad<BM, NW>::N + StageLoad<BN, NW>::N + 1;   // a thread's loads of a block
+  static constexpr int EVERY = MT * NT / LOADS / 2 > 0 ? MT * NT / LOADS / 2 + 1 : 1;   // products between two of them
+  static constexpr int ROWS = (BM + BN) * 128, STAGE = ROWS + NW * 256;           // bytes: codes, each wave's scales
   static constexpr bool EXACT = sizeof(T) == 4;
-  static_assert(WN <= 128, "one weight scale per wave");
-  static_assert(MT >= AHEAD, "the products ahead are of this or the next operand");
+  static_assert(WN <= 128 && WM <= 64, "one weight scale per wave, one activation scale per lane");
+  static_assert(MT >= AHEAD && NT % 2 == 0, "the products ahead are of this or the next operand");
+  static_assert(LOADS * EVERY <= MT * NT + AHEAD, "every load has its place");
+  static_assert((STAGES - 2) * LOADS < 64, "the wait counts them");
+  static_assert(STAGES * STAGE <= 160 * 1024, "a workgroup's LDS");
   StageLoad<BM, NW> la;
   StageLoad<BN, NW> lb;
-  const float *sa[MT], *sb;
+  const float *sa, *sb;                                  // uniform
+  uint32_t sa_off;                                       // the lane's row of the wave's tile
   int64_t as_blk, bs_blk;
   int nb, k, wv, wm, wn, j, g, seg;
   Pieces pa, pb;
   v4f acc[MT][NT];
-  float ns[MT], nsb;                                     // the next block's scales
+  float sbv;                                             // weight scales of 64 blocks, one per lane
 
-  static constexpr int LOADS = StageLoad<BM, NW>::N + StageLoad<BN, NW>::N;
   ECHO_DEV void load_one(int t, int i, uint8_t *__restrict__ stage) const {
+    constexpr int NA = StageLoad<BM, NW>::N, NB = StageLoad<BN, NW>::N;
     const uint32_t back = seg < k - t * 128 ? 0u : static_cast<uint32_t>(seg);
-    if (i < StageLoad<BM, NW>::N) la.load(stage, t, i, wv, back);
-    else lb.load(stage + BM * 128, t, i - StageLoad<BM, NW>::N, wv, back);
+    if (i < NA) la.load(stage, t, i, wv, back);
+    else if (i < NA + NB) lb.load(stage + BM * 128, t, i - NA, wv, back);
+    else
+      __builtin_amdgcn_global_load_lds((glb_void *)(sa + t * as_blk + sa_off), (lds_void *)(stage + ROWS + wv * 256), 4, 0, 0);
   }
   ECHO_DEV void load(int t, uint8_t *__restrict__ stage) const {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load_one(t, i, stage);
   }
-  ECHO_DEV void load_scales(int t) {
-#pragma unroll
-    for (int x = 0; x < MT; ++x) ns[x] = sa[x][t * as_blk];
-    nsb = sb[t * bs_blk];
-  }
+  ECHO_DEV void load_weight_scales(int t) { sbv = sb[min(t + lane_id(), nb - 1) * bs_blk]; }
   template <bool TAIL>
   ECHO_DEV void operand_of(Operand<EXACT> &o, const uint8_t *__restrict__ stage, const Pieces &p, int rows16, int left) const {
     v8i v = p.read(stage, rows16);
     if (TAIL) v = keep_bytes(v, g, left);
     o.set(v);
   }
-  // Block t from `cur`; with NEXT block t + 1's loads go to `nxt`.  Product i is issued before the
+  // Waits until the loads of all blocks but the `later` youngest have arrived, at most STAGES - 2.
+  template <int R = STAGES - 2>
+  ECHO_DEV static void wait(int later) {
+    if constexpr (R == 0) {
+      __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    } else {
+      if (later >= R) __builtin_amdgcn_s_waitcnt(vmcnt(R * LOADS));
+      else wait<R - 1>(later);
+    }
+  }
+  // Block t from `cur`; with NEXT block t + STAGES - 1's loads go to `nxt`.  Product i is issued before the
   // FMAs of product i - AHEAD; a weight operand is read once the one before the last has been used.
   template <bool TAIL, bool NEXT>
   ECHO_DEV void block(int t, uint8_t *__restrict__ cur, uint8_t *__restrict__ nxt) {
+    if (t > 0 && (t & 63) == 0) {
+      load_weight_scales(t);
+      __builtin_amdgcn_s_waitcnt(vmcnt(0));              // here, not on every block's way
+    }
+    const float sbt = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sbv), t & 63));
     float s[MT];
 #pragma unroll
-    for (int x = 0; x < MT; ++x) s[x] = ns[x] * nsb;
-    if (NEXT) load_scales(t + 1);
+    for (int x = 0; x < MT; ++x) s[x] = reinterpret_cast<const float *>(cur + ROWS + wv * 256)[16 * x + j] * sbt;
     const int left = k - t * 128;
     Operand<EXACT> av[MT], bv[2];
     operand_of<TAIL>(bv[0], cur + BM * 128, pb, 0, left);
@@ -310,7 +346,7 @@ struct Tile {
         pin(pb);
         operand_of<TAIL>(bv[(y + 1) & 1], cur + BM * 128, pb, y + 1, left);
       }
-      if (NEXT && i % EVERY == 1 && i / EVERY < LOADS) load_one(t + 1, i / EVERY, nxt);
+      if (NEXT && i % EVERY == EVERY - 1 && i / EVERY < LOADS) load_one(t + STAGES - 1, i / EVERY, nxt);
       v4f co = {0.f, 0.f, 0.f, 0.f};
       if (e >= 0) co = c[e % AHEAD];
       if (i < MT * NT) {
@@ -327,10 +363,10 @@ struct Tile {
   }
 };
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel(MatArgs a) {
-  typedef Tile<T, BM, BN, WM, WN> K;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
+  typedef Tile<T, BM, BN, WM, WN, STAGES> K;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGES][K::STAGE];
   K w;
   w.wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int l = lane_id();
@@ -350,29 +386,38 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
   w.lb.init(a.b, a.ldb, n0, a.n, w.wv, w.seg);
   w.as_blk = a.as_blk;
   w.bs_blk = a.bs_blk;
-#pragma unroll
-  for (int x = 0; x < K::MT; ++x) w.sa[x] = a.sa + min(m0 + w.wm + 16 * x + w.j, a.m - 1) * a.as_row;
+  w.sa = a.sa + m0 * a.as_row;
+  w.sa_off = static_cast<uint32_t>(min(w.wm + min(l, WM - 1), a.m - 1 - m0)) * static_cast<uint32_t>(a.as_row);
   w.sb = a.sb + (min(n0 + w.wn, a.n - 1) >> 7) * a.bs_row;
 #pragma unroll
   for (int x = 0; x < K::MT; ++x)
 #pragma unroll
     for (int y = 0; y < K::NT; ++y) w.acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
   if (w.nb > 0) {
-    w.load(0, lds[0]);
-    w.load_scales(0);
+    w.load_weight_scales(0);
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t) w.load(min(t, w.nb - 1), lds[t]);   // no branch: the loads stay countable
   }
-  auto arrive = [&] {
-    __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): the block's loads, issued one block ago
-    __syncthreads();
+  // Block t is in LDS for every wave, and every wave has read block t - 1 (its products have taken
+  // the operands).  A plain barrier: __syncthreads() would wait for the younger blocks' loads too.
+  auto arrive = [&](int t) {
+    K::wait(w.nb - 1 - t);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
-  int t = 0;
-  for (; t + 1 < w.nb; ++t) {
-    arrive();
-    w.template block<false, true>(t, lds[t & 1], lds[(t & 1) ^ 1]);
+  int t = 0, cur = 0, nxt = STAGES - 1;
+  for (; t + STAGES - 1 < w.nb; ++t) {
+    arrive(t);
+    w.template block<false, true>(t, lds[cur], lds[nxt]);
+    nxt = cur;
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
   }
-  if (w.nb > 0) {
-    arrive();
-    w.template block<true, false>(t, lds[t & 1], lds[(t & 1) ^ 1]);   // the last one may be short
+  for (; t < w.nb; ++t) {                                // nothing more to load; the last block may be short
+    arrive(t);
+    w.template block<true, false>(t, lds[cur], lds[nxt]);
+    nxt = cur;
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
   }
   if (a.wide && m0 + BM <= a.m && n0 + BN <= a.n) {      // a whole tile: no bounds, 16 bytes a store
 #pragma unroll
@@ -403,28 +448,42 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
       store_c<T>(a, m0 + w.wm + 16 * x + w.j, n0 + w.wn + 16 * y + 4 * w.g, w.acc[x][y]);
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, int STAGES>
 static void launch_tiles(const MatArgs &a, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>((static_cast<int64_t>(a.m) + BM - 1) / BM * ((static_cast<int64_t>(a.n) + BN - 1) / BN));
-  matmul_tile_kernel<T, BM, BN, WM, WN><<<tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
+  matmul_tile_kernel<T, BM, BN, WM, WN, STAGES><<<tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
 }
 
 template <typename T>
 static int launch_matmul(const MatArgs &a, hipStream_t st) {
   const auto cdiv = [](int32_t x, int32_t y) { return static_cast<uint32_t>((static_cast<int64_t>(x) + y - 1) / y); };
+  const auto tiles = [&](int bm, int bn) { return static_cast<int64_t>(cdiv(a.m, bm)) * cdiv(a.n, bn); };
+  // Up to 32 rows the weights' bytes are the cost: as many workgroups as there are 16-row weight
+  // tiles, or half as many once those fill the chip (MI355X, 20 x 1024 x 2048: 4.5 us with 16 weight
+  // rows, 5.5 with 32; 32 x 8192 x 2048: 8.6 and 6.7; 64 x 64 tiles take 7.6 and 8.1).
   if (a.m <= 16) {
-    matmul_few_kernel<T, 1, 1><<<dim3(cdiv(a.n, 16), cdiv(a.m, 16)), SW * 64, 0, st>>>(a);
-  } else if (a.m <= 64) {
-    matmul_few_kernel<T, 2, 2><<<dim3(cdiv(a.n, 32), cdiv(a.m, 32)), SW * 64, 0, st>>>(a);
+    matmul_few_kernel<T, 1, 1><<<dim3(cdiv(a.n, 16)), SW * 64, 0, st>>>(a);
+  } else if (a.m <= 32 && a.n < 256 * 32) {
+    matmul_few_kernel<T, 2, 1><<<dim3(cdiv(a.n, 16)), SW * 64, 0, st>>>(a);
+  } else if (a.m <= 32) {
+    matmul_few_kernel<T, 2, 2><<<dim3(cdiv(a.n, 32)), SW * 64, 0, st>>>(a);
   } else {
-    const int64_t big = static_cast<int64_t>(cdiv(a.m, 256)) * cdiv(a.n, 256);
-    if constexpr (sizeof(T) == 2) {
-      if (big >= 256) {
-        launch_tiles<T, 256, 256, 64, 128>(a, st);
-        return check_launch("matmul_fp8");
-      }
+    // The largest tile that still gives each of the 256 CUs one.  Small tiles keep more stages in
+    // flight, since a block of theirs is multiplied before the next could arrive (MI355X, three
+    // stages against two for 64 x 128: 256 x 8192 x 2048 10.2 us and 12.8; 128 x 128 tiles with two:
+    // 20.4; 8192 x 128 x 4096: 12.8 us in 64 x 64, 36 in 128 x 128).
+    bool done = false;
+    if constexpr (sizeof(T) == 2) {                      // fp32 results hold their operands as bf16: too many registers
+      if ((done = tiles(256, 256) >= 256)) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
     }
-    launch_tiles<T, 128, 128, 64, 64>(a, st);
+    if (done) {
+    } else if (tiles(128, 128) >= 256) {
+      launch_tiles<T, 128, 128, 64, 64, 2>(a, st);
+    } else if (tiles(64, 128) >= 256) {
+      launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
+    } else {
+      launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
+    }
   }
   return check_launch("matmul_fp8");
 }

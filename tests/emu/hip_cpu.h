@@ -140,6 +140,7 @@ inline void emu_amdgcn_global_load_lds(const void *g, void *lds, unsigned size, 
 }
 inline void emu_amdgcn_s_waitcnt(int) {}
 inline void emu_amdgcn_s_setprio(int) {}
+#define emu_amdgcn_s_barrier() emu::barrier()
 
 // ---- host runtime
 typedef int hipError_t;

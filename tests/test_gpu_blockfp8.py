@@ -208,3 +208,31 @@ def test_quant_then_product_of_hidden_states():
     xv, s = x.double().numpy(), O.spread(host(sa).astype(np.float64), k)
     bound = (np.abs(xv) * 2.0 ** -4 + s * 2.0 ** -10) @ np.abs(bv).T * 1.001
     assert (np.abs(f64(c) - xv @ bv.T) <= bound).all()
+
+
+# Every tile's shape at sizes that fill the chip with it, edges included (the products' last rows,
+# columns and block are partial), and one whole number of tiles.
+@pytest.mark.parametrize("m,n,k,kind", [
+    (4100, 4111, 400, "bf16"), (4096, 4096, 384, "fp16"), (2000, 2100, 300, "fp32"), (2000, 2100, 777, "bf16"),
+    (2048, 2048, 256, "fp32"), (1030, 2050, 700, "bf16"), (1024, 2048, 1152, "fp16"), (1024, 2048, 130, "fp32"),
+    (640, 640, 1500, "bf16"), (640, 640, 1408, "fp32"), (33, 4000, 640, "bf16"), (32, 8192, 1111, "bf16"),
+    (31, 1000, 2047, "fp32"), (16, 3001, 2048, "fp16")])
+def test_product_full_size_tiles_exact(m, n, k, kind):
+    """Whole numbers and powers of two as scales: exact in fp32 in any order and on either matrix
+    core (a product is at most 2^4 times another's unit, far above 2^-13), so the result is the
+    float64 one rounded once."""
+    announce("product tiles", m, n, k, kind)
+    g = torch.Generator().manual_seed(m + n + k)
+    ld = -(-k // 16) * 16
+    f8 = torch.float8_e4m3fn
+    ints = lambda r: torch.randint(-4, 5, (r, k), generator=g).double()
+    av, bv = ints(m), ints(n)
+    code = lambda v: torch.cat([v.float().to(f8).view(torch.uint8), torch.full((v.shape[0], ld - k), 0x7F, dtype=torch.uint8)], 1)
+    nb = -(-k // 128)
+    sa = 2.0 ** torch.randint(-3, 1, (m, nb), generator=g)
+    sb = 2.0 ** torch.randint(-3, 1, (-(-n // 128), nb), generator=g)
+    c = torch.full((m, n), -77.0, dtype=TYPES[kind], device="cuda")
+    B.matmul_fp8(code(av).cuda()[:, :k], sa.cuda(), code(bv).cuda()[:, :k], sb.cuda(), c)
+    spread = lambda s: s.double().repeat_interleave(128, 1)[:, :k]
+    want = (av * spread(sa)).cuda() @ (bv * spread(sb.repeat_interleave(128, 0)[:n])).cuda().t()
+    assert torch.equal(c, want.to(TYPES[kind]))
