@@ -12,15 +12,19 @@
 //
 // A row is held by G lanes of 8 values (G the power of two that covers D), so a wave reads 64/G
 // rows with 16-byte loads, the sums are butterflies over those lanes, and the partner of a
-// rotated half comes from another lane of the row.  Everything is read once and written once:
-// the kernel is bound by HBM at many tokens and by launch latency at few.  Query rows and key
-// rows are separate workgroups, so a wave loads the norm's weights once for all its rows.
+// rotated half comes from another lane of the row.  Everything is read once and written once.
+//
+// A wave takes HU loads' worth of rows.  Where a side has at least as many heads as a load has
+// rows, they are heads of ONE token: its position, its angles and every address but the lane's
+// part are the same for the whole wave, so they are scalar work and the angles are read once for
+// all its heads.  With fewer heads (the indexer's single key) a load takes several tokens instead,
+// lest most lanes idle.
 #include "float_types.cuh"
 
 namespace echo {
 
 constexpr int HT = 256;          // threads per workgroup
-constexpr int HU = 4;            // row groups per wave
+constexpr int HU = 4;            // loads per wave
 
 struct HeadSide {                // the query or the key side
   const void *x;
@@ -28,6 +32,8 @@ struct HeadSide {                // the query or the key side
   int64_t xt, xh, yt, yh;        // strides of tokens and heads, in elements
   const float *weight, *bias;
   int32_t heads, norm;
+  uint32_t chunks;               // waves per token; 0: a load takes several tokens
+  int32_t across;                // heads of a token in one load, a power of two, where chunks is 0
 };
 struct Fp8Side {                 // what the FP8 form writes
   const float *w;
@@ -46,7 +52,7 @@ struct HeadArgs {
   const int32_t *pos;
   const float *cos_sin;
   int32_t n_tok, dim, rot_begin, rot, n_pos;
-  uint32_t q_groups;             // workgroups of the query side
+  uint32_t waves[2];             // of each side
   float eps;
 };
 
@@ -57,16 +63,12 @@ ECHO_DEV void load_f8(const float *__restrict__ p, float (&v)[VEC]) {
   for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
 }
 
-template <typename T, int G, bool FP8, bool NEXT>
-__global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
-  constexpr int ROWS = 64 / G;                       // rows of one wave-wide load
+// One wave's rows of side s.  ONE: heads of one token, HU loads of 64 / G; otherwise HU loads of
+// several tokens' heads.
+template <typename T, int G, bool FP8, bool NEXT, bool ONE>
+ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32_t wave) {
+  constexpr int ROWS = 64 / G;                       // rows of one load
   const int l = lane_id(), sub = l / G, j = l % G;
-  const bool is_k = blockIdx.x >= a.q_groups;
-  const HeadSide &s = a.side[is_k ? 1 : 0];
-  const uint32_t blk = is_k ? blockIdx.x - a.q_groups : blockIdx.x;
-  const uint32_t first = (blk * (HT / 64) + (threadIdx.x >> 6)) * (HU * ROWS);
-  const uint32_t heads = static_cast<uint32_t>(s.heads);
-  const uint32_t n_rows = static_cast<uint32_t>(a.n_tok) * heads;
   const bool in_row = j * VEC < a.dim;
 
   // this lane's place in the rotation
@@ -76,6 +78,30 @@ __global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
   const int angle = NEXT ? e >> 1 : (second ? e - half : e);
   const int mate = turns && !NEXT ? l + (second ? -(half / VEC) : half / VEC) : l;
 
+  // its tokens and heads: token tok + u * tok_step, head head + u * head_step
+  int32_t tok, head, tok_step, head_step;
+  if (ONE) {
+    tok = static_cast<int32_t>(wave / s.chunks);
+    head = static_cast<int32_t>(wave - tok * s.chunks) * (HU * ROWS) + sub;
+    tok_step = 0;
+    head_step = ROWS;
+  } else {
+    tok_step = ROWS / s.across;
+    tok = static_cast<int32_t>(wave) * HU * tok_step + sub / s.across;
+    head = sub % s.across;
+    head_step = 0;
+  }
+  Raw8<T> raw[HU];
+  int32_t pos[HU];
+  bool live[HU];
+#pragma unroll
+  for (int u = 0; u < HU; ++u) {
+    const int32_t t = tok + u * tok_step, h = head + u * head_step;
+    const bool in = t < a.n_tok && h < s.heads;
+    pos[u] = ONE ? a.pos[t] : in ? a.pos[t] : -1;
+    raw[u] = in && in_row ? load8(static_cast<const T *>(s.x) + t * s.xt + (h * s.xh + j * VEC)) : zero8<T>();
+    live[u] = in && pos[u] >= 0 && pos[u] < a.n_pos;
+  }
   float wt[VEC], bi[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) { wt[i] = 1.f; bi[i] = 0.f; }
@@ -83,35 +109,24 @@ __global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
     if (s.weight) load_f8(s.weight + j * VEC, wt);
     if (s.bias) load_f8(s.bias + j * VEC, bi);
   }
-
-  Raw8<T> raw[HU];
-  int32_t pos[HU];
-  uint32_t tok[HU], head[HU];
+  float c[VEC], d[VEC];                              // cosines and sines of the lane's angles
 #pragma unroll
   for (int u = 0; u < HU; ++u) {
-    const uint32_t row = first + u * ROWS + sub;
-    const bool in = row < n_rows;
-    tok[u] = in ? row / heads : 0u;
-    head[u] = in ? row - tok[u] * heads : 0u;
-    pos[u] = in ? a.pos[tok[u]] : -1;                // -1: nothing is written
-    raw[u] = in && in_row ? load8(static_cast<const T *>(s.x) + tok[u] * s.xt + head[u] * s.xh + j * VEC)
-                          : zero8<T>();
-  }
+    if (u == 0 || !ONE) {
 #pragma unroll
-  for (int u = 0; u < HU; ++u) {
-    const bool live = pos[u] >= 0 && pos[u] < a.n_pos;
-    float c[VEC], d[VEC];
+      for (int i = 0; i < VEC; ++i) { c[i] = 1.f; d[i] = 0.f; }
+      if (turns && (ONE ? pos[u] >= 0 && pos[u] < a.n_pos : live[u])) {
+        const float *cs = a.cos_sin + static_cast<int64_t>(pos[u]) * a.rot + angle;
+        if (NEXT) {
+          const f32x4 cv = *reinterpret_cast<const f32x4 *>(cs), sv = *reinterpret_cast<const f32x4 *>(cs + half);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) { c[i] = 1.f; d[i] = 0.f; }
-    if (turns && live) {
-      const float *cs = a.cos_sin + static_cast<int64_t>(pos[u]) * a.rot + angle;
-      if (NEXT) {
-        const f32x4 cv = *reinterpret_cast<const f32x4 *>(cs), sv = *reinterpret_cast<const f32x4 *>(cs + half);
+          for (int i = 0; i < 4; ++i) { c[i] = cv[i]; d[i] = sv[i]; }
+        } else {
+          load_f8(cs, c);
+          load_f8(cs + half, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { c[i] = cv[i]; d[i] = sv[i]; }
-      } else {
-        load_f8(cs, c);
-        load_f8(cs + half, d);
+          for (int i = 0; i < VEC; ++i) d[i] = second ? d[i] : -d[i];
+        }
       }
     }
     float x[VEC];
@@ -147,28 +162,41 @@ __global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float p = __shfl(x[i], mate, 64);
-        if (turns) x[i] = x[i] * c[i] + (second ? p : -p) * d[i];
+        if (turns) x[i] = x[i] * c[i] + p * d[i];
       }
     }
     const float amax = FP8 ? group_amax<G>(x) : 0.f;
-    if (!live) continue;
+    if (!live[u]) continue;
+    const int32_t t = tok + u * tok_step, h = head + u * head_step;
     if (!FP8) {
-      if (in_row) store8(static_cast<T *>(s.y) + tok[u] * s.yt + head[u] * s.yh + j * VEC, x);
+      if (in_row) store8(static_cast<T *>(s.y) + t * s.yt + (h * s.yh + j * VEC), x);
       continue;
     }
     const Fp8Scale sc = fp8_scale(amax);
     const u32x2 code = quantise8(x, sc.inv);
     if (!is_k) {
-      const int64_t row = static_cast<int64_t>(tok[u]) * heads + head[u];
+      const int64_t row = static_cast<int64_t>(t) * s.heads + h;
       *reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC) = code;
-      if (j == 0) a.f.w_out[row] = a.f.w[tok[u] * a.f.wt + head[u]] * sc.scale * a.f.w_mul;
+      if (j == 0) a.f.w_out[row] = a.f.w[t * a.f.wt + h] * sc.scale * a.f.w_mul;
     } else {
-      const int64_t slot = a.f.slot[tok[u]];
+      const int64_t slot = a.f.slot[t];
       if (slot < 0 || slot >= a.f.n_slots) continue;
       *reinterpret_cast<u32x2 *>(a.f.k_cache + slot * D + j * VEC) = code;
       if (j == 0) a.f.k_scale[slot] = sc.scale;
     }
   }
+}
+
+// Waves of the query side first, then those of the key side.
+template <typename T, int G, bool FP8, bool NEXT>
+__global__ __launch_bounds__(HT) void heads_kernel(HeadArgs a) {
+  const uint32_t id = blockIdx.x * (HT / 64) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const bool is_k = id >= a.waves[0];
+  const uint32_t wave = is_k ? id - a.waves[0] : id;
+  if (is_k && wave >= a.waves[1]) return;
+  const HeadSide &s = a.side[is_k ? 1 : 0];
+  if (s.chunks) heads_wave<T, G, FP8, NEXT, true>(a, s, is_k, wave);
+  else heads_wave<T, G, FP8, NEXT, false>(a, s, is_k, wave);
 }
 
 template <typename T, int G, bool FP8>
@@ -179,17 +207,27 @@ static void launch_heads_g(const HeadArgs &a, bool next, uint32_t grid, hipStrea
     heads_kernel<T, G, FP8, false><<<grid, HT, 0, st>>>(a);
 }
 
-static uint32_t row_groups(int64_t rows, int g) {
-  const int64_t per = static_cast<int64_t>(HT / 64) * HU * (64 / g);
-  return static_cast<uint32_t>((rows + per - 1) / per);
+// Shares a side's rows out to waves; returns their number.
+static uint32_t side_waves(HeadSide &s, int64_t n_tok, int g) {
+  const int rows = 64 / g;
+  if (s.heads == 0) return 0;
+  if (s.heads >= rows) {
+    s.chunks = static_cast<uint32_t>((s.heads + HU * rows - 1) / (HU * rows));
+    return static_cast<uint32_t>(n_tok * s.chunks);
+  }
+  s.chunks = 0;
+  s.across = 1;
+  while (s.across < s.heads) s.across *= 2;
+  const int64_t per = static_cast<int64_t>(HU) * (rows / s.across);
+  return static_cast<uint32_t>((n_tok + per - 1) / per);
 }
 
 template <typename T, bool FP8>
 static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
   int g = 2;
   while (g * VEC < a.dim) g *= 2;
-  a.q_groups = row_groups(static_cast<int64_t>(a.n_tok) * a.side[0].heads, g);
-  const uint32_t grid = a.q_groups + row_groups(static_cast<int64_t>(a.n_tok) * a.side[1].heads, g);
+  for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g);
+  const uint32_t grid = static_cast<uint32_t>((static_cast<uint64_t>(a.waves[0]) + a.waves[1] + HT / 64 - 1) / (HT / 64));
   if (FP8) {
     launch_heads_g<T, 16, FP8>(a, next, grid, st);
   } else {
@@ -251,8 +289,8 @@ static int check_heads(const char *fn, const echo_qk_args *q, bool *empty) {
 
 static HeadArgs head_args(const echo_qk_args *q) {
   HeadArgs a = {};
-  a.side[0] = HeadSide{q->q, nullptr, q->q_tok_stride, q->q_head_stride, 0, 0, q->q_weight, q->q_bias, q->n_q_heads, q->q_norm};
-  a.side[1] = HeadSide{q->k, nullptr, q->k_tok_stride, q->k_head_stride, 0, 0, q->k_weight, q->k_bias, q->n_k_heads, q->k_norm};
+  a.side[0] = HeadSide{q->q, nullptr, q->q_tok_stride, q->q_head_stride, 0, 0, q->q_weight, q->q_bias, q->n_q_heads, q->q_norm, 0, 1};
+  a.side[1] = HeadSide{q->k, nullptr, q->k_tok_stride, q->k_head_stride, 0, 0, q->k_weight, q->k_bias, q->n_k_heads, q->k_norm, 0, 1};
   a.pos = q->pos;
   a.cos_sin = q->cos_sin;
   a.n_tok = q->n_tok;
