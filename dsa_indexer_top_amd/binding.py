@@ -407,7 +407,6 @@ def page_step(len_in, new_len, page_table, page_size, free_list, count_in, len_o
     if not (len_in.dtype is i32 and new_len.dtype is i32 and len_out.dtype is i32 and row_begin.dtype is i32
             and pos.dtype is i32 and count_in.dtype is i32 and count_out.dtype is i32 and status.dtype is i32
             and free_list.dtype is i32 and page_table.dtype is i32 and slot.dtype is torch.int64
-            and len_in.dim() == new_len.dim() == len_out.dim() == row_begin.dim() == pos.dim() == slot.dim() == 1
             and new_len.numel() == n and len_out.numel() == n and row_begin.numel() == n + 1
             and pos.numel() == cap and count_in.numel() == 1 and count_out.numel() == 1
             and status.numel() == 1 and page_table.dim() == 2 and page_table.shape[0] == n

@@ -32,11 +32,14 @@ constexpr int VEC = 8;           // elements per lane
 // Eight consecutive elements as loaded: 16 bytes (bf16, fp16) or 32 (fp32).
 template <typename T> struct Raw8 { u32x4 w[sizeof(T) * VEC / 16]; };
 
+// Read once by the whole launch, so past the caches (8191 x 45 x 128 fp16 heads on MI355X: 40.1 us
+// with plain loads, 36.8 with these).
 template <typename T>
 ECHO_DEV Raw8<T> load8(const T *__restrict__ p) {
   Raw8<T> r;
 #pragma unroll
-  for (unsigned i = 0; i < sizeof(T) * VEC / 16; ++i) r.w[i] = reinterpret_cast<const u32x4 *>(p)[i];
+  for (unsigned i = 0; i < sizeof(T) * VEC / 16; ++i)
+    r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p) + i);
   return r;
 }
 template <typename T>

@@ -176,7 +176,9 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
     const u32x2 code = quantise8(x, sc.inv);
     if (!is_k) {
       const int64_t row = static_cast<int64_t>(t) * s.heads + h;
-      *reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC) = code;
+      // 8 bytes a lane: past the caches a prefill chunk's codes leave faster (32768 tokens: 175.6 us
+      // with plain stores, 165.7 with these)
+      __builtin_nontemporal_store(code, reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC));
       if (j == 0) a.f.w_out[row] = a.f.w[t * a.f.wt + h] * sc.scale * a.f.w_mul;
     } else {
       const int64_t slot = a.f.slot[t];

@@ -10,11 +10,13 @@
 // always a token of the step, so the lane that maps that token also writes the page's table entry
 // and no second pass over pages is needed.
 //
-// All of it is latency: the bytes of a decode step fit in a few cache lines per request.  A step
-// of few tokens therefore runs as ONE workgroup and one launch, its prefix sums in LDS.  A step of
-// many tokens (chunked prefill: 16 bytes written per token) takes the prefix sums in one
-// workgroup and then fills the maps from the whole chip, with a launch in between for the pages
-// that come back.
+// All of it is latency: the bytes of a decode step fit in a few cache lines per request.  A step of
+// few tokens therefore runs as ONE workgroup and one launch, its prefix sums in LDS (256 requests
+// on MI355X: 4.7 us).  A step of many tokens (chunked prefill: 16 bytes written per token) takes two
+// launches: the plan (prefix sums, made by every workgroup for itself, and the return of the
+// finished requests' pages, shared out among them) and the fill of the maps from the whole chip
+// (61 requests with up to 8192 new tokens each: 4.0 + 5.5 us; with a launch of its own for the return and
+// the searches in global memory it took 14.8 us).
 #include "float_types.cuh"
 
 namespace echo {
@@ -64,31 +66,43 @@ ECHO_DEV PageRow page_row(const PageArgs &a, int r) {
   return p;
 }
 
-// Workspace (or LDS): prefix sums of the returned and the needed pages, and the step's totals.
-struct PageSums {
-  int32_t *back, *need;          // [n_rows + 1]
-  int32_t *head;                 // [0] free pages after the return, [1] new tokens
+// The plan of a step, in LDS or the workspace: prefix sums, the lengths that are kept, and totals.
+struct PagePlan {
+  int32_t *back, *need, *begin;  // [n_rows + 1]: returned pages, new pages, new tokens before a request
+  int32_t *kept;                 // [n_rows + 1]: its length without the new tokens (the last is not used)
+  int32_t *head;                 // [0] free pages after the return, [1] after the step, [2] 1: refused
 };
+constexpr int PLAN_HEAD = 4;
+ECHO_DEV PagePlan plan_at(int32_t *p, int rows) {
+  return PagePlan{p, p + (rows + 1), p + 2 * (rows + 1), p + 3 * (rows + 1), p + 4 * (rows + 1)};
+}
 
-// Prefix sums of a step by one workgroup of PT threads; each thread owns a run of consecutive
-// requests.  Writes the sums, row_begin, the new lengths and the new count, or, for a step that is
-// refused, zero sums, the old lengths, the old count and a status bit.  begin: where the kernel
-// itself reads row_begin from (LDS or the output).
-ECHO_DEV void page_sums(const PageArgs &a, const PageSums &s, int32_t *begin, uint32_t *tmp) {
+// Plan of a step by one workgroup of PT threads, each of which owns a run of consecutive requests
+// (PER > 0: at most PER of them, kept in registers between the sums and the writing).  A step that
+// is refused gets zero sums, the old lengths and count, and its status bits (set by `tell` alone).
+template <int PER>
+ECHO_DEV void make_plan(const PageArgs &a, const PagePlan &s, uint32_t *tmp, bool tell) {
   constexpr int NW = PT / 64;
   const int t = threadIdx.x, w = t >> 6, l = lane_id();
   const int per = (a.n_rows + PT - 1) / PT;
   const int r0 = min(t * per, a.n_rows), r1 = min(r0 + per, a.n_rows);
   uint32_t sum[3] = {0, 0, 0};
   bool bad = false;
-  for (int r = r0; r < r1; ++r) {
-    const PageRow p = page_row(a, r);
+  auto add = [&](const PageRow &p) {
     sum[0] = OpSat{}(sum[0], p.back);
     sum[1] = OpSat{}(sum[1], p.need);
     sum[2] = OpSat{}(sum[2], p.fresh);
     bad |= p.bad;
-  }
+  };
   const int32_t count = a.count_in[0];
+  PageRow own[PER > 0 ? PER : 1];
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (r0 + i < r1) { own[i] = page_row(a, r0 + i); add(own[i]); }
+  } else {
+    for (int r = r0; r < r1; ++r) add(page_row(a, r));
+  }
   uint32_t incl[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -117,35 +131,65 @@ ECHO_DEV void page_sums(const PageArgs &a, const PageSums &s, int32_t *begin, ui
   uint32_t at[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) at[i] = why ? 0u : base[i] + incl[i] - sum[i];
-  for (int r = r0; r < r1; ++r) {
-    const PageRow p = page_row(a, r);
+  auto put = [&](int r, const PageRow &p) {
     s.back[r] = at[0];
     s.need[r] = at[1];
-    begin[r] = at[2];
-    if (begin != a.row_begin) a.row_begin[r] = at[2];
-    const int32_t len = a.len_in[r];
-    a.len_out[r] = why ? len : p.len + static_cast<int32_t>(p.fresh);
+    s.begin[r] = at[2];
+    s.kept[r] = why ? a.len_in[r] : p.len;
     if (!why) { at[0] += p.back; at[1] += p.need; at[2] += p.fresh; }
+  };
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (r0 + i < r1) put(r0 + i, own[i]);
+  } else {
+    for (int r = r0; r < r1; ++r) put(r, page_row(a, r));
   }
   if (t == 0) {
     const int n = a.n_rows;
     s.back[n] = why ? 0 : total[0];
     s.need[n] = why ? 0 : total[1];
-    begin[n] = why ? 0 : total[2];
-    if (begin != a.row_begin) a.row_begin[n] = begin[n];
+    s.begin[n] = why ? 0 : total[2];
+    s.kept[n] = 0;
     s.head[0] = why ? count : static_cast<int32_t>(have);
-    s.head[1] = begin[n];
-    if (why) atomicOr(a.status, why);
+    s.head[1] = s.head[0] - s.need[n];
+    if (why && tell) atomicOr(a.status, why);
   }
-  __syncthreads();                             // count_in is read before count_out is written
-  if (t == 0) a.count_out[0] = s.head[0] - s.need[a.n_rows];
+  __syncthreads();
 }
 
-// Request r's returned pages onto the stack, by `n` threads.
-ECHO_DEV void return_pages(const PageArgs &a, const PageSums &s, int32_t first_free, int r, int t, int n) {
-  const int32_t b = s.back[r], cnt = s.back[r + 1] - b;
-  const int32_t *src = a.page_table + static_cast<int64_t>(r) * a.max_pages;
-  for (int i = t; i < cnt; i += n) a.free_list[first_free + b + i] = src[i];
+// The step's lengths, count and row_begin, by n threads; nothing reads the old ones any more.
+ECHO_DEV void publish(const PageArgs &a, const PagePlan &s, int t, int n) {
+  for (int r = t; r < a.n_rows; r += n) {
+    const int32_t b = s.begin[r];
+    a.row_begin[r] = b;
+    a.len_out[r] = s.kept[r] + (s.begin[r + 1] - b);
+  }
+  if (t == 0) {
+    a.row_begin[a.n_rows] = s.begin[a.n_rows];
+    a.count_out[0] = s.head[1];
+  }
+}
+
+// Request q's returned pages onto the stack, by n threads.
+ECHO_DEV void return_row(const PageArgs &a, const PagePlan &s, int q, int t, int n) {
+  const int32_t b = s.back[q], cnt = s.back[q + 1] - b;
+  int32_t *dst = a.free_list + (s.head[0] - s.back[a.n_rows] + b);
+  const int32_t *src = a.page_table + static_cast<int64_t>(q) * a.max_pages;
+  for (int i = t; i < cnt; i += n) dst[i] = src[i];
+}
+// The same for all requests by one workgroup, a wave per request: 64 requests are looked at together.
+ECHO_DEV void return_rows(const PageArgs &a, const PagePlan &s) {
+  constexpr int NW = PT / 64;
+  const int l = lane_id();
+  for (int r0 = threadIdx.x >> 6; r0 < a.n_rows; r0 += 64 * NW) {
+    const int r = r0 + l * NW;
+    uint64_t some = __ballot(r < a.n_rows && s.back[r + 1] > s.back[r]);
+    while (some) {
+      return_row(a, s, r0 + (__ffsll(static_cast<unsigned long long>(some)) - 1) * NW, l, 64);
+      some &= some - 1;
+    }
+  }
 }
 
 // The last request of [lo, hi) whose first token is <= t; begin[lo] <= t < begin[hi].
@@ -157,21 +201,14 @@ ECHO_DEV int find_row(const int32_t *begin, int lo, int hi, int32_t t) {
   return lo;
 }
 
-// Maps token t of the step (request r), and writes the table entry of a page that starts here.
-ECHO_DEV void map_token(const PageArgs &a, const PageSums &s, const int32_t *begin, int32_t top, int r, int32_t t) {
-  const int32_t b = begin[r], fresh = begin[r + 1] - b;
-  const int32_t end = a.len_out[r], pos = end - fresh + (t - b);
-  const int32_t page = pos >> a.shift, in_page = pos & ((1 << a.shift) - 1);
-  const int32_t up = (1 << a.shift) - 1;
-  const int32_t old = static_cast<int32_t>((static_cast<int64_t>(end - fresh) + up) >> a.shift);
+// Maps token t of the step (request r), and writes the table entry of a page that starts with it.
+ECHO_DEV void map_token(const PageArgs &a, const PagePlan &s, int r, int32_t t) {
+  const int32_t kept = s.kept[r], pos = kept + (t - s.begin[r]);
+  const int32_t up = (1 << a.shift) - 1, page = pos >> a.shift, in_page = pos & up;
+  const int32_t old = static_cast<int32_t>((static_cast<int64_t>(kept) + up) >> a.shift);
   int32_t *entry = a.page_table + static_cast<int64_t>(r) * a.max_pages + page;
-  int32_t id;
-  if (page < old) {
-    id = *entry;
-  } else {
-    id = a.free_list[top - 1 - (s.need[r] + page - old)];
-    if (in_page == 0) *entry = id;
-  }
+  const int32_t id = page < old ? *entry : a.free_list[s.head[0] - 1 - (s.need[r] + page - old)];
+  if (page >= old && in_page == 0) *entry = id;
   a.slot[t] = (static_cast<int64_t>(id) << a.shift) + in_page;
   if (a.row) a.row[t] = r;
   a.pos[t] = pos;
@@ -183,52 +220,68 @@ ECHO_DEV void map_none(const PageArgs &a, int32_t t) {
   a.pos[t] = -1;
 }
 
+constexpr int PG_PER = PG_ONE_ROWS / PT;
+
 __global__ __launch_bounds__(PT) void page_step_kernel(PageArgs a) {
-  __shared__ int32_t back[PG_ONE_ROWS + 1];
-  __shared__ int32_t need[PG_ONE_ROWS + 1];
-  __shared__ int32_t begin[PG_ONE_ROWS + 1];
-  __shared__ int32_t head[2];
+  __shared__ int32_t plan[4 * (PG_ONE_ROWS + 1) + PLAN_HEAD];
   __shared__ uint32_t tmp[4 * (PT / 64)];
-  const PageSums s = {back, need, head};
+  const PagePlan s = plan_at(plan, a.n_rows);
   const int tid = threadIdx.x;
-  page_sums(a, s, begin, tmp);
-  const int32_t top = head[0], total = head[1];
-  if (back[a.n_rows] > 0) {                    // a wave per request with pages to return
-    const int32_t first_free = top - back[a.n_rows];
-    for (int r = tid >> 6; r < a.n_rows; r += PT / 64) return_pages(a, s, first_free, r, tid & 63, 64);
-  }
+  make_plan<PG_PER>(a, s, tmp, true);
+  publish(a, s, tid, PT);
+  if (s.back[a.n_rows] > 0) return_rows(a, s);
   __syncthreads();                             // returned pages may be handed out again
+  const int32_t total = s.begin[a.n_rows];
   for (int32_t t = tid; t < a.max_new; t += PT) {
-    if (t < total) map_token(a, s, begin, top, find_row(begin, 0, a.n_rows, t), t);
+    if (t < total) map_token(a, s, find_row(s.begin, 0, a.n_rows, t), t);
     else map_none(a, t);
   }
 }
 
-__global__ __launch_bounds__(PT) void page_sums_kernel(PageArgs a, PageSums s) {
+// Up to PG_ONE_ROWS requests: every workgroup makes the plan in its LDS and returns its share of the
+// pages; the first one writes the plan out.  Nothing that another workgroup reads is written.
+__global__ __launch_bounds__(PT) void page_plan_kernel(PageArgs a, int32_t *ws) {
+  __shared__ int32_t plan[4 * (PG_ONE_ROWS + 1) + PLAN_HEAD];
   __shared__ uint32_t tmp[4 * (PT / 64)];
-  page_sums(a, s, a.row_begin, tmp);
+  const PagePlan s = plan_at(plan, a.n_rows);
+  make_plan<PG_PER>(a, s, tmp, blockIdx.x == 0);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < 4 * (a.n_rows + 1) + 2; i += PT) ws[i] = plan[i];
+  if (s.back[a.n_rows] > 0)
+    for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) return_row(a, s, r, threadIdx.x, PT);
 }
 
-__global__ __launch_bounds__(PF_T) void page_return_kernel(PageArgs a, PageSums s) {
-  const int32_t first_free = s.head[0] - s.back[a.n_rows];
-  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x)
-    return_pages(a, s, first_free, r, threadIdx.x, PF_T);
+// More requests: one workgroup, the plan in the workspace.
+__global__ __launch_bounds__(PT) void page_plan_many_kernel(PageArgs a, int32_t *ws) {
+  __shared__ uint32_t tmp[4 * (PT / 64)];
+  const PagePlan s = plan_at(ws, a.n_rows);
+  make_plan<0>(a, s, tmp, true);
+  if (s.back[a.n_rows] > 0) return_rows(a, s);
 }
 
-// One token per lane.  The requests of a wave's 64 tokens lie between those of its first and last
-// token, found first (all lanes alike); a wave inside one request, the usual case of a prefill,
-// searches no further.
-__global__ __launch_bounds__(PF_T) void page_fill_kernel(PageArgs a, PageSums s) {
-  const int32_t top = s.head[0], total = s.head[1];
-  const int64_t t64 = static_cast<int64_t>(blockIdx.x) * PF_T + threadIdx.x;
-  const int64_t w0 = t64 - lane_id();
-  if (t64 >= a.max_new) return;
-  const int32_t t = static_cast<int32_t>(t64);
-  if (t >= total) { map_none(a, t); return; }
-  const int32_t last = static_cast<int32_t>(min(w0 + 63, static_cast<int64_t>(total) - 1));
-  const int lo = find_row(a.row_begin, 0, a.n_rows, static_cast<int32_t>(w0));
-  const int hi = find_row(a.row_begin, lo, a.n_rows, last);
-  map_token(a, s, a.row_begin, top, find_row(a.row_begin, lo, hi + 1, t), t);
+// One token per lane (four of them, their loads together, took 8.1 us where one takes 5.5).  The
+// requests of a wave's 64 tokens lie between those of its first and last token, found first (all
+// lanes alike); a wave inside one request, the usual case of a prefill, searches no further.  LDS:
+// with a copy of the plan in LDS.  The last workgroup publishes the lengths.
+template <bool LDS>
+__global__ __launch_bounds__(PF_T) void page_fill_kernel(PageArgs a, int32_t *ws) {
+  __shared__ int32_t copy[LDS ? 4 * (PG_ONE_ROWS + 1) + PLAN_HEAD : 1];
+  if (LDS) {
+    for (int i = threadIdx.x; i < 4 * (a.n_rows + 1) + 2; i += PF_T) copy[i] = ws[i];
+    __syncthreads();
+  }
+  const PagePlan s = plan_at(LDS ? copy : ws, a.n_rows);
+  if (blockIdx.x == gridDim.x - 1) { publish(a, s, threadIdx.x, PF_T); return; }
+  const int32_t total = s.begin[a.n_rows];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * PF_T + threadIdx.x, w0 = t - lane_id();
+  if (t < total) {
+    const int32_t last = static_cast<int32_t>(min(w0 + 63, static_cast<int64_t>(total) - 1));
+    const int lo = find_row(s.begin, 0, a.n_rows, static_cast<int32_t>(w0));
+    const int hi = find_row(s.begin, lo, a.n_rows, last);
+    map_token(a, s, find_row(s.begin, lo, hi + 1, static_cast<int32_t>(t)), static_cast<int32_t>(t));
+  } else if (t < a.max_new) {
+    map_none(a, static_cast<int32_t>(t));
+  }
 }
 
 }  // namespace echo
@@ -238,7 +291,7 @@ using namespace echo;
 extern "C" size_t echo_page_workspace_bytes(int32_t n_rows, int32_t max_new) {
   (void)max_new;
   if (n_rows < 0) return 0;
-  return sizeof(int32_t) * (2 * (static_cast<size_t>(n_rows) + 1) + 2);
+  return sizeof(int32_t) * (4 * (static_cast<size_t>(n_rows) + 1) + PLAN_HEAD);
 }
 
 extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes, void *stream) {
@@ -265,9 +318,14 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
     return fail(ECHO_EWORKSPACE, "echo_page_step: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
                 echo_page_workspace_bytes(p->n_rows, p->max_new));
   int32_t *w = static_cast<int32_t *>(ws);
-  const PageSums s = {w, w + p->n_rows + 1, w + 2 * (p->n_rows + 1)};
-  page_sums_kernel<<<1, PT, 0, st>>>(a, s);
-  if (p->done && p->n_rows) page_return_kernel<<<min(p->n_rows, 1024), PF_T, 0, st>>>(a, s);
-  if (p->max_new) page_fill_kernel<<<(static_cast<uint32_t>(p->max_new) + PF_T - 1) / PF_T, PF_T, 0, st>>>(a, s);
+  const bool lds = p->n_rows <= PG_ONE_ROWS;
+  if (lds)
+    page_plan_kernel<<<p->done ? max(1, min(p->n_rows, 64)) : 1, PT, 0, st>>>(a, w);
+  else
+    page_plan_many_kernel<<<1, PT, 0, st>>>(a, w);
+  // one workgroup more than the tokens take publishes the lengths
+  const uint32_t fill = static_cast<uint32_t>((static_cast<int64_t>(p->max_new) + PF_T - 1) / PF_T) + 1;
+  if (lds) page_fill_kernel<true><<<fill, PF_T, 0, st>>>(a, w);
+  else page_fill_kernel<false><<<fill, PF_T, 0, st>>>(a, w);
   return check_launch("page_step");
 }

@@ -95,6 +95,7 @@ def transform(src):
     src = src.replace("#include <hip/hip_runtime.h>", '#include "hip_cpu.h"')
     src = src.replace("__builtin_amdgcn_", "emu_amdgcn_")
     src = src.replace("__builtin_nontemporal_load", "emu_nontemporal_load")
+    src = src.replace("__builtin_nontemporal_store", "emu_nontemporal_store")
     src = re.sub(r"__attribute__\(\(address_space\(\d\)\)\)", "", src)
     src = PIN.sub("((void)0);", src)
     src = SHARED.sub(lambda m: "static %s%s%s; static const bool %s_emu_lds = "

@@ -106,6 +106,7 @@ template <typename T> inline T atomicCAS(T *p, T expected, T v) {
 }
 
 template <typename T> inline T emu_nontemporal_load(const T *p) { return *p; }
+template <typename T> inline void emu_nontemporal_store(T v, T *p) { *p = v; }
 
 // ---- wave intrinsics
 unsigned long long __ballot(bool pred);
