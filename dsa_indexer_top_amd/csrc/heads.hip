@@ -94,6 +94,8 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
   Raw8<T> raw[HU];
   int32_t pos[HU];
   bool live[HU];
+  float w[HU];                                       // FP8: the head's weight, or the key's row
+  int64_t slot[HU];
 #pragma unroll
   for (int u = 0; u < HU; ++u) {
     const int32_t t = tok + u * tok_step, h = head + u * head_step;
@@ -101,6 +103,10 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
     pos[u] = ONE ? a.pos[t] : in ? a.pos[t] : -1;
     raw[u] = in && in_row ? load8(static_cast<const T *>(s.x) + t * s.xt + (h * s.xh + j * VEC)) : zero8<T>();
     live[u] = in && pos[u] >= 0 && pos[u] < a.n_pos;
+    if (FP8) {                                       // here, or each would be one more round trip at the end
+      w[u] = in && !is_k ? a.f.w[t * a.f.wt + h] : 0.f;
+      slot[u] = in && is_k ? a.f.slot[t] : -1;
+    }
   }
   float wt[VEC], bi[VEC];
 #pragma unroll
@@ -179,12 +185,11 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
       // 8 bytes a lane: past the caches a prefill chunk's codes leave faster (32768 tokens: 175.6 us
       // with plain stores, 165.7 with these)
       __builtin_nontemporal_store(code, reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC));
-      if (j == 0) a.f.w_out[row] = a.f.w[t * a.f.wt + h] * sc.scale * a.f.w_mul;
+      if (j == 0) a.f.w_out[row] = w[u] * sc.scale * a.f.w_mul;
     } else {
-      const int64_t slot = a.f.slot[t];
-      if (slot < 0 || slot >= a.f.n_slots) continue;
-      *reinterpret_cast<u32x2 *>(a.f.k_cache + slot * D + j * VEC) = code;
-      if (j == 0) a.f.k_scale[slot] = sc.scale;
+      if (slot[u] < 0 || slot[u] >= a.f.n_slots) continue;
+      *reinterpret_cast<u32x2 *>(a.f.k_cache + slot[u] * D + j * VEC) = code;
+      if (j == 0) a.f.k_scale[slot[u]] = sc.scale;
     }
   }
 }
