@@ -375,3 +375,78 @@ class PrefillChunkRunner:
 
     def close(self):
         self.host_buf.close()
+
+
+class PagedIndexerRunner:
+    """The indexer over a paged key cache from hidden states on: page tables and free pages on the
+    device, the projections' FP8 weights, the cache, and one step's buffers for up to max_new tokens.
+    step() enqueues, on one stream and without looking at a length on the host: the step's page maps;
+    the hidden states to FP8 and through the key, head-weight and query projections; the key's layer
+    norm, both rotations and the FP8 forms, the keys going to their pages.  score() then scores
+    every request's newest query against its pages and selects its top-k, for a step that gave each
+    request one token.  Weights are (codes, scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden],
+    ww [64, hidden].  No arithmetic of the method lives here."""
+
+    def __init__(self, n_rows, page_size, max_pages, n_pages, max_new, topk, wq, wk, ww, cos_sin,
+                 k_weight, k_bias, w_mul, eps=1e-6, interleaved=False):
+        import torch
+        dev, i32, u8, f32, bf16 = "cuda", torch.int32, torch.uint8, torch.float32, torch.bfloat16
+        self.wq, self.wk, self.ww = wq, wk, ww
+        self.cos_sin, self.k_weight, self.k_bias = cos_sin, k_weight, k_bias
+        self.page_size, self.topk, self.w_mul, self.eps, self.interleaved = page_size, topk, w_mul, eps, interleaved
+        self.n_rows, self.max_len = n_rows, max_pages * page_size
+        # the cache and who holds its pages
+        self.lens = torch.zeros(n_rows, dtype=i32, device=dev)
+        self.table = torch.zeros((n_rows, max_pages), dtype=i32, device=dev)
+        self.free = torch.arange(n_pages, dtype=i32, device=dev)
+        self.count = torch.full((1,), n_pages, dtype=i32, device=dev)
+        self.status = torch.zeros(1, dtype=i32, device=dev)
+        self.k = torch.zeros((n_pages * page_size, 128), dtype=u8, device=dev)
+        self.k_scale = torch.zeros(n_pages * page_size, dtype=f32, device=dev)
+        # one step
+        self.new_len = torch.zeros(n_rows, dtype=i32, device=dev)
+        self.done = torch.zeros(n_rows, dtype=u8, device=dev)
+        self.row_begin = torch.empty(n_rows + 1, dtype=i32, device=dev)
+        self.slot = torch.empty(max_new, dtype=torch.int64, device=dev)
+        self.row = torch.empty(max_new, dtype=i32, device=dev)
+        self.pos = torch.empty(max_new, dtype=i32, device=dev)
+        self.ws = torch.empty(B.page_workspace_bytes(n_rows, max_new), dtype=u8, device=dev)
+        hid, q_hid = wk[0].shape[1], wq[0].shape[1]
+        self.x = torch.zeros((max_new, hid), dtype=bf16, device=dev)
+        self.xq = torch.zeros((max_new, q_hid), dtype=bf16, device=dev)
+        codes = lambda n: torch.empty((max_new, -(-n // 16) * 16), dtype=u8, device=dev)[:, :n]
+        scales = lambda n: torch.empty((-(-n // 128), max_new), dtype=f32, device=dev).t()
+        self.x8, self.xs = codes(hid), scales(hid)
+        self.xq8, self.xqs = codes(q_hid), scales(q_hid)
+        self.q = torch.empty((max_new, 64 * 128), dtype=bf16, device=dev)
+        self.kk = torch.empty((max_new, 128), dtype=bf16, device=dev)
+        self.w = torch.empty((max_new, 64), dtype=f32, device=dev)
+        self.q8 = torch.empty((max_new, 64, 128), dtype=u8, device=dev)
+        self.w_out = torch.empty((max_new, 64), dtype=f32, device=dev)
+        self.scores = torch.empty((n_rows, self.max_len), dtype=f32, device=dev)
+        self.idx = torch.empty((n_rows, topk), dtype=i32, device=dev)
+        self.ws_topk = torch.empty(max(B.topk_workspace_bytes(n_rows, self.max_len), 256), dtype=u8, device=dev)
+
+    def step(self, stream=None):
+        """One step of the requests' new_len tokens (x and xq hold their states in request order),
+        after the requests flagged in done gave back their pages."""
+        B.page_step(self.lens, self.new_len, self.table, self.page_size, self.free, self.count, self.lens,
+                    self.count, self.row_begin, self.slot, self.row, self.pos, self.status, self.ws,
+                    done=self.done, stream=stream)
+        B.quant_fp8(self.x, self.x8, self.xs, stream=stream)
+        B.quant_fp8(self.xq, self.xq8, self.xqs, stream=stream)
+        B.matmul_fp8(self.x8, self.xs, *self.wk, self.kk, stream=stream)
+        B.matmul_fp8(self.x8, self.xs, *self.ww, self.w, stream=stream)
+        B.matmul_fp8(self.xq8, self.xqs, *self.wq, self.q, stream=stream)
+        n = self.q.shape[0]
+        B.indexer_qk(self.q.view(n, 64, 128), self.kk.view(n, 1, 128), self.w, self.q8, self.w_out, self.k,
+                     self.k_scale, self.slot, self.pos, self.cos_sin, w_mul=self.w_mul,
+                     interleaved=self.interleaved, k_norm=B.NORM_LAYER, k_weight=self.k_weight,
+                     k_bias=self.k_bias, eps=self.eps, stream=stream)
+
+    def score(self, stream=None):
+        """Scores and top-k of the step's queries, one per request."""
+        r = self.n_rows
+        B.index_scores_paged(self.q8[:r], self.w_out[:r], self.k, self.k_scale, self.table, self.page_size,
+                             self.lens, self.max_len, self.scores, stream=stream)
+        B.topk(self.scores, self.lens, self.max_len, self.topk, self.idx, self.ws_topk, stream=stream)

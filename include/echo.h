@@ -645,8 +645,9 @@ int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols
  * 16 and every row, the last too, is readable up to k rounded up to 16; what stands behind k is
  * ignored.  c must not overlap an input.  The result does not depend on what runs beside it: no
  * atomics, no workspace.  m = 0 or n = 0: ECHO_OK; k = 0 writes zeros.  ECHO_EINVAL for negative
- * sizes, NULL pointers, an unknown type, lda or ldb below k, ldc below n; ECHO_EUNSUPPORTED for
- * other alignments or more than 2^31 - 1 output tiles.
+ * sizes, NULL pointers, an unknown type, lda or ldb below k, ldc below n, c not aligned to its type;
+ * ECHO_EUNSUPPORTED for other alignments, lda, ldb or as_row above 2^22, negative scale strides, and
+ * sizes beyond the grid (n, m or k near 2^31, 2^28 output tiles of 128 x 128).
  */
 int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t as_row, int64_t as_blk,
                     const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk, int32_t m,

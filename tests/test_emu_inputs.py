@@ -12,7 +12,8 @@ from test_emu_kernels import ASAN, ROOT, TSAN, _run_selection, build_emu
 
 pytestmark = pytest.mark.skipif(ASAN is None, reason="clang AddressSanitizer runtime not found")
 
-SELECTION = ["tests/test_gpu_pages.py", "tests/test_gpu_blockfp8.py", "tests/test_gpu_heads.py"]
+SELECTION = ["tests/test_gpu_pages.py", "tests/test_gpu_blockfp8.py", "tests/test_gpu_heads.py", "tests/test_gpu_inputs.py",
+             "-k", "not full"]
 
 
 def _passed(text):
