@@ -8,7 +8,6 @@ used only to hold device memory and to name streams.  If the library is missing 
 
 import ctypes as C
 import os
-import struct
 
 import torch
 
@@ -105,12 +104,12 @@ _SIGS = {
     "echo_graph_launch": (C.c_int, [P, P]),
     "echo_graph_destroy": (C.c_int, [P]),
     "echo_page_workspace_bytes": (SZ, [I32, I32]),
-    "echo_page_step": (C.c_int, [C.c_char_p, P, SZ, P]),
+    "echo_page_step": (C.c_int, [P, P, SZ, P]),
     "echo_quant_fp8": (C.c_int, [P, I32, I64, I32, I64, P, I64, P, I64, I64, P]),
     "echo_matmul_fp8": (C.c_int, [P, I64, P, I64, I64, P, I64, P, I64, I64, I32, I32, I32, P, I64,
                                   I32, P]),
-    "echo_qk_norm_rope": (C.c_int, [C.c_char_p, P, I64, I64, P, I64, I64, P]),
-    "echo_indexer_qk": (C.c_int, [C.c_char_p, P, I64, F32, P, P, P, P, P, I64, P]),
+    "echo_qk_norm_rope": (C.c_int, [P, P, I64, I64, P, I64, I64, P]),
+    "echo_indexer_qk": (C.c_int, [P, P, I64, F32, P, P, P, P, P, I64, P]),
     "echo_host_alloc": (C.c_int, [SZ, C.c_int, C.POINTER(P), C.POINTER(P)]),
     "echo_host_free": (C.c_int, [P]),
 }
@@ -340,58 +339,29 @@ def step_advance(step_dev, stream=None):
 
 
 # ---------------------------------------------------------------- before the scores
-# The calls below take tensors whole, so their types, shapes, strides and device are checked here
-# before anything is enqueued (ECHO_EINVAL); the rest of the checks are the library's.  A step of a
-# few tokens runs in about the time this takes, so what is right is found out in one expression and
-# only what is wrong is looked at again for its message.
-DEVICE_TYPE = "cuda"
-_PAGE = struct.Struct("=5i4x13Q")         # echo_page_args
-_QK = struct.Struct("=11if2Q4q6Q")        # echo_qk_args
-_F8 = (torch.uint8, torch.float8_e4m3fn)
-_FLOATS = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The calls below take tensors whole: native/tensor_calls.cpp checks their types, shapes, strides and
+# device (ECHO_EINVAL before anything is enqueued) and calls the library, since a step of a few
+# tokens runs in about the time that the same checks would take here.
+DEVICE_TYPE = "cuda"                     # where tensors have to be; anything else: not checked
+
+_tensor_calls = None
 
 
-def _refuse(fn, what):
-    raise EchoError(fn, ECHO_EINVAL, what)
+def _calls():
+    """The native module, set up with this library's functions; raises if it has not been built."""
+    global _tensor_calls
+    if _tensor_calls is None:
+        from . import _tensor_calls as m
+        L = lib()
+        m.setup(EchoError, torch._C._cuda_getCurrentRawStream if DEVICE_TYPE == "cuda" else (lambda dev: 0),
+                *(C.cast(getattr(L, "echo_" + n), P).value for n in (
+                    "last_error", "page_step", "quant_fp8", "matmul_fp8", "qk_norm_rope", "indexer_qk")))
+        _tensor_calls = m
+    return _tensor_calls
 
 
-def _stream_on(fn, stream, dev):
-    """The stream's handle, for tensors of device `dev`, which has to be the current one."""
-    if DEVICE_TYPE == "cuda":
-        cur = torch.cuda.current_device()
-        if dev != cur:
-            _refuse(fn, "tensors on device %d; the current device is cuda:%d" % (dev, cur))
-        if stream is None and _raw_stream is not None:
-            return _raw_stream(cur)
-    return stream_handle(stream)
-
-
-def _explain(fn, dev, want):
-    """Refuses the first tensor that is not what (name, tensor, types, shape) says: contiguous (of
-    that shape where one is given), of one of the types, on device `dev`."""
-    for name, t, dtypes, shape in want:
-        if t is None:
-            continue
-        if t.dtype not in dtypes:
-            _refuse(fn, "%s is %s, not %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-        if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-            _refuse(fn, "%s is not a contiguous tensor%s" % (name, "" if shape is None else " of shape %s" % (shape,)))
-        if t.get_device() != dev:
-            _refuse(fn, "%s is on another device than the first tensor" % name)
-    _refuse(fn, "a tensor does not match the others")
-
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _row_stride(fn, name, t, rows, cols):
-    """Row stride of a [rows, cols] matrix whose rows are contiguous."""
-    row, col = t.stride()
-    if col != 1 and cols > 1:
-        _refuse(fn, "the rows of %s are not contiguous" % name)
-    return row if rows > 1 else max(row, cols)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def page_workspace_bytes(n_rows, max_new):
@@ -402,131 +372,19 @@ def page_step(len_in, new_len, page_table, page_size, free_list, count_in, len_o
               row_begin, slot, row, pos, status, ws, done=None, stream=None):
     """One step of a paged cache's tables and maps (echo_page_step); ws may be None for a step
     that needs no workspace, done and row may be None."""
-    fn, i32 = "echo_page_step", torch.int32
-    n, cap, dev = len_in.numel(), slot.numel(), len_in.get_device()
-    if not (len_in.dtype is i32 and new_len.dtype is i32 and len_out.dtype is i32 and row_begin.dtype is i32
-            and pos.dtype is i32 and count_in.dtype is i32 and count_out.dtype is i32 and status.dtype is i32
-            and free_list.dtype is i32 and page_table.dtype is i32 and slot.dtype is torch.int64
-            and new_len.numel() == n and len_out.numel() == n and row_begin.numel() == n + 1
-            and pos.numel() == cap and count_in.numel() == 1 and count_out.numel() == 1
-            and status.numel() == 1 and page_table.dim() == 2 and page_table.shape[0] == n
-            and len_in.is_contiguous() and new_len.is_contiguous() and len_out.is_contiguous()
-            and row_begin.is_contiguous() and pos.is_contiguous() and slot.is_contiguous()
-            and free_list.is_contiguous() and page_table.is_contiguous()
-            and dev == new_len.get_device() == page_table.get_device() == free_list.get_device()
-            == count_in.get_device() == len_out.get_device() == count_out.get_device()
-            == row_begin.get_device() == slot.get_device() == pos.get_device() == status.get_device()
-            and (row is None or (row.dtype is i32 and row.shape == pos.shape and row.is_contiguous()
-                                 and row.get_device() == dev))
-            and (done is None or (done.dtype in (torch.uint8, torch.bool) and done.shape == len_in.shape
-                                  and done.is_contiguous() and done.get_device() == dev))
-            and (ws is None or (ws.is_contiguous() and ws.get_device() == dev))):
-        width = page_table.shape[1] if page_table.dim() == 2 else 0
-        _explain(fn, dev, (
-            ("len_in", len_in, (i32,), (n,)), ("new_len", new_len, (i32,), (n,)),
-            ("page_table", page_table, (i32,), (n, width)), ("free_list", free_list, (i32,), None),
-            ("count_in", count_in, (i32,), (1,)), ("len_out", len_out, (i32,), (n,)),
-            ("count_out", count_out, (i32,), (1,)), ("row_begin", row_begin, (i32,), (n + 1,)),
-            ("slot", slot, (torch.int64,), (cap,)), ("row", row, (i32,), (cap,)), ("pos", pos, (i32,), (cap,)),
-            ("status", status, (i32,), (1,)), ("done", done, (torch.uint8, torch.bool), (n,)),
-            ("ws", ws, () if ws is None else (ws.dtype,), None)))
-    st = _stream_on(fn, stream, dev)
-    a = _PAGE.pack(n, page_size, page_table.shape[1], free_list.numel(), cap, len_in.data_ptr(),
-                   new_len.data_ptr(), _ptr(done), page_table.data_ptr(), free_list.data_ptr(),
-                   count_in.data_ptr(), len_out.data_ptr(), count_out.data_ptr(), row_begin.data_ptr(),
-                   slot.data_ptr(), _ptr(row), pos.data_ptr(), status.data_ptr())
-    _check(fn, lib().echo_page_step(a, _ptr(ws), 0 if ws is None else ws.nbytes, st))
+    _calls().page_step(len_in, new_len, page_table, page_size, free_list, count_in, len_out, count_out,
+                       row_begin, slot, row, pos, status, ws, done, _handle(stream), DEVICE_TYPE != "cuda")
 
 
 def quant_fp8(x, y, scale, stream=None):
     """FP8 codes y and scales [rows, ceil(cols / 128)] (any strides) of a matrix x."""
-    fn = "echo_quant_fp8"
-    kind, dev = _FLOATS.get(x.dtype), x.get_device()
-    if kind is None or x.dim() != 2:
-        _refuse(fn, "x is not a matrix of bf16, fp16 or fp32")
-    rows, cols = x.shape
-    if y.shape != x.shape or scale.shape != (rows, (cols + 127) // 128):
-        _refuse(fn, "shapes %s, %s, %s" % (tuple(x.shape), tuple(y.shape), tuple(scale.shape)))
-    if y.dtype not in _F8 or scale.dtype is not torch.float32:
-        _refuse(fn, "y is not FP8 codes or scale not fp32")
-    if dev != y.get_device() or dev != scale.get_device():
-        _refuse(fn, "x, y and scale are on different devices")
-    s0, s1 = scale.stride()
-    st = _stream_on(fn, stream, dev)
-    _check(fn, lib().echo_quant_fp8(x.data_ptr(), kind, rows, cols, _row_stride(fn, "x", x, rows, cols), y.data_ptr(),
-                                    _row_stride(fn, "y", y, rows, cols), scale.data_ptr(), s0, s1, st))
-
-
-def _codes(fn, name, t, rows, k):
-    """Row stride of a matrix of FP8 codes whose rows are read in 16-byte pieces."""
-    if t.dtype not in _F8:
-        _refuse(fn, "%s is %s, not FP8 codes" % (name, t.dtype))
-    ld = _row_stride(fn, name, t, rows, k)
-    if rows < 2:
-        ld = (ld + 15) // 16 * 16          # of no row's distance from another
-    if k % 16 and rows and t.untyped_storage().nbytes() - t.storage_offset() < (rows - 1) * ld + (k + 15) // 16 * 16:
-        _refuse(fn, "the last row of %s ends inside a 16-byte piece" % name)
-    return ld
+    _calls().quant_fp8(x, y, scale, _handle(stream), DEVICE_TYPE != "cuda")
 
 
 def matmul_fp8(a, a_scale, b, b_scale, c, stream=None):
     """c [m, n] = a [m, k] times b [n, k] transposed, FP8 codes with fp32 scales: a_scale [m,
     ceil(k / 128)] and b_scale [ceil(n / 128), ceil(k / 128)], any strides."""
-    fn = "echo_matmul_fp8"
-    if a.dim() != 2 or b.dim() != 2 or c.dim() != 2:
-        _refuse(fn, "a, b and c are matrices")
-    m, k = a.shape
-    n, kb = b.shape
-    dev, kind, nb = a.get_device(), _FLOATS.get(c.dtype), (k + 127) // 128
-    if kb != k or c.shape != (m, n) or a_scale.shape != (m, nb) or b_scale.shape != ((n + 127) // 128, nb):
-        _refuse(fn, "shapes %s" % (tuple(tuple(t.shape) for t in (a, a_scale, b, b_scale, c)),))
-    if kind is None or a_scale.dtype is not torch.float32 or b_scale.dtype is not torch.float32:
-        _refuse(fn, "c is not bf16, fp16 or fp32, or a scale not fp32")
-    if not dev == a_scale.get_device() == b.get_device() == b_scale.get_device() == c.get_device():
-        _refuse(fn, "tensors on different devices")
-    ar, ab = a_scale.stride()
-    br, bb = b_scale.stride()
-    st = _stream_on(fn, stream, dev)
-    _check(fn, lib().echo_matmul_fp8(a.data_ptr(), _codes(fn, "a", a, m, k), a_scale.data_ptr(), ar, ab, b.data_ptr(),
-                                     _codes(fn, "b", b, n, k), b_scale.data_ptr(), br, bb, m, n, k, c.data_ptr(),
-                                     _row_stride(fn, "c", c, m, n), kind, st))
-
-
-def _heads_strides(fn, name, t):
-    """Strides of tokens and heads; the stride of a dimension of one means nothing."""
-    tok, head, one = t.stride()
-    n, h, d = t.shape
-    if one != 1 and d > 1 and n and h:
-        _refuse(fn, "the heads of %s are not contiguous" % name)
-    return tok if n > 1 else 0, head if h > 1 else 0
-
-
-def _qk_args(fn, dev, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias, k_norm,
-             k_weight, k_bias):
-    """The packed echo_qk_args, the types, shapes and devices of its tensors checked."""
-    kind, f32 = _FLOATS.get(q.dtype), torch.float32
-    if kind is None or k.dtype is not q.dtype or q.dim() != 3 or k.dim() != 3:
-        _refuse(fn, "q and k are not [tokens, heads, head_dim] of one type, bf16, fp16 or fp32")
-    n, hq, dim = q.shape
-    nk, hk, dk = k.shape
-    if nk != n or dk != dim:
-        _refuse(fn, "q and k have other numbers of tokens or other head sizes")
-    if not (pos.dtype is torch.int32 and pos.dim() == 1 and pos.numel() == n and pos.is_contiguous()
-            and dev == k.get_device() == pos.get_device()):
-        _explain(fn, dev, (("pos", pos, (torch.int32,), (n,)),))
-    n_pos, rot = INF, 0
-    if cos_sin is not None:
-        if not (cos_sin.dtype is f32 and cos_sin.dim() == 2 and cos_sin.is_contiguous() and cos_sin.get_device() == dev):
-            _explain(fn, dev, (("cos_sin", cos_sin, (f32,), None),))
-        n_pos, rot = cos_sin.shape
-    for name, t in (("q_weight", q_weight), ("q_bias", q_bias), ("k_weight", k_weight), ("k_bias", k_bias)):
-        if t is not None and not (t.dtype is f32 and t.numel() == dim and t.is_contiguous() and t.get_device() == dev):
-            _explain(fn, dev, ((name, t, (f32,), (dim,)),))
-    qt, qh = _heads_strides(fn, "q", q)
-    kt, kh = _heads_strides(fn, "k", k)
-    return _QK.pack(n, hq, hk, dim, kind, q_norm, k_norm, rot_begin, rot, 1 if interleaved else 0, n_pos, eps,
-                    q.data_ptr(), k.data_ptr(), qt, qh, kt, kh, _ptr(q_weight), _ptr(q_bias), _ptr(k_weight),
-                    _ptr(k_bias), pos.data_ptr(), _ptr(cos_sin))
+    _calls().matmul_fp8(a, a_scale, b, b_scale, c, _handle(stream), DEVICE_TYPE != "cuda")
 
 
 def qk_norm_rope(q, k, q_out, k_out, pos, cos_sin, rot_begin=0, interleaved=False, q_norm=NORM_NONE,
@@ -534,17 +392,8 @@ def qk_norm_rope(q, k, q_out, k_out, pos, cos_sin, rot_begin=0, interleaved=Fals
                  stream=None):
     """Norms and rotation of query and key heads [tokens, heads, head_dim], any strides of tokens
     and heads; the rotated part has cos_sin's width.  q_out / k_out may be q / k."""
-    fn = "echo_qk_norm_rope"
-    dev = q.get_device()
-    a = _qk_args(fn, dev, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias,
-                 k_norm, k_weight, k_bias)
-    if not (q_out.shape == q.shape and k_out.shape == k.shape and q_out.dtype is q.dtype
-            and k_out.dtype is q.dtype and dev == q_out.get_device() == k_out.get_device()):
-        _refuse(fn, "q_out or k_out does not match its input")
-    qt, qh = _heads_strides(fn, "q_out", q_out)
-    kt, kh = _heads_strides(fn, "k_out", k_out)
-    st = _stream_on(fn, stream, dev)
-    _check(fn, lib().echo_qk_norm_rope(a, q_out.data_ptr(), qt, qh, k_out.data_ptr(), kt, kh, st))
+    _calls().qk_norm_rope(q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias, k_norm,
+                          k_weight, k_bias, _handle(stream), DEVICE_TYPE != "cuda", q_out, k_out)
 
 
 def indexer_qk(q, k, w, q8, w_out, k_cache, k_scale, slot, pos, cos_sin, w_mul=1.0, rot_begin=0,
@@ -553,31 +402,9 @@ def indexer_qk(q, k, w, q8, w_out, k_cache, k_scale, slot, pos, cos_sin, w_mul=1
     """The indexer's inputs from query heads q [tokens, heads, 128], keys k [tokens, 1, 128] and
     head weights w [tokens, heads]: FP8 queries q8, weights w_out with the queries' scales folded
     in, and the keys as rows slot[t] of k_cache [slots, 128] / k_scale [slots]."""
-    fn, f32 = "echo_indexer_qk", torch.float32
-    dev = q.get_device()
-    a = _qk_args(fn, dev, q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias,
-                 k_norm, k_weight, k_bias)
-    n, heads, dim = q.shape
-    slots = k_scale.numel()
-    if not (w.dtype is f32 and w.shape == (n, heads) and q8.dtype in _F8 and q8.shape == q.shape
-            and q8.is_contiguous() and w_out.dtype is f32 and w_out.shape == (n, heads) and w_out.is_contiguous()
-            and k_cache.dtype in _F8 and k_cache.is_contiguous() and k_cache.numel() == slots * dim
-            and k_scale.dtype is f32 and k_scale.is_contiguous() and slot.dtype is torch.int64
-            and slot.dim() == 1 and slot.numel() == n and slot.is_contiguous()
-            and dev == w.get_device() == q8.get_device() == w_out.get_device() == k_cache.get_device()
-            == k_scale.get_device() == slot.get_device()):
-        if k_cache.numel() != slots * dim:
-            _refuse(fn, "k_cache and k_scale hold different numbers of keys")
-        _explain(fn, dev, (
-            ("w", w.contiguous(), (f32,), (n, heads)), ("q8", q8, _F8, (n, heads, dim)),
-            ("w_out", w_out, (f32,), (n, heads)), ("k_cache", k_cache, _F8, None),
-            ("k_scale", k_scale, (f32,), None), ("slot", slot, (torch.int64,), (n,))))
-    wt = w.stride()
-    if wt[1] != 1 and heads > 1:
-        _refuse(fn, "the rows of w are not contiguous")
-    st = _stream_on(fn, stream, dev)
-    _check(fn, lib().echo_indexer_qk(a, w.data_ptr(), wt[0], w_mul, q8.data_ptr(), w_out.data_ptr(),
-                                     k_cache.data_ptr(), k_scale.data_ptr(), slot.data_ptr(), slots, st))
+    _calls().indexer_qk(q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias, k_norm,
+                        k_weight, k_bias, _handle(stream), DEVICE_TYPE != "cuda", w, q8, w_out, k_cache,
+                        k_scale, slot, w_mul)
 
 
 class CapturedGraph:

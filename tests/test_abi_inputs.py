@@ -3,6 +3,7 @@ the library's or the binding's argument checks, or has nothing to do, before the
 touched."""
 
 import os
+import struct
 
 import pytest
 import torch
@@ -15,6 +16,8 @@ pytestmark = [pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="library
               pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only without a GPU")]
 
 F = 0x1000                     # never dereferenced
+PAGE = struct.Struct("=5i4x13Q")          # echo_page_args
+QK = struct.Struct("=11if2Q4q6Q")         # echo_qk_args
 
 
 def err():
@@ -26,7 +29,7 @@ def page_args(**kw):
              free_list=F, count_in=F, len_out=F, count_out=F, row_begin=F, slot=F, row=0, pos=F, status=F)
     assert set(kw) <= set(a)
     a.update(kw)
-    return B._PAGE.pack(*a.values())
+    return PAGE.pack(*a.values())
 
 
 def test_page_step_argument_errors():
@@ -92,7 +95,7 @@ def qk_args(**kw):
              pos=F, cos_sin=F)
     assert set(kw) <= set(a)
     a.update(kw)
-    return B._QK.pack(*a.values())
+    return QK.pack(*a.values())
 
 
 def both_calls():
