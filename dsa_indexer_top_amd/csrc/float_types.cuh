@@ -42,6 +42,16 @@ ECHO_DEV Raw8<T> load8(const T *__restrict__ p) {
     r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p) + i);
   return r;
 }
+// The same from any address the type allows: gfx950 reads 16 bytes at any of them.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+template <typename T>
+ECHO_DEV Raw8<T> load8_any(const T *__restrict__ p) {
+  Raw8<T> r;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) * VEC / 16; ++i) r.w[i] = reinterpret_cast<const u32x4_any *>(p)[i];
+  return r;
+}
 template <typename T>
 ECHO_DEV Raw8<T> zero8() {
   Raw8<T> r;

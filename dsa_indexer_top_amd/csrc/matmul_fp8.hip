@@ -448,6 +448,151 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
       store_c<T>(a, m0 + w.wm + 16 * x + w.j, n0 + w.wn + 16 * y + 4 * w.g, w.acc[x][y]);
 }
 
+// ---------------------------------------------------------------- few tiles
+template <bool V> struct Const { static constexpr bool value = V; };
+
+// 64 x 64 outputs per workgroup, its waves taking the scale blocks in turn: each multiplies whole
+// blocks through LDS stages of its own, so no wave waits for another until the sums are joined at the
+// end, in wave order.  Where no more than one tile falls to a CU this keeps a block in flight for
+// every wave (MI355X: 64 x 1024 x 4096 8.5 us against 12.0 with 64 x 64 tiles whose waves share the
+// stages, 100 x 1000 x 8000 13.3 against 21.2, 77 x 1000 x 1111 in fp32 6.4 against 7.3).
+template <typename T, int SW, int STAGES>
+__global__ __launch_bounds__(SW * 64) void matmul_split_kernel(MatArgs a) {
+  constexpr int MT = 4, NT = 4, SIDE = 64, LOADS = 2 * SIDE / 8 + 1;
+  constexpr int STAGE = 2 * SIDE * 128 + 256;
+  constexpr bool EXACT = sizeof(T) == 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SW][STAGES][STAGE];
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int l = lane_id(), j = l & 15, g = l >> 4;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, (a.m + SIDE - 1) / SIDE, (a.n + SIDE - 1) / SIDE, tm, tn);
+  const int32_t m0 = tm * SIDE, n0 = tn * SIDE;
+  const int nb = (a.k + 127) >> 7, own = nb > wv ? (nb - wv + SW - 1) / SW : 0;    // this wave's blocks
+
+  // a load is 8 rows of 8 pieces; the pieces' exchange alternates between loads
+  uint32_t row[2][SIDE / 8];
+#pragma unroll
+  for (int i = 0; i < SIDE / 8; ++i) {
+    const int r = i * 8 + (l >> 3);
+    row[0][i] = static_cast<uint32_t>(min(r, a.m - 1 - m0)) * static_cast<uint32_t>(a.lda);
+    row[1][i] = static_cast<uint32_t>(min(r, a.n - 1 - n0)) * static_cast<uint32_t>(a.ldb);
+  }
+  const uint32_t sa_off = static_cast<uint32_t>(min(l, a.m - 1 - m0)) * static_cast<uint32_t>(a.as_row);
+  const uint8_t *pa0 = a.a + m0 * a.lda, *pb0 = a.b + n0 * a.ldb;
+  const float *sa = a.sa + m0 * a.as_row, *sb = a.sb + (n0 >> 7) * a.bs_row;
+  const int seg0 = ((l & 7) ^ (l >> 4)) << 4;
+  auto load_one = [&](int t, int i, uint8_t *__restrict__ stage) {
+    if (i < 2 * SIDE / 8) {
+      const int side = i / (SIDE / 8), r = i % (SIDE / 8);
+      const int seg = seg0 ^ ((r & 1) << 6);
+      const uint8_t *p = (side ? pb0 : pa0) + static_cast<int64_t>(t) * 128;
+      __builtin_amdgcn_global_load_lds((glb_void *)(p + (row[side][r] + (seg < a.k - t * 128 ? seg : 0))),
+                                       (lds_void *)(stage + (side * SIDE + r * 8) * 128), 16, 0, 0);
+    } else {
+      __builtin_amdgcn_global_load_lds((glb_void *)(sa + t * a.as_blk + sa_off), (lds_void *)(stage + 2 * SIDE * 128), 4, 0, 0);
+    }
+  };
+  Pieces pa, pb;
+  pa.init(j, g);
+  pb = pa;
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y) acc[x][y] = v4f{0.f, 0.f, 0.f, 0.f};
+  float sbv = 0.f;                                       // weight scales of 64 own blocks, one per lane
+
+  // Own block i (block t) from cur, with MORE own block i + STAGES - 1's loads going to nxt; without, it
+  // may be short.
+  auto block = [&](int i, uint8_t *__restrict__ cur, uint8_t *__restrict__ nxt, auto more) {
+    constexpr bool MORE = decltype(more)::value;
+    const int t = wv + i * SW, left = a.k - t * 128;
+    const float sbt = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sbv), i & 63));
+    float s[MT];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) s[x] = reinterpret_cast<const float *>(cur + 2 * SIDE * 128)[16 * x + j] * sbt;
+    Operand<EXACT> av[MT], bv[2];
+    auto get = [&](Operand<EXACT> &o, const uint8_t *__restrict__ stage, const Pieces &p, int rows16) {
+      v8i v = p.read(stage, rows16);
+      if (!MORE) v = keep_bytes(v, g, left);
+      o.set(v);
+    };
+    get(bv[0], cur + SIDE * 128, pb, 0);
+#pragma unroll
+    for (int x = 0; x < MT; ++x) get(av[x], cur, pa, x);
+    constexpr int AHEAD = 2;
+    v4f c[AHEAD];
+#pragma unroll
+    for (int u = 0; u < MT * NT + AHEAD; ++u) {
+      const int x = u % MT, y = u / MT, e = u - AHEAD;
+      if (x == 0 && y + 1 < NT) {
+        pin(pb);
+        get(bv[(y + 1) & 1], cur + SIDE * 128, pb, y + 1);
+      }
+      if (MORE && u < LOADS) load_one(t + (STAGES - 1) * SW, u, nxt);
+      v4f co = {0.f, 0.f, 0.f, 0.f};
+      if (e >= 0) co = c[e % AHEAD];
+      if (u < MT * NT) {
+        pin(bv[y & 1], co);
+        v4f cn = mfma128(bv[y & 1], av[x]);
+        pin(cn, co);
+        c[u % AHEAD] = cn;
+      }
+      if (e >= 0) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[e % MT][e / MT][v] = fmaf(co[v], s[e % MT], acc[e % MT][e / MT][v]);
+      }
+    }
+  };
+  static_assert(LOADS <= MT * NT + 2 && STAGES >= 2, "every load has its place");
+  if (own > 0) {
+    sbv = sb[min(wv + l * SW, nb - 1) * a.bs_blk];
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) load_one(wv + min(i, own - 1) * SW, q, lds[wv][i]);
+  }
+  int i = 0, cur = 0, nxt = STAGES - 1;
+  auto arrive = [&](auto full) {                         // full: STAGES - 2 younger blocks are on their way
+    if (i > 0 && (i & 63) == 0) {
+      sbv = sb[min(wv + (i + l) * SW, nb - 1) * a.bs_blk];
+      __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt(decltype(full)::value ? (STAGES - 2) * LOADS : 0));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  };
+  auto step = [&] {
+    __builtin_amdgcn_wave_barrier();
+    nxt = cur;
+    cur = cur + 1 == STAGES ? 0 : cur + 1;
+  };
+  for (; i + STAGES - 1 < own; ++i) {
+    arrive(Const<true>{});
+    block(i, lds[wv][cur], lds[wv][nxt], Const<true>{});
+    step();
+  }
+  for (; i < own; ++i) {
+    arrive(Const<false>{});
+    block(i, lds[wv][cur], lds[wv][nxt], Const<false>{});
+    step();
+  }
+  // join, 16 KB per wave in the stages it no longer reads
+  float *part = reinterpret_cast<float *>(lds[wv][0]);
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y) *reinterpret_cast<v4f *>(part + ((x * NT + y) * 64 + l) * 4) = acc[x][y];
+  __syncthreads();
+  for (int i = wv; i < MT * NT; i += SW) {
+    v4f sum = *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(lds[0][0]) + (i * 64 + l) * 4);
+#pragma unroll
+    for (int q = 1; q < SW; ++q) sum += *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(lds[q][0]) + (i * 64 + l) * 4);
+    store_c<T>(a, m0 + 16 * (i / NT) + j, n0 + 16 * (i % NT) + 4 * g, sum);
+  }
+}
+
 template <typename T, int BM, int BN, int WM, int WN, int STAGES>
 static void launch_tiles(const MatArgs &a, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>((static_cast<int64_t>(a.m) + BM - 1) / BM * ((static_cast<int64_t>(a.n) + BN - 1) / BN));
@@ -482,7 +627,10 @@ static int launch_matmul(const MatArgs &a, hipStream_t st) {
     } else if (tiles(64, 128) >= 256) {
       launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
     } else {
-      launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
+      // one tile a CU: its waves share out the scale blocks, unless there are hardly more than
+      // waves (1000 x 1000 x 300: 4.5 us, 4.3 with shared stages)
+      if (tiles(64, 64) <= 256 && a.k > 5 * 128) matmul_split_kernel<T, 4, 2><<<static_cast<uint32_t>(tiles(64, 64)), 256, 0, st>>>(a);
+      else launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
     }
   }
   return check_launch("matmul_fp8");

@@ -10,11 +10,11 @@
 namespace echo {
 
 constexpr int QT = 256;          // threads per workgroup
-constexpr int QU = 4;            // groups of four blocks per wave
 
-// WIDE: rows start 16-byte aligned in x and 8-byte aligned in y, so whole 8-element pieces are
-// read and written at once; otherwise element by element.
-template <typename T, bool WIDE>
+// QU groups of four blocks per wave.  WIDE: rows start 16-byte aligned in x and 8-byte aligned in y;
+// otherwise whole 8-element pieces are read and written at any address.  The end of a row that is
+// no whole piece goes element by element.
+template <typename T, bool WIDE, int QU>
 __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int64_t ldx, int32_t n_cols,
                                                    uint32_t n_blk, uint32_t total, uint8_t *__restrict__ y,
                                                    int64_t ldy, float *__restrict__ scale, int64_t s_row,
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int6
     left[u] = in ? min(max(n_cols - c, 0), VEC) : -1;        // -1: no such block
     const T *p = x + row[u] * ldx + c;
     if (left[u] <= 0) raw[u] = zero8<T>();
-    else if (WIDE && left[u] == VEC) raw[u] = load8(p);
+    else if (left[u] == VEC) raw[u] = WIDE ? load8(p) : load8_any(p);
     else raw[u] = load8_part(p, left[u]);
   }
 #pragma unroll
@@ -46,8 +46,9 @@ __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int6
     if (left[u] < 0) continue;
     if (j == 0) scale[row[u] * s_row + blk[u] * s_blk] = s.scale;
     uint8_t *p = y + row[u] * ldy + static_cast<int>(blk[u]) * 128 + j * VEC;
-    if (WIDE && left[u] == VEC) {
-      *reinterpret_cast<u32x2 *>(p) = code;
+    if (left[u] == VEC) {
+      if (WIDE) *reinterpret_cast<u32x2 *>(p) = code;
+      else *reinterpret_cast<u32x2_any *>(p) = code;
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
@@ -56,18 +57,27 @@ __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int6
   }
 }
 
+template <typename T, int QU>
+static void launch_quant_u(const void *x, int64_t ldx, int32_t n_cols, uint32_t n_blk, uint32_t total, uint8_t *y,
+                           int64_t ldy, float *scale, int64_t s_row, int64_t s_blk, hipStream_t st) {
+  constexpr uint32_t PER = QU * 4 * (QT / 64);                   // blocks of a workgroup
+  const uint32_t grid = (total + PER - 1) / PER;
+  const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * sizeof(T) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(y) % 8 == 0 && ldy % 8 == 0;
+  if (wide)
+    quant_kernel<T, true, QU><<<grid, QT, 0, st>>>(static_cast<const T *>(x), ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk);
+  else
+    quant_kernel<T, false, QU><<<grid, QT, 0, st>>>(static_cast<const T *>(x), ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk);
+}
+
 template <typename T>
 static int launch_quant(const void *x, int64_t n_rows, int32_t n_cols, int64_t ldx, uint8_t *y, int64_t ldy,
                         float *scale, int64_t s_row, int64_t s_blk, hipStream_t st) {
   const uint32_t n_blk = (static_cast<uint32_t>(n_cols) + 127u) / 128u;
   const uint32_t total = static_cast<uint32_t>(n_rows * n_blk);
-  const uint32_t grid = (total + QU * 4 * (QT / 64) - 1) / (QU * 4 * (QT / 64));
-  const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * sizeof(T) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(y) % 8 == 0 && ldy % 8 == 0;
-  if (wide)
-    quant_kernel<T, true><<<grid, QT, 0, st>>>(static_cast<const T *>(x), ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk);
-  else
-    quant_kernel<T, false><<<grid, QT, 0, st>>>(static_cast<const T *>(x), ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk);
+  // Four groups a wave once that gives every CU a workgroup or more; few blocks are over sooner spread thin.
+  if (total >= 256 * 4 * 4 * (QT / 64)) launch_quant_u<T, 4>(x, ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk, st);
+  else launch_quant_u<T, 1>(x, ldx, n_cols, n_blk, total, y, ldy, scale, s_row, s_blk, st);
   return check_launch("quant_fp8");
 }
 

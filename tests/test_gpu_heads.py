@@ -57,6 +57,9 @@ CASES = [
     (12, 4, 2, 256, 256, 0, False, "layer", "layer", True, True),
     (20, 3, 1, 40, 32, 8, False, "rms", "layer", False, False),
     (4, 2, 2, 200, 16, 184, False, "none", "none", False, False),
+    # enough heads for several loads a wave: a token's heads in whole and partial chunks, few heads
+    (270, 37, 2, 64, 64, 0, False, "rms", "layer", True, True),
+    (1100, 3, 17, 128, 64, 64, True, "layer", "rms", True, False),
 ]
 
 
@@ -186,6 +189,7 @@ INDEXER = [
     (50, 64, 64, 64, False, 50),
     (13, 3, 128, 0, False, 100),
     (6, 0, 64, 0, False, 9),
+    (300, 64, 64, 0, False, 301),
 ]
 
 
