@@ -250,8 +250,10 @@ ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
 // waves per SIMD allow beside the operands: 64 x 128 outputs per wave.
 //
 // Workgroups go to the 8 XCDs in turn, each with an L2 of its own, so consecutive tiles of one XCD
-// are neighbours: it gets one eighth of the tiles, taken in bands of BAND tile rows.
-constexpr int BAND = 8;
+// are neighbours: it gets one eighth of the tiles, taken in bands of BAND tile rows.  Its 32 CUs then
+// hold about 5 x 6 tiles, which read the fewest different rows of a and b (16384 x 8192 x 2048 on
+// MI355X: 308 us with bands of 8, 291 with 4, 287 with 5, 289 with 6).
+constexpr int BAND = 5;
 ECHO_DEV void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t &tm, uint32_t &tn) {
   const uint32_t total = mt * nt, xcd = id & 7u, i = id >> 3;
   const uint32_t each = total >> 3, more = total & 7u;         // the first `more` XCDs take one more
@@ -616,14 +618,18 @@ static int launch_matmul(const MatArgs &a, hipStream_t st) {
     // The largest tile that still gives each of the 256 CUs one.  Small tiles keep more stages in
     // flight, since a block of theirs is multiplied before the next could arrive (MI355X, three
     // stages against two for 64 x 128: 256 x 8192 x 2048 10.2 us and 12.8; 128 x 128 tiles with two:
-    // 20.4; 8192 x 128 x 4096: 12.8 us in 64 x 64, 36 in 128 x 128).
+    // 20.4; 8192 x 128 x 4096: 12.8 us in 64 x 64, 36 in 128 x 128).  128 x 128 tiles want two
+    // workgroups a CU (2500^3: 35.5 us with two stages, 41.9 with three) unless there is one tile a
+    // CU (1024 x 4096 x 4096: 28.0 and 24.0).
     bool done = false;
     if constexpr (sizeof(T) == 2) {                      // fp32 results hold their operands as bf16: too many registers
       if ((done = tiles(256, 256) >= 256)) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
     }
     if (done) {
-    } else if (tiles(128, 128) >= 256) {
+    } else if (tiles(128, 128) > 256) {
       launch_tiles<T, 128, 128, 64, 64, 2>(a, st);
+    } else if (tiles(128, 128) >= 192) {                 // one a CU: a third stage instead of a second workgroup
+      launch_tiles<T, 128, 128, 64, 64, 3>(a, st);
     } else if (tiles(64, 128) >= 256) {
       launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
     } else {
