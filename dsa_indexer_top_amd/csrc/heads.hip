@@ -245,6 +245,8 @@ static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
     loads = 1;
     for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
   }
+  if (static_cast<uint64_t>(a.waves[0]) + a.waves[1] >= (1u << 26))
+    return fail(ECHO_EUNSUPPORTED, "qk heads: more waves than a launch holds (2^26)");
   const uint32_t grid = static_cast<uint32_t>((static_cast<uint64_t>(a.waves[0]) + a.waves[1] + HT / 64 - 1) / (HT / 64));
   if (FP8) {
     launch_heads_g<T, 16, FP8>(a, loads, next, grid, st);
@@ -296,6 +298,7 @@ static int check_heads(const char *fn, const echo_qk_args *q, bool *empty) {
   const int64_t most = 0x7FFFFFFF - 65536;
   if (static_cast<int64_t>(q->n_tok) * q->n_q_heads > most || static_cast<int64_t>(q->n_tok) * q->n_k_heads > most)
     return fail(ECHO_EUNSUPPORTED, "%s: more than 2^31 - 2^16 heads in all", fn);
+  if (misaligned(q->pos, 4)) return fail(ECHO_EINVAL, "%s: pos is not aligned to its type", fn);
   const int64_t vec = q->type == ECHO_FP32 ? 4 : 8;                 // elements in 16 bytes
   if (misaligned(q->q_weight, 16) || misaligned(q->q_bias, 16) || misaligned(q->k_weight, 16) ||
       misaligned(q->k_bias, 16) || misaligned(q->cos_sin, 16) ||
@@ -334,6 +337,11 @@ extern "C" int echo_qk_norm_rope(const echo_qk_args *q, void *q_out, int64_t qo_
   if ((q->n_q_heads && (misaligned(q_out, 16) || qo_tok_stride % vec || qo_head_stride % vec)) ||
       (q->n_k_heads && (misaligned(k_out, 16) || ko_tok_stride % vec || ko_head_stride % vec)))
     return fail(ECHO_EUNSUPPORTED, "echo_qk_norm_rope: an output or its stride is not a multiple of 16 bytes");
+  const auto overlaps = [&](int32_t heads, int64_t tok, int64_t head) {
+    return (heads > 1 && head < q->head_dim) || (heads > 0 && q->n_tok > 1 && tok < q->head_dim);
+  };
+  if (overlaps(q->n_q_heads, qo_tok_stride, qo_head_stride) || overlaps(q->n_k_heads, ko_tok_stride, ko_head_stride))
+    return fail(ECHO_EINVAL, "echo_qk_norm_rope: output heads overlap");
   HeadArgs a = head_args(q);
   a.side[0].y = q_out; a.side[0].yt = qo_tok_stride; a.side[0].yh = qo_head_stride;
   a.side[1].y = k_out; a.side[1].yt = ko_tok_stride; a.side[1].yh = ko_head_stride;
@@ -354,6 +362,8 @@ extern "C" int echo_indexer_qk(const echo_qk_args *q, const float *w, int64_t w_
     return fail(ECHO_EINVAL, "echo_indexer_qk: NULL pointer");
   if (misaligned(q8, 8) || misaligned(k_cache, 8))
     return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: q8 or k_cache is not 8-byte aligned");
+  if (misaligned(w, 4) || misaligned(w_out, 4) || misaligned(k_scale, 4) || misaligned(slot, 8))
+    return fail(ECHO_EINVAL, "echo_indexer_qk: a pointer is not aligned to its type");
   HeadArgs a = head_args(q);
   a.f = Fp8Side{w, w_tok_stride, w_mul, q8, w_out, k_cache, k_scale, slot, n_slots};
   return launch_typed<true>(q, a, S(stream));

@@ -659,11 +659,13 @@ extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_sca
   if (reinterpret_cast<uintptr_t>(a) % 16 || reinterpret_cast<uintptr_t>(b) % 16 || lda % 16 || ldb % 16)
     return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: a, b, lda or ldb is not a multiple of 16");
   const int64_t tiles = ((static_cast<int64_t>(m) + 127) / 128) * ((static_cast<int64_t>(n) + 127) / 128);
+  if (k > 0x7FFFFFFF - 256 || n > (1 << 26) || m > (1 << 26) || tiles >= (1 << 24))
+    return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: size beyond the grid");
   if (as_row < 0 || as_row > (1 << 22) || as_blk < 0 || bs_row < 0 || bs_blk < 0)
     return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: a scale stride below 0, or activation scales more than 2^22 apart");
   if (lda > (1 << 22) || ldb > (1 << 22)) return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: rows of more than 2^22 bytes");
-  if (k > 0x7FFFFFFF - 256 || n > 0x7FFFFFFF - 256 || m > 0x7FFFFFFF - 256 || tiles > 0x7FFFFFFF / 8)
-    return fail(ECHO_EUNSUPPORTED, "echo_matmul_fp8: size beyond the grid");
+  if (reinterpret_cast<uintptr_t>(a_scale) % 4 || reinterpret_cast<uintptr_t>(b_scale) % 4)
+    return fail(ECHO_EINVAL, "echo_matmul_fp8: a scale is not aligned to its type");
   const size_t size = c_type == ECHO_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(c) % size) return fail(ECHO_EINVAL, "echo_matmul_fp8: c is not aligned to its type");
   const MatArgs x = {a, b, a_scale, b_scale, lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc, m, n, k, c,

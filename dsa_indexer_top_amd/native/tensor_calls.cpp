@@ -120,8 +120,10 @@ void check(const char *fn, int code) {
 int64_t row_stride(const char *fn, const char *name, const at::Tensor &t) {
   const int64_t rows = t.size(0), cols = t.size(1);
   if (cols > 1 && t.stride(1) != 1) refuse(fn, "the rows of %s are not contiguous", name);
-  return rows > 1 ? t.stride(0) : std::max(t.stride(0), cols);
+  return rows > 1 ? t.stride(0) : cols;
 }
+// The stride of a dimension of one means nothing.
+int64_t stride(const at::Tensor &t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; }
 
 template <typename F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t need, F f) {
@@ -195,7 +197,7 @@ PyObject *quant_fp8(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
     w.same("scale", scale);
     const int64_t ldx = row_stride(fn, "x", *x), ldy = row_stride(fn, "y", *y);
     check(fn, g_quant(address(x), kind, rows, count32(fn, cols), ldx, static_cast<uint8_t *>(address(y)), ldy,
-                      static_cast<float *>(address(scale)), scale->stride(0), scale->stride(1), w.stream(o[3], o[4] == Py_True)));
+                      static_cast<float *>(address(scale)), stride(*scale, 0), stride(*scale, 1), w.stream(o[3], o[4] == Py_True)));
   });
 }
 
@@ -230,17 +232,17 @@ PyObject *matmul_fp8(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
     w.same("b_scale", bs);
     w.same("c", c);
     const int64_t lda = codes_stride(fn, "a", *a), ldb = codes_stride(fn, "b", *b), ldc = row_stride(fn, "c", *c);
-    check(fn, g_matmul(static_cast<const uint8_t *>(address(a)), lda, static_cast<const float *>(address(as)), as->stride(0), as->stride(1),
-                       static_cast<const uint8_t *>(address(b)), ldb, static_cast<const float *>(address(bs)), bs->stride(0),
-                       bs->stride(1), count32(fn, m), count32(fn, n), count32(fn, k), address(c), ldc, kind, w.stream(o[5], o[6] == Py_True)));
+    check(fn, g_matmul(static_cast<const uint8_t *>(address(a)), lda, static_cast<const float *>(address(as)), stride(*as, 0), stride(*as, 1),
+                       static_cast<const uint8_t *>(address(b)), ldb, static_cast<const float *>(address(bs)), stride(*bs, 0),
+                       stride(*bs, 1), count32(fn, m), count32(fn, n), count32(fn, k), address(c), ldc, kind, w.stream(o[5], o[6] == Py_True)));
   });
 }
 
-// Strides of tokens and heads; the stride of a dimension of one means nothing.
+// Strides of tokens and heads.
 void head_strides(const char *fn, const char *name, const at::Tensor &t, int64_t &tok, int64_t &head) {
   if (t.numel() && t.size(2) > 1 && t.stride(2) != 1) refuse(fn, "the heads of %s are not contiguous", name);
-  tok = t.size(0) > 1 ? t.stride(0) : 0;
-  head = t.size(1) > 1 ? t.stride(1) : 0;
+  tok = stride(t, 0);
+  head = stride(t, 1);
 }
 
 constexpr int QK = 15;              // arguments of qk_args: q, k, pos, cos_sin, rot_begin, ..., k_bias

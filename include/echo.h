@@ -627,9 +627,9 @@ int echo_page_step(const echo_page_args *a, void *ws, size_t ws_bytes, void *str
  * short): scale = max(largest |x| of the block / 448, 2^-126), y = x / scale rounded to the nearest
  * E4M3FN number.  x has type x_type and row stride ldx, y row stride ldy (both in elements);
  * scale[r * scale_row + b * scale_blk].  What the codes of a block with a NaN or an infinity
- * stand for is NaN.  Any alignment is taken; rows of x on 16 bytes and of y on 8 are faster.  ECHO_EINVAL for
- * negative sizes, NULL pointers, an unknown type and strides that make rows overlap;
- * ECHO_EUNSUPPORTED beyond 2^30 columns or 2^31 - 1 blocks.  No rows or columns: ECHO_OK.
+ * stand for is NaN.  x and scale are aligned to their types, y to nothing; rows of x on 16 bytes
+ * and of y on 8 are fastest.  ECHO_EINVAL for negative sizes, NULL pointers, an unknown type and
+ * strides that make rows overlap; ECHO_EUNSUPPORTED above 2^30 columns or from 2^30 blocks on.  No rows or columns: ECHO_OK.
  */
 int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols, int64_t ldx, uint8_t *y,
                    int64_t ldy, float *scale, int64_t scale_row, int64_t scale_blk, void *stream);
@@ -647,7 +647,7 @@ int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols
  * atomics, no workspace.  m = 0 or n = 0: ECHO_OK; k = 0 writes zeros.  ECHO_EINVAL for negative
  * sizes, NULL pointers, an unknown type, lda or ldb below k, ldc below n, c not aligned to its type;
  * ECHO_EUNSUPPORTED for other alignments, lda, ldb or as_row above 2^22, negative scale strides, and
- * sizes beyond the grid (n, m or k near 2^31, 2^28 output tiles of 128 x 128).
+ * sizes beyond a launch (m or n above 2^26, 2^24 output tiles of 128 x 128).
  */
 int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t as_row, int64_t as_blk,
                     const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk, int32_t m,
@@ -660,11 +660,13 @@ int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t
  * pair of angle i is (rot_begin + i, rot_begin + rot_dim / 2 + i), or with interleaved != 0
  * (rot_begin + 2 i, rot_begin + 2 i + 1): (u, v) becomes (u cos - v sin, v cos + u sin).  Values
  * are computed in fp32 and rounded once.  q and k are [n_tok, heads, head_dim] of type `type`
- * with strides in elements; weights and biases are fp32 [head_dim] or NULL (1 and 0).  A token
+ * with strides in elements; weights and biases are fp32 [head_dim] or NULL (1 and 0), not read
+ * without a norm.  A token
  * whose pos is outside [0, n_pos) is padding: nothing of it is written.  head_dim is a multiple of 8
  * up to 256, rot_dim (0: none, cos_sin may be NULL) a multiple of 16, rot_begin of 8; pointers and
- * strides of q, k, cos_sin, weights and outputs are multiples of 16 bytes.  Anything else is
- * ECHO_EUNSUPPORTED.
+ * strides of q, k, cos_sin, weights and outputs are multiples of 16 bytes; anything else is
+ * ECHO_EUNSUPPORTED, as are more than 2^31 - 2^16 heads in all.  ECHO_EINVAL for negative sizes,
+ * NULL pointers, an unknown type or norm, a rotated part behind the head's end, eps below 0 or NaN.
  */
 typedef struct {
   int32_t n_tok, n_q_heads, n_k_heads, head_dim;
@@ -680,7 +682,7 @@ typedef struct {
 } echo_qk_args;
 
 /* q_out and k_out have the inputs' type; each may be its input (same strides) but overlap nothing
- * else. */
+ * else, nor may their heads overlap (ECHO_EINVAL). */
 int echo_qk_norm_rope(const echo_qk_args *a, void *q_out, int64_t qo_tok_stride, int64_t qo_head_stride,
                       void *k_out, int64_t ko_tok_stride, int64_t ko_head_stride, void *stream);
 

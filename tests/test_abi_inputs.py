@@ -66,7 +66,7 @@ def test_quant_argument_errors():
     assert call(x=F + 1) == call(s=F + 2) == B.ECHO_EINVAL and "aligned" in err()
     assert call(t=B.FP32, x=F + 2) == B.ECHO_EINVAL
     assert call(cols=(1 << 30) + 1, ldx=1 << 31, ldy=1 << 31) == B.ECHO_EUNSUPPORTED
-    assert call(rows=1 << 40) == B.ECHO_EUNSUPPORTED
+    assert call(rows=1 << 40) == call(rows=1 << 30, cols=1) == B.ECHO_EUNSUPPORTED
     assert call(rows=0) == call(cols=0) == B.ECHO_OK
 
 
@@ -83,7 +83,8 @@ def test_matmul_argument_errors():
     assert call(lda=1 << 23) == call(ldb=(1 << 22) + 16) == B.ECHO_EUNSUPPORTED
     assert call(ar=-1) == call(ar=(1 << 22) + 1) == call(ab=-1) == call(br=-1) == call(bb=-1) == B.ECHO_EUNSUPPORTED
     assert call(c=F + 1) == B.ECHO_EINVAL and call(c=F + 2, t=B.FP32) == B.ECHO_EINVAL
-    big = 0x7FFFFFFF
+    assert call(sa=F + 2) == call(sb=F + 1) == B.ECHO_EINVAL
+    big = (1 << 26) + 1
     assert call(m=big) == call(n=big, ldc=big) == B.ECHO_EUNSUPPORTED
     assert call(m=1 << 24, n=1 << 24, ldc=1 << 24) == B.ECHO_EUNSUPPORTED
     assert call(m=0) == call(n=0, ldc=0) == B.ECHO_OK
@@ -127,12 +128,15 @@ def test_heads_argument_errors():
     assert rope(None, 1024, 128, F, 128, 128) == rope(F, 1024, 128, None, 128, 128) == B.ECHO_EINVAL
     assert rope(F + 8, 1024, 128, F, 128, 128) == rope(F, 1024, 130, F, 128, 128) == B.ECHO_EUNSUPPORTED
     assert rope(F, 1024, 128, F, 130, 128) == B.ECHO_EUNSUPPORTED
+    assert rope(F, 1024, 0, F, 128, 128) == rope(F, 64, 128, F, 128, 128) == B.ECHO_EINVAL and "overlap" in err()
+    assert rope(F, 1024, 128, F, 0, 128) == rope(F, -1024, 128, F, 128, 128) == B.ECHO_EINVAL
     idx = lambda w=F, q8=F, wo=F, kc=F, ks=F, sl=F, n=64, **kw: L.echo_indexer_qk(qk_args(**kw), w, 8, 1.0, q8, wo, kc, ks, sl, n, None)
     assert idx(head_dim=64) == B.ECHO_EUNSUPPORTED and idx(n_k_heads=2) == B.ECHO_EUNSUPPORTED
     assert idx(n=-1) == B.ECHO_EINVAL
     for name in ("w", "q8", "wo", "kc", "ks", "sl"):
         assert idx(**{name: None}) == B.ECHO_EINVAL and "NULL" in err(), name
     assert idx(q8=F + 4) == idx(kc=F + 1) == B.ECHO_EUNSUPPORTED
+    assert idx(w=F + 2) == idx(wo=F + 1) == idx(ks=F + 2) == idx(sl=F + 4) == idx(pos=F + 2) == B.ECHO_EINVAL
 
 
 # ---------------------------------------------------------------- the binding's own checks
