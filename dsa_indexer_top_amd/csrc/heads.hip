@@ -237,11 +237,12 @@ template <typename T, bool FP8>
 static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
   int g = 2;
   while (g * VEC < a.dim) g *= 2;
-  // Four loads a wave, for their common angles and weights, once that gives every SIMD a wave;
-  // fewer rows are over sooner spread thin (MI355X, 64 tokens' indexer inputs: 6.0 us with four, 3.9 with one).
+  // Four loads a wave, for their common angles and weights, from 8192 waves on; fewer rows are over
+  // sooner spread thin (MI355X, indexer inputs: 64 tokens 3.2 us with one load, 6.0 with four; 512
+  // tokens 6.2 and 8.2; 1024 9.4 and 10.0; 4096 27.7 and 23.9).
   int loads = 4;
   for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
-  if (static_cast<uint64_t>(a.waves[0]) + a.waves[1] < 1024) {
+  if (static_cast<uint64_t>(a.waves[0]) + a.waves[1] < 8192) {
     loads = 1;
     for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
   }

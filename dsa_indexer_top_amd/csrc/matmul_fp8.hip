@@ -237,17 +237,19 @@ ECHO_DEV v8i keep_bytes(v8i v, int g, int left) {
   return v;
 }
 
-// BM activation rows x BN weight rows per workgroup, WM x WN per wave; two stages in LDS.  While a
-// block is multiplied the next one's loads are issued one by one between the products: issued
+// BM activation rows x BN weight rows per workgroup, WM x WN per wave; STAGES blocks in LDS.  While
+// one is multiplied the loads of a later one are issued one by one between the products: issued
 // together at the start of the block they held up its first operand reads (8192^3 on MI355X: 2105
 // against 2188 TFLOP/s).
 //
 // What bounds the 256 x 256 tile: an MFMA takes 32 cycles of its SIMD's matrix core and its result
-// four FMAs of 4 cycles, so the products can hide everything else; counters give 58% of cycles
-// multiplying at 8192^3 at the 1.81 GHz the chip then ran (1.98 GHz at 50% before the loads were
-// spread): the clock falls as the cores fill.  Without any loads the same code reaches 2650
-// TFLOP/s, without the FMAs 2200.  A wave's accumulators are 128 registers, the most that two
-// waves per SIMD allow beside the operands: 64 x 128 outputs per wave.
+// four FMAs of 4 cycles, so the products could hide everything else.  At 8192^3 (478 us, 2300
+// TFLOP/s) counters give 59% of cycles multiplying at the 1.84 GHz the chip then ran; with 50% it
+// ran at 1.98 GHz: the clock falls as the cores fill.  Measured on an earlier form of the loop at
+// 2110 TFLOP/s: without its loads 2650, without three of the four FMAs 2200, without barriers 2%
+// more.  A wave's accumulators are 128 registers, the most that two waves per SIMD allow beside the
+// operands: 64 x 128 outputs per wave.  At 16384 x 8192 x 2048 (264 to 317 us, by box and clock)
+// writing the result adds 50 to 60 us: tiles of a size end together and the next ones wait for HBM.
 //
 // Workgroups go to the 8 XCDs in turn, each with an L2 of its own, so consecutive tiles of one XCD
 // are neighbours: it gets one eighth of the tiles, taken in bands of BAND tile rows.  Its 32 CUs then

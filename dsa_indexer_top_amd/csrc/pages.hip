@@ -12,7 +12,7 @@
 //
 // All of it is latency: the bytes of a decode step fit in a few cache lines per request.  A step of
 // few tokens therefore runs as ONE workgroup and one launch, its prefix sums in LDS (256 requests
-// on MI355X: 4.7 us).  A step of many tokens (chunked prefill: 16 bytes written per token) takes two
+// on MI355X: 4.6 us a step, 2048: 11.3).  A step of many tokens (chunked prefill: 16 bytes written per token) takes two
 // launches: the plan (prefix sums, made by every workgroup for itself, and the return of the
 // finished requests' pages, shared out among them) and the fill of the maps from the whole chip
 // (61 requests with up to 8192 new tokens each: 4.0 + 5.5 us; with a launch of its own for the return and
@@ -23,8 +23,10 @@ namespace echo {
 
 constexpr int PT = 512;                        // threads of the one-workgroup kernels
 constexpr int PG_ONE_ROWS = 2048;              // requests whose prefix sums fit in LDS
-constexpr int PG_ONE_TOKENS = 8192;            // new tokens one workgroup maps
+constexpr int PG_ONE_TOKENS = 7 * PT;          // new tokens one workgroup maps: at 64 requests' 1024 tokens
+                                               // 4.1 us against 6.2 in two launches, at 4096 6.8 against 6.4
 constexpr int PF_T = 256;                      // threads of the fill and the return of pages
+constexpr uint32_t FEW = 4;                    // new tokens that a request's own thread maps
 constexpr uint32_t SAT = 0x7FFFFFFFu;
 
 // A sum that stops at 2^31 - 1, still associative: the prefix sums of a step whose totals are
@@ -70,7 +72,8 @@ ECHO_DEV PageRow page_row(const PageArgs &a, int r) {
 struct PagePlan {
   int32_t *back, *need, *begin;  // [n_rows + 1]: returned pages, new pages, new tokens before a request
   int32_t *kept;                 // [n_rows + 1]: its length without the new tokens (the last is not used)
-  int32_t *head;                 // [0] free pages after the return, [1] after the step, [2] 1: refused
+  int32_t *head;                 // [0] free pages after the return, [1] after the step, [2] a request has
+                                 // more than FEW new tokens
 };
 constexpr int PLAN_HEAD = 4;
 ECHO_DEV PagePlan plan_at(int32_t *p, int rows) {
@@ -87,12 +90,13 @@ ECHO_DEV void make_plan(const PageArgs &a, const PagePlan &s, uint32_t *tmp, boo
   const int per = (a.n_rows + PT - 1) / PT;
   const int r0 = min(t * per, a.n_rows), r1 = min(r0 + per, a.n_rows);
   uint32_t sum[3] = {0, 0, 0};
-  bool bad = false;
+  bool bad = false, many = false;
   auto add = [&](const PageRow &p) {
     sum[0] = OpSat{}(sum[0], p.back);
     sum[1] = OpSat{}(sum[1], p.need);
     sum[2] = OpSat{}(sum[2], p.fresh);
     bad |= p.bad;
+    many |= p.fresh > FEW;
   };
   const int32_t count = a.count_in[0];
   PageRow own[PER > 0 ? PER : 1];
@@ -109,10 +113,10 @@ ECHO_DEV void make_plan(const PageArgs &a, const PagePlan &s, uint32_t *tmp, boo
     incl[i] = wave_incl_scan_op(sum[i], 0u, OpSat{});
     if (l == 63) tmp[i * NW + w] = incl[i];
   }
-  const bool any_bad = __ballot(bad) != 0;
-  if (l == 63) tmp[3 * NW + w] = any_bad;
+  const uint32_t flags = (__ballot(bad) != 0 ? 1u : 0u) | (__ballot(many) != 0 ? 2u : 0u);
+  if (l == 63) tmp[3 * NW + w] = flags;
   __syncthreads();
-  uint32_t base[3] = {0, 0, 0}, total[3] = {0, 0, 0}, refuse = 0;
+  uint32_t base[3] = {0, 0, 0}, total[3] = {0, 0, 0}, seen = 0;
   for (int v = 0; v < NW; ++v) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
@@ -120,11 +124,11 @@ ECHO_DEV void make_plan(const PageArgs &a, const PagePlan &s, uint32_t *tmp, boo
       if (v < w) base[i] = OpSat{}(base[i], x);
       total[i] = OpSat{}(total[i], x);
     }
-    refuse |= tmp[3 * NW + v];
+    seen |= tmp[3 * NW + v];
   }
   const int64_t have = static_cast<int64_t>(count) + total[0];
   int32_t why = 0;
-  if (refuse || total[2] == SAT || total[2] > static_cast<uint32_t>(a.max_new)) why |= ECHO_ST_BAD_LEN;
+  if ((seen & 1u) || total[2] == SAT || total[2] > static_cast<uint32_t>(a.max_new)) why |= ECHO_ST_BAD_LEN;
   if (count < 0 || total[0] == SAT || total[1] == SAT || have > a.n_pages || static_cast<int64_t>(total[1]) > have)
     why |= ECHO_ST_NO_PAGES;
   // exclusive prefix of the thread's first request; exact whenever the step is not refused
@@ -153,6 +157,7 @@ ECHO_DEV void make_plan(const PageArgs &a, const PagePlan &s, uint32_t *tmp, boo
     s.kept[n] = 0;
     s.head[0] = why ? count : static_cast<int32_t>(have);
     s.head[1] = s.head[0] - s.need[n];
+    s.head[2] = seen >> 1;
     if (why && tell) atomicOr(a.status, why);
   }
   __syncthreads();
@@ -171,27 +176,6 @@ ECHO_DEV void publish(const PageArgs &a, const PagePlan &s, int t, int n) {
   }
 }
 
-// Request q's returned pages onto the stack, by n threads.
-ECHO_DEV void return_row(const PageArgs &a, const PagePlan &s, int q, int t, int n) {
-  const int32_t b = s.back[q], cnt = s.back[q + 1] - b;
-  int32_t *dst = a.free_list + (s.head[0] - s.back[a.n_rows] + b);
-  const int32_t *src = a.page_table + static_cast<int64_t>(q) * a.max_pages;
-  for (int i = t; i < cnt; i += n) dst[i] = src[i];
-}
-// The same for all requests by one workgroup, a wave per request: 64 requests are looked at together.
-ECHO_DEV void return_rows(const PageArgs &a, const PagePlan &s) {
-  constexpr int NW = PT / 64;
-  const int l = lane_id();
-  for (int r0 = threadIdx.x >> 6; r0 < a.n_rows; r0 += 64 * NW) {
-    const int r = r0 + l * NW;
-    uint64_t some = __ballot(r < a.n_rows && s.back[r + 1] > s.back[r]);
-    while (some) {
-      return_row(a, s, r0 + (__ffsll(static_cast<unsigned long long>(some)) - 1) * NW, l, 64);
-      some &= some - 1;
-    }
-  }
-}
-
 // The last request of [lo, hi) whose first token is <= t; begin[lo] <= t < begin[hi].
 ECHO_DEV int find_row(const int32_t *begin, int lo, int hi, int32_t t) {
   while (hi - lo > 1) {
@@ -199,6 +183,26 @@ ECHO_DEV int find_row(const int32_t *begin, int lo, int hi, int32_t t) {
     if (begin[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// Returned pages of the step onto the stack by one workgroup, a wave per request; 64 requests are
+// looked at together.  (Every page found by a search in the prefix sums instead: 18.1 us for 2048
+// requests with 128 finished against 14.2; four requests of a wave together: 14.4.)
+ECHO_DEV void return_rows(const PageArgs &a, const PagePlan &s) {
+  constexpr int NW = PT / 64;
+  const int l = lane_id();
+  int32_t *top = a.free_list + (s.head[0] - s.back[a.n_rows]);
+  for (int r0 = threadIdx.x >> 6; r0 < a.n_rows; r0 += 64 * NW) {
+    const int r = r0 + l * NW;
+    uint64_t some = __ballot(r < a.n_rows && s.back[r + 1] > s.back[r]);
+    while (some) {
+      const int q = r0 + (__ffsll(static_cast<unsigned long long>(some)) - 1) * NW;
+      some &= some - 1;
+      const int32_t b = s.back[q], cnt = s.back[q + 1] - b;
+      const int32_t *src = a.page_table + static_cast<int64_t>(q) * a.max_pages;
+      for (int i = l; i < cnt; i += 64) top[b + i] = src[i];
+    }
+  }
 }
 
 // Maps token t of the step (request r), and writes the table entry of a page that starts with it.
@@ -232,10 +236,13 @@ __global__ __launch_bounds__(PT) void page_step_kernel(PageArgs a) {
   if (s.back[a.n_rows] > 0) return_rows(a, s);
   __syncthreads();                             // returned pages may be handed out again
   const int32_t total = s.begin[a.n_rows];
-  for (int32_t t = tid; t < a.max_new; t += PT) {
-    if (t < total) map_token(a, s, find_row(s.begin, 0, a.n_rows, t), t);
-    else map_none(a, t);
+  if (!s.head[2]) {                            // a decode step: a thread per request, nothing to search
+    for (int r = tid; r < a.n_rows; r += PT)
+      for (int32_t t = s.begin[r]; t < s.begin[r + 1]; ++t) map_token(a, s, r, t);
+  } else {
+    for (int32_t t = tid; t < total; t += PT) map_token(a, s, find_row(s.begin, 0, a.n_rows, t), t);
   }
+  for (int32_t t = total + tid; t < a.max_new; t += PT) map_none(a, t);
 }
 
 // Up to PG_ONE_ROWS requests: every workgroup makes the plan in its LDS and returns its share of the
@@ -247,8 +254,11 @@ __global__ __launch_bounds__(PT) void page_plan_kernel(PageArgs a, int32_t *ws) 
   make_plan<PG_PER>(a, s, tmp, blockIdx.x == 0);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < 4 * (a.n_rows + 1) + 2; i += PT) ws[i] = plan[i];
-  if (s.back[a.n_rows] > 0)
-    for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) return_row(a, s, r, threadIdx.x, PT);
+  // the finished requests' pages, a workgroup per request
+  int32_t *top = a.free_list + (s.head[0] - s.back[a.n_rows]);
+  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x)
+    for (int i = s.back[r] + threadIdx.x; i < s.back[r + 1]; i += PT)
+      top[i] = a.page_table[static_cast<int64_t>(r) * a.max_pages + (i - s.back[r])];
 }
 
 // More requests: one workgroup, the plan in the workspace.

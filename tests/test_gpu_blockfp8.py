@@ -45,8 +45,7 @@ def check_codes(codes, scale, x, what=""):
     assert (off <= O.nearest_distance(t) + 4 * U * np.abs(t)).all(), (what, np.max(off - O.nearest_distance(t)))
 
 
-# the last two: enough blocks for several a wave, aligned rows and odd ones
-QUANT = [(1, 128), (1, 1), (3, 127), (5, 129), (33, 300), (2, 2047), (17, 1024), (260, 8), (1, 5000), (1030, 2048), (1100, 2047)]
+QUANT = [(1, 128), (1, 1), (3, 127), (5, 129), (33, 300), (2, 2047), (17, 1024), (260, 8), (1, 5000), (40, 2047)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -55,12 +54,19 @@ def test_quant(rows, cols, kind):
     announce("quant", rows, cols, kind)
     rng = np.random.default_rng(rows * 1000 + cols)
     x = torch.from_numpy(rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)) * 2)).to(TYPES[kind])
-    ld = cols + 1 if rows == 1100 else -(-cols // 16) * 16
+    ld = cols + 1 if rows in (40, 4110) else -(-cols // 16) * 16     # rows at any address, or on 16 bytes
     y = torch.full((rows, ld), 0xEE, dtype=torch.uint8, device="cuda")
     scale = torch.full((rows, -(-cols // 128)), -1.0, device="cuda")
     B.quant_fp8(x.cuda(), y[:, :cols], scale)
     check_codes(host(y)[:, :cols], host(scale), x.double().numpy())
     assert (host(y)[:, cols:] == 0xEE).all()          # what stands behind a row is left
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,cols", [(4100, 2048), (4110, 2047)])
+def test_quant_full(rows, cols, kind):
+    """Enough blocks for several a wave."""
+    test_quant(rows, cols, kind)
 
 
 def test_quant_strides_and_odd_addresses():

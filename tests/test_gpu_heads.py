@@ -57,9 +57,13 @@ CASES = [
     (12, 4, 2, 256, 256, 0, False, "layer", "layer", True, True),
     (20, 3, 1, 40, 32, 8, False, "rms", "layer", False, False),
     (4, 2, 2, 200, 16, 184, False, "none", "none", False, False),
-    # enough heads for several loads a wave: a token's heads in whole and partial chunks, few heads
-    (270, 37, 2, 64, 64, 0, False, "rms", "layer", True, True),
-    (1100, 3, 17, 128, 64, 64, True, "layer", "rms", True, False),
+    (60, 37, 2, 64, 64, 0, False, "rms", "layer", True, True),
+]
+# Enough heads for several loads a wave: a token's heads in whole and partial chunks, few heads.
+FULL = [
+    (4200, 37, 2, 64, 64, 0, False, "rms", "layer", True, True),
+    (8300, 3, 17, 128, 64, 64, True, "layer", "rms", True, False),
+    (9000, 1, 6, 96, 32, 8, False, "layer", "rms", True, True),
 ]
 
 
@@ -104,6 +108,12 @@ def test_heads(c, kind):
     wq, Tq, wk, Tk = want_of(c, q, k, par, cs, pos, 1e-5)
     close(f64(qo), wq, Tq, kind)
     close(f64(ko), wk, Tk, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("c", FULL, ids=lambda c: "t%d_%d+%d_d%d" % c[:4])
+def test_heads_full(c, kind):
+    test_heads(c, kind)
 
 
 def test_views_of_one_projection_in_place():
@@ -189,8 +199,8 @@ INDEXER = [
     (50, 64, 64, 64, False, 50),
     (13, 3, 128, 0, False, 100),
     (6, 0, 64, 0, False, 9),
-    (300, 64, 64, 0, False, 301),
 ]
+INDEXER_FULL = [(2300, 64, 64, 0, False, 2301), (2300, 64, 64, 64, True, 2300)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -224,6 +234,12 @@ def test_indexer_inputs(n, h, rot, begin, inter, slots, kind):
     check_fp8(host(cache)[rows], host(cache_scale)[rows].astype(np.float64), wk[~lost, 0], Tk[~lost, 0], "k")
     rest = np.setdiff1d(np.arange(slots), rows)
     assert (host(cache)[rest] == 0xEE).all() and (host(cache_scale)[rest] == -77).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,h,rot,begin,inter,slots", INDEXER_FULL)
+def test_indexer_inputs_full(n, h, rot, begin, inter, slots, kind):
+    test_indexer_inputs(n, h, rot, begin, inter, slots, kind)
 
 
 def test_indexer_padding_tokens():

@@ -68,6 +68,8 @@ CASES = [
     dict(n=3, page=65536, ctx=200000, chunk=40, done=1),
     dict(n=2049, page=16, ctx=40, chunk=2, done=300),       # more requests than one workgroup holds
     dict(n=9, page=128, ctx=300, chunk=2000, done=2),       # more tokens than one workgroup maps
+    dict(n=40, page=16, ctx=3000, chunk=30, done=30),       # more pages come back than threads
+    dict(n=40, page=16, ctx=9000, chunk=200, done=33),
 ]
 
 
