@@ -12,19 +12,19 @@
 //
 // All of it is latency: the bytes of a decode step fit in a few cache lines per request.  A step of
 // few tokens therefore runs as ONE workgroup and one launch, its prefix sums in LDS (256 requests
-// on MI355X: 4.6 us a step, 2048: 11.3).  A step of many tokens (chunked prefill: 16 bytes written per token) takes two
-// launches: the plan (prefix sums, made by every workgroup for itself, and the return of the
-// finished requests' pages, shared out among them) and the fill of the maps from the whole chip
-// (61 requests with up to 8192 new tokens each: 4.0 + 5.5 us; with a launch of its own for the return and
-// the searches in global memory it took 14.8 us).
+// on MI355X: 4.6 us a step, 2048: 11.3).  A step of many tokens (chunked prefill: 16 bytes written
+// per token) takes two launches: the plan (prefix sums, made by every workgroup for itself, and the
+// return of the finished requests' pages, shared out among them) and the fill of the maps from the
+// whole chip (61 requests with up to 8192 new tokens each: 4.0 + 5.5 us; with a launch of its own
+// for the return and the searches in global memory it took 14.8 us).
 #include "float_types.cuh"
 
 namespace echo {
 
 constexpr int PT = 512;                        // threads of the one-workgroup kernels
 constexpr int PG_ONE_ROWS = 2048;              // requests whose prefix sums fit in LDS
-constexpr int PG_ONE_TOKENS = 7 * PT;          // new tokens one workgroup maps: at 64 requests' 1024 tokens
-                                               // 4.1 us against 6.2 in two launches, at 4096 6.8 against 6.4
+constexpr int PG_ONE_TOKENS = 7 * PT;          // new tokens one workgroup maps: 64 requests' 1024 tokens
+                                               // 4.1 us against 6.2 in two launches, 4096 6.8 against 6.4
 constexpr int PF_T = 256;                      // threads of the fill and the return of pages
 constexpr uint32_t FEW = 4;                    // new tokens that a request's own thread maps
 constexpr uint32_t SAT = 0x7FFFFFFFu;

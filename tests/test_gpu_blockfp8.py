@@ -176,6 +176,23 @@ def test_product_strides(m):
     assert (got[:, :3] == -77.0).all() and (got[:, 3 + n:] == -77.0).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n", [(3, 150), (50, 150), (300, 270),
+                                 *(pytest.param(m, n, id=f"full-{m}-{n}") for m, n in [(1700, 2050), (4100, 8201)])])
+def test_product_at_odd_addresses(m, n, kind):
+    """The same bits whether or not a row starts at a multiple of a wide store; nothing beside them."""
+    rng = np.random.default_rng(m)
+    k = 140
+    a, b, sa, sb = product_case(rng, m, n, k)
+    ops = (dev(a)[:, :k], dev(sa), dev(b)[:, :k], dev(sb))
+    want = torch.empty((m, -(-n // 8) * 8), dtype=TYPES[kind], device="cuda")[:, :n]
+    B.matmul_fp8(*ops, want)
+    c = torch.full((m, -(-n // 2) * 2 + 5), -77.0, dtype=TYPES[kind], device="cuda")
+    B.matmul_fp8(*ops, c[:, 1:1 + n])
+    assert torch.equal(c[:, 1:1 + n], want)
+    assert (c[:, :1] == -77.0).all() and (c[:, 1 + n:] == -77.0).all()
+
+
 @pytest.mark.parametrize("m", [2, 40, 140])
 def test_product_nan_stays_in_its_row_and_column(m):
     rng = np.random.default_rng(9)
