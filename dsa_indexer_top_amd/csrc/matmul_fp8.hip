@@ -18,6 +18,7 @@ struct MatArgs {
   int64_t lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc;
   int32_t m, n, k;
   void *c;
+  bool odd;                       // a row of c may start between two dwords
 };
 
 ECHO_DEV v8i operand(const u32x4 &x, const u32x4 &y) {
@@ -88,6 +89,7 @@ ECHO_DEV v4f mfma128(const Operand<true> &x, const Operand<true> &y) {
 // instead, rows of odd length cost more: 16384 x 8191 x 2048 in bf16 431 us against 352 us,
 // 16000 x 1203 x 177 in fp16 54 us against 28 us on MI355X. Even rows measure the same both ways.
 typedef v4f v4f_any __attribute__((aligned(4)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
 
 template <typename T>
 ECHO_DEV u32x2 pack4(const v4f &v) {
@@ -113,17 +115,30 @@ ECHO_DEV void store_c(const MatArgs &a, int64_t i, int32_t j, const v4f &v) {
   }
 }
 
+// The first `count` of eight 16-bit outputs.
+template <typename T>
+ECHO_DEV void store_some(T *p, const u32x4 &v, int count) {
+  if (count >= 8) {
+    *reinterpret_cast<u32x4_any *>(p) = v;
+  } else if (count > 0) {
+    const bool half = count & 4;
+    if (half) *reinterpret_cast<u32x2_any *>(p) = u32x2{v[0], v[1]};
+    if (count & 2) *reinterpret_cast<u32_any *>(p + (count & 4)) = half ? v[2] : v[0];
+    const uint32_t last = count & 2 ? (half ? v[3] : v[1]) : (half ? v[2] : v[0]);
+    if (count & 1) reinterpret_cast<uint16_t *>(p)[count - 1] = static_cast<uint16_t>(last);
+  }
+}
+
 // ---------------------------------------------------------------- few rows
 // One workgroup per 16 * NT weight rows and all (at most 16 * MT) activation rows; its 8 waves take
 // the scale blocks in turn and their sums are joined in LDS in wave order.  Reading the weights is
 // what costs here (1 x 8192 x 8192 on MI355X: 13.6 us = 4.9 TB/s; 1 x 8192 x 2048: 5.1 us, mostly
 // the launch and one round trip), so every output type gets the exact products.
-constexpr int SW = 8;
-template <typename T, int MT, int NT>
+template <typename T, int MT, int NT, int SW>
 __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
   __shared__ float part[SW][MT * NT][64 * 4];
   const int wv = threadIdx.x >> 6, l = lane_id(), j = l & 15, g = l >> 4;
-  const int32_t n0 = blockIdx.x * (16 * NT), m0 = 0;
+  const int32_t n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
   const int nb = (a.k + 127) >> 7;
   const uint8_t *bp[NT], *ap[MT];
 #pragma unroll
@@ -427,37 +442,59 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
     nxt = cur;
     cur = cur + 1 == STAGES ? 0 : cur + 1;
   }
-  if (m0 + BM <= a.m && n0 + BN <= a.n) {                // a whole tile: no bounds, 16 bytes a store
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int y = 0; y < K::NT; ++y)
+#pragma unroll
+      for (int x = 0; x < K::MT; ++x)
+        store_c<T>(a, m0 + w.wm + 16 * x + w.j, n0 + w.wn + 16 * y + 4 * w.g, w.acc[x][y]);
+  } else {
+    // Two neighbouring tiles: lane rows of 16 exchange halves, so that a lane holds eight
+    // consecutive outputs, lane groups 0 and 2 those of the first tile.
+    constexpr int PAIRS = K::NT / 2;
+    const auto eight = [&](int x, int y) {
+      const u32x2 p = pack4<T>(w.acc[x][2 * y]), q = pack4<T>(w.acc[x][2 * y + 1]);
+      const v2u lo = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+      const v2u hi = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+      return u32x4{lo[0], hi[0], lo[1], hi[1]};
+    };
+    const int32_t col = n0 + w.wn + 16 * (w.g & 1) + 8 * (w.g >> 1);
+    if (m0 + BM <= a.m && n0 + BN <= a.n && !a.odd) {    // a whole tile of even rows: no bounds
+#pragma unroll
+      for (int x = 0; x < K::MT; ++x) {
+        T *row = static_cast<T *>(a.c) + static_cast<int64_t>(m0 + w.wm + 16 * x + w.j) * a.ldc + col;
+#pragma unroll
+        for (int y = 0; y < PAIRS; ++y) *reinterpret_cast<u32x4_any *>(row + 32 * y) = eight(x, y);
+      }
+      return;
+    }
+    // Rows that start between two dwords are written one output further on: a lane gives up its first
+    // output to the lane in front and takes the next lane's.
+    const int next = w.j + 16 * (0x0132 >> (4 * w.g) & 3);
 #pragma unroll
     for (int x = 0; x < K::MT; ++x) {
-      T *row = static_cast<T *>(a.c) + static_cast<int64_t>(m0 + w.wm + 16 * x + w.j) * a.ldc + n0 + w.wn;
-      if constexpr (sizeof(T) == 4) {
+      const int32_t i = m0 + w.wm + 16 * x + w.j;
+      T *row = static_cast<T *>(a.c) + static_cast<int64_t>(i) * a.ldc;
+      const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(row + n0) >> 1) & 1;
+      u32x4 d = eight(x, 0);
 #pragma unroll
-        for (int y = 0; y < K::NT; ++y) *reinterpret_cast<v4f_any *>(row + 16 * y + 4 * w.g) = w.acc[x][y];
-      } else {
-        // Two neighbouring tiles: lane rows of 16 exchange halves, so that a lane holds eight
-        // consecutive outputs, lane groups 0 and 2 those of the first tile.
-        row += 16 * (w.g & 1) + 8 * (w.g >> 1);
-#pragma unroll
-        for (int y = 0; y < K::NT; y += 2) {
-          const u32x2 p = pack4<T>(w.acc[x][y]), q = pack4<T>(w.acc[x][y + 1]);
-          const v2u lo = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
-          const v2u hi = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
-          *reinterpret_cast<u32x4_any *>(row + 16 * y) = u32x4{lo[0], hi[0], lo[1], hi[1]};
-        }
+      for (int y = 0; y < PAIRS; ++y) {
+        const u32x4 after = y + 1 < PAIRS ? eight(x, y + 1) : d;
+        const uint32_t end = __shfl(w.g == 0 ? after[0] : d[0], next);
+        const int32_t to = col + 32 * y + odd;
+        const int count = i >= a.m ? 0 : min(a.n - to, y + 1 == PAIRS && w.g == 3 ? 8 - odd : 8);
+        if (odd && y == 0 && w.g == 0 && i < a.m && col < a.n) reinterpret_cast<uint16_t *>(row)[col] = static_cast<uint16_t>(d[0]);
+        const u32x4 v = odd ? u32x4{d[0] >> 16 | d[1] << 16, d[1] >> 16 | d[2] << 16, d[2] >> 16 | d[3] << 16, d[3] >> 16 | end << 16} : d;
+        store_some(row + to, v, count);
+        d = after;
       }
     }
-    return;
   }
-#pragma unroll
-  for (int y = 0; y < K::NT; ++y)
-#pragma unroll
-    for (int x = 0; x < K::MT; ++x)
-      store_c<T>(a, m0 + w.wm + 16 * x + w.j, n0 + w.wn + 16 * y + 4 * w.g, w.acc[x][y]);
 }
 
 // ---------------------------------------------------------------- few tiles
 template <bool V> struct Const { static constexpr bool value = V; };
+template <int V> struct Int { static constexpr int value = V; };
 
 // 64 x 64 outputs per workgroup, its waves taking the scale blocks in turn: each multiplies whole
 // blocks through LDS stages of its own, so no wave waits for another until the sums are joined at the
@@ -614,12 +651,16 @@ static int launch_matmul(const MatArgs &a, hipStream_t st) {
   // Up to 32 rows the weights' bytes are the cost: as many workgroups as there are 16-row weight
   // tiles, or half as many once those fill the chip (MI355X, 20 x 1024 x 2048: 4.5 us with 16 weight
   // rows, 5.5 with 32; 32 x 8192 x 2048: 8.6 and 6.7; 64 x 64 tiles take 7.6 and 8.1).
-  if (a.m <= 16) {
-    matmul_few_kernel<T, 1, 1><<<dim3(cdiv(a.n, 16)), SW * 64, 0, st>>>(a);
-  } else if (a.m <= 32 && a.n < 256 * 32) {
-    matmul_few_kernel<T, 2, 1><<<dim3(cdiv(a.n, 16)), SW * 64, 0, st>>>(a);
-  } else if (a.m <= 32) {
-    matmul_few_kernel<T, 2, 2><<<dim3(cdiv(a.n, 32)), SW * 64, 0, st>>>(a);
+  const auto few = [&](auto mt, auto nt, auto sw) {
+    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, SW = decltype(sw)::value;
+    matmul_few_kernel<T, MT, NT, SW><<<dim3(cdiv(a.n, 16 * NT), cdiv(a.m, 16 * MT)), SW * 64, 0, st>>>(a);
+  };
+  if (a.m <= 16 || tiles(16, 16) <= 256) {
+    few(Int<1>{}, Int<1>{}, Int<8>{});
+  } else if ((a.m <= 32 && a.n < 256 * 32) || tiles(32, 16) <= 256) {
+    few(Int<2>{}, Int<1>{}, Int<8>{});
+  } else if (a.m <= 32 || tiles(32, 32) <= 256) {
+    few(Int<2>{}, Int<2>{}, Int<8>{});
   } else {
     // The largest tile that still gives each of the 256 CUs one.  Small tiles keep more stages in
     // flight, since a block of theirs is multiplied before the next could arrive (MI355X, three
@@ -674,7 +715,8 @@ extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_sca
     return fail(ECHO_EINVAL, "echo_matmul_fp8: a scale is not aligned to its type");
   const size_t size = c_type == ECHO_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(c) % size) return fail(ECHO_EINVAL, "echo_matmul_fp8: c is not aligned to its type");
-  const MatArgs x = {a, b, a_scale, b_scale, lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc, m, n, k, c};
+  const MatArgs x = {a, b, a_scale, b_scale, lda, ldb, as_row, as_blk, bs_row, bs_blk, ldc, m, n, k, c,
+                     reinterpret_cast<uintptr_t>(c) % 4 != 0 || ldc * size % 4 != 0};
   switch (c_type) {
     case ECHO_BF16: return launch_matmul<bf16_t>(x, S(stream));
     case ECHO_FP16: return launch_matmul<fp16_t>(x, S(stream));

@@ -151,6 +151,13 @@ def test_product(m, n, k, kind):
     assert (got[:, n:] == -77.0).all()
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", [(600, 530, 140), (520, 600, 1030), (33, 4100, 270)])
+def test_product_of_more_tiles(m, n, k, kind):
+    """More outputs than the chip's workgroups of 32 x 32: the wider tiles, and their waves sharing K."""
+    test_product(m, n, k, kind)
+
+
 @pytest.mark.parametrize("m,n,k", [(5, 40, 300), (40, 70, 500), (140, 140, 384)])
 def test_product_exact_on_whole_numbers(m, n, k):
     """Small whole numbers and powers of two as scales: every partial sum is exact in fp32."""
@@ -177,7 +184,7 @@ def test_product_strides(m):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("m,n", [(3, 150), (50, 150), (300, 270),
+@pytest.mark.parametrize("m,n", [(3, 150), (50, 150), (300, 270), (600, 530),
                                  *(pytest.param(m, n, id=f"full-{m}-{n}") for m, n in [(1700, 2050), (4100, 8201)])])
 def test_product_at_odd_addresses(m, n, kind):
     """The same bits whether or not a row starts at a multiple of a wide store; nothing beside them."""
