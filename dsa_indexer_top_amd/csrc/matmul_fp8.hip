@@ -85,9 +85,9 @@ ECHO_DEV v4f mfma128(const Operand<true> &x, const Operand<true> &y) {
   return c;
 }
 
-// Outputs at any address their type allows: gfx950 writes 8 or 16 bytes there. Written one by one
-// instead, rows of odd length cost more: 16384 x 8191 x 2048 in bf16 431 us against 352 us,
-// 16000 x 1203 x 177 in fp16 54 us against 28 us on MI355X. Even rows measure the same both ways.
+// Outputs at any address their type allows: gfx950 writes 8 or 16 bytes there.  Written one by one,
+// rows of odd length cost more (16384 x 8191 x 2048 in bf16 on MI355X: 431 us, 352 in wide stores
+// between dwords, 313 in wide stores a dword on).
 typedef v4f v4f_any __attribute__((aligned(4)));
 typedef uint32_t u32_any __attribute__((aligned(2)));
 
@@ -129,12 +129,14 @@ ECHO_DEV void store_some(T *p, const u32x4 &v, int count) {
   }
 }
 
-// ---------------------------------------------------------------- few rows
-// One workgroup per 16 * NT weight rows and all (at most 16 * MT) activation rows; its 8 waves take
-// the scale blocks in turn and their sums are joined in LDS in wave order.  Reading the weights is
-// what costs here (1 x 8192 x 8192 on MI355X: 13.6 us = 4.9 TB/s; 1 x 8192 x 2048: 5.1 us, mostly
-// the launch and one round trip), so every output type gets the exact products.
-template <typename T, int MT, int NT, int SW>
+// ---------------------------------------------------------------- few outputs
+// One workgroup per 16 * NT weight rows and 16 * MT activation rows; its 8 waves take the scale blocks
+// in turn and their sums are joined in LDS in wave order (four waves are 3% faster up to K = 1000, 20 to
+// 40% slower at 6000; sixteen up to 30% slower).  Reading the weights is what costs here (1 x 8192 x
+// 8192 on MI355X: 13.0 us = 5.2 TB/s; 1 x 8192 x 2048: 5.1 us, mostly the launch and one round
+// trip), so every output type gets the exact products.
+constexpr int SW = 8;
+template <typename T, int MT, int NT>
 __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {
   __shared__ float part[SW][MT * NT][64 * 4];
   const int wv = threadIdx.x >> 6, l = lane_id(), j = l & 15, g = l >> 4;
@@ -468,8 +470,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_tile_kernel
       }
       return;
     }
-    // Rows that start between two dwords are written one output further on: a lane gives up its first
-    // output to the lane in front and takes the next lane's.
+    // Stores that start between two dwords take twice as long (8192 x 6273 x 128: 70 us, 6272 columns
+    // 30).  Such rows are written one output further on: a lane gives up its first output to the lane in
+    // front and takes the next lane's (35 us).
     const int next = w.j + 16 * (0x0132 >> (4 * w.g) & 3);
 #pragma unroll
     for (int x = 0; x < K::MT; ++x) {
@@ -499,8 +502,7 @@ template <int V> struct Int { static constexpr int value = V; };
 // 64 x 64 outputs per workgroup, its waves taking the scale blocks in turn: each multiplies whole
 // blocks through LDS stages of its own, so no wave waits for another until the sums are joined at the
 // end, in wave order.  Where no more than one tile falls to a CU this keeps a block in flight for
-// every wave (MI355X: 64 x 1024 x 4096 8.5 us against 12.0 with 64 x 64 tiles whose waves share the
-// stages, 100 x 1000 x 8000 13.3 against 21.2, 77 x 1000 x 1111 in fp32 6.4 against 7.3).
+// every wave.
 template <typename T, int SW, int STAGES>
 __global__ __launch_bounds__(SW * 64) void matmul_split_kernel(MatArgs a) {
   constexpr int MT = 4, NT = 4, SIDE = 64, LOADS = 2 * SIDE / 8 + 1;
@@ -648,43 +650,40 @@ template <typename T>
 static int launch_matmul(const MatArgs &a, hipStream_t st) {
   const auto cdiv = [](int32_t x, int32_t y) { return static_cast<uint32_t>((static_cast<int64_t>(x) + y - 1) / y); };
   const auto tiles = [&](int bm, int bn) { return static_cast<int64_t>(cdiv(a.m, bm)) * cdiv(a.n, bn); };
-  // Up to 32 rows the weights' bytes are the cost: as many workgroups as there are 16-row weight
-  // tiles, or half as many once those fill the chip (MI355X, 20 x 1024 x 2048: 4.5 us with 16 weight
-  // rows, 5.5 with 32; 32 x 8192 x 2048: 8.6 and 6.7; 64 x 64 tiles take 7.6 and 8.1).
-  const auto few = [&](auto mt, auto nt, auto sw) {
-    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, SW = decltype(sw)::value;
-    matmul_few_kernel<T, MT, NT, SW><<<dim3(cdiv(a.n, 16 * NT), cdiv(a.m, 16 * MT)), SW * 64, 0, st>>>(a);
+  const auto few = [&](auto mt, auto nt) {
+    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value;
+    matmul_few_kernel<T, MT, NT><<<dim3(cdiv(a.n, 16 * NT), cdiv(a.m, 16 * MT)), SW * 64, 0, st>>>(a);
   };
-  if (a.m <= 16 || tiles(16, 16) <= 256) {
-    few(Int<1>{}, Int<1>{}, Int<8>{});
+  // The smallest tile that gives each of the 256 CUs at most one: below that, what a CU can load is
+  // what takes the time.  All times are us on MI355X, in bf16 unless said.
+  if (a.m <= 16 || tiles(16, 16) <= 256) {               // 116 x 100 x 6000: 6.4, split 64 x 64 tiles 10.5
+    few(Int<1>{}, Int<1>{});
   } else if ((a.m <= 32 && a.n < 256 * 32) || tiles(32, 16) <= 256) {
-    few(Int<2>{}, Int<1>{}, Int<8>{});
-  } else if (a.m <= 32 || tiles(32, 32) <= 256) {
-    few(Int<2>{}, Int<2>{}, Int<8>{});
+    few(Int<2>{}, Int<1>{});                             // 64 x 2048 x 6000: 9.3, 10.6 and 14.0 in 16 x 16 and 64 x 64
+  } else if (a.m <= 32 || tiles(32, 32) <= 256) {        // 512 x 512 x 6000: 12.5 and 16.5 in 64 x 64,
+    few(Int<2>{}, Int<2>{});                             // 600 x 530 x 2048, more than 256: 10.8 and 6.3
+  } else if (tiles(64, 64) <= 256) {
+    // Its waves share out the scale blocks (700 x 700 x 4000: 12.3, with shared stages 13.0; fp32 14.6
+    // and 19.4) unless there are hardly more than waves (1000 x 1000 x 300: 4.5 and 4.2).
+    if (a.k > 5 * 128) matmul_split_kernel<T, 4, 2><<<static_cast<uint32_t>(tiles(64, 64)), 256, 0, st>>>(a);
+    else launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
+  } else if (tiles(64, 128) <= 256) {                    // 1728 x 640 x 5000: 21.3, 26.2 in 64 x 64
+    launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
   } else {
-    // The largest tile that still gives each of the 256 CUs one.  Small tiles keep more stages in
-    // flight, since a block of theirs is multiplied before the next could arrive (MI355X, three
-    // stages against two for 64 x 128: 256 x 8192 x 2048 10.2 us and 12.8; 128 x 128 tiles with two:
-    // 20.4; 8192 x 128 x 4096: 12.8 us in 64 x 64, 36 in 128 x 128).  128 x 128 tiles want two
-    // workgroups a CU (2500^3: 35.5 us with two stages, 41.9 with three) unless there is one tile a
-    // CU (1024 x 4096 x 4096: 28.0 and 24.0).
     bool done = false;
-    if constexpr (sizeof(T) == 2) {                      // fp32 results hold their operands as bf16: too many registers
-      if ((done = tiles(256, 256) >= 256)) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
+    if constexpr (sizeof(T) == 2) {
+      // One 128 x 128 tile a CU wants a third stage (2000 x 2000 x 5000: 31.7, 41.9 with two), more a
+      // second workgroup (2500 x 3000 x 5000: 50.5 with two stages, 59.7 with three).  From two a CU
+      // 256 x 256 tiles are faster (5117 x 2046 x 5000: 67.9 and 89.5) unless their last round leaves
+      // more than a quarter of the CUs without one (280 tiles, 5117 x 3582 x 2048: 58.7 and 50.7; 448
+      // tiles, 7165 x 4094 x 2048: 64.7 and 75.1).
+      const int64_t big = tiles(256, 256), rounds = (big + 255) / 256;
+      if ((done = tiles(128, 128) <= 256)) launch_tiles<T, 128, 128, 64, 64, 3>(a, st);
+      else if ((done = tiles(128, 128) > 512 && (rounds == 1 || big >= rounds * 192))) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
     }
-    if (done) {
-    } else if (tiles(128, 128) > 256) {
-      launch_tiles<T, 128, 128, 64, 64, 2>(a, st);
-    } else if (tiles(128, 128) >= 192) {                 // one a CU: a third stage instead of a second workgroup
-      launch_tiles<T, 128, 128, 64, 64, 3>(a, st);
-    } else if (tiles(64, 128) >= 256) {
-      launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
-    } else {
-      // one tile a CU: its waves share out the scale blocks, unless there are hardly more than
-      // waves (1000 x 1000 x 300: 4.5 us, 4.3 with shared stages)
-      if (tiles(64, 64) <= 256 && a.k > 5 * 128) matmul_split_kernel<T, 4, 2><<<static_cast<uint32_t>(tiles(64, 64)), 256, 0, st>>>(a);
-      else launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
-    }
+    // fp32 results hold their operands as bf16: too many registers for the largest tile, and always
+    // two stages (2112 x 1024 x 2048: 20.6, 22.1 with three)
+    if (!done) launch_tiles<T, 128, 128, 64, 64, 2>(a, st);
   }
   return check_launch("matmul_fp8");
 }

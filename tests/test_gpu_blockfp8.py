@@ -185,7 +185,8 @@ def test_product_strides(m):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("m,n", [(3, 150), (50, 150), (300, 270), (600, 530),
-                                 *(pytest.param(m, n, id=f"full-{m}-{n}") for m, n in [(1700, 2050), (4100, 8201)])])
+                                 *(pytest.param(m, n, id=f"full-{m}-{n}") for m, n in [(1200, 1010), (1700, 2050), (2200, 2010),
+                                                                                   (4100, 8201)])])
 def test_product_at_odd_addresses(m, n, kind):
     """The same bits whether or not a row starts at a multiple of a wide store; nothing beside them."""
     rng = np.random.default_rng(m)
@@ -247,7 +248,9 @@ def test_quant_then_product_of_hidden_states():
     (4100, 4111, 400, "bf16"), (4096, 4096, 384, "fp16"), (2000, 2100, 300, "fp32"), (2000, 2100, 777, "bf16"),
     (2048, 2048, 256, "fp32"), (1030, 2050, 700, "bf16"), (1024, 2048, 1152, "fp16"), (1024, 2048, 130, "fp32"),
     (640, 640, 1500, "bf16"), (640, 640, 1408, "fp32"), (33, 4000, 640, "bf16"), (32, 8192, 1111, "bf16"),
-    (31, 1000, 2047, "fp32"), (16, 3001, 2048, "fp16")])
+    (31, 1000, 2047, "fp32"), (16, 3001, 2048, "fp16"), (1200, 1010, 260, "bf16"), (1200, 1010, 1100, "fp32"),
+    (2200, 2010, 700, "fp16"), (4100, 2570, 520, "bf16"), (64, 2047, 1500, "fp16"), (509, 510, 2047, "bf16"),
+    (120, 101, 6001, "fp32")])
 def test_product_full_size_tiles_exact(m, n, k, kind):
     """Whole numbers and powers of two as scales: exact in fp32 in any order and on either matrix
     core (a product is at most 2^4 times another's unit, far above 2^-13), so the result is the
