@@ -215,6 +215,7 @@ static void launch_heads_u(const HeadArgs &a, bool next, uint32_t grid, hipStrea
 template <typename T, int G, bool FP8>
 static void launch_heads_g(const HeadArgs &a, int loads, bool next, uint32_t grid, hipStream_t st) {
   if (loads == 1) launch_heads_u<T, G, FP8, 1>(a, next, grid, st);
+  else if (loads == 2) launch_heads_u<T, G, FP8, 2>(a, next, grid, st);
   else launch_heads_u<T, G, FP8, 4>(a, next, grid, st);
 }
 
@@ -237,15 +238,21 @@ template <typename T, bool FP8>
 static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
   int g = 2;
   while (g * VEC < a.dim) g *= 2;
-  // Four loads a wave, for their common angles and weights, from 8192 waves on; fewer rows are over
-  // sooner spread thin (MI355X, indexer inputs: 64 tokens 3.2 us with one load, 6.0 with four; 512
-  // tokens 6.2 and 8.2; 1024 9.4 and 10.0; 4096 27.7 and 23.9).
-  int loads = 4;
-  for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
-  if (static_cast<uint64_t>(a.waves[0]) + a.waves[1] < 8192) {
-    loads = 1;
+  // Several loads a wave, for their common angles and weights, where there are waves enough and few
+  // of their loads are of nothing; fewer rows are over sooner spread thin.  On MI355X in us with one,
+  // two and four: indexer inputs of 64 tokens 3.3, 4.1, 6.2, of 1400 11.4, 10.5, 11.7, of 32768 197,
+  // 167, 152; 8191 tokens of 40 + 5 heads 41.3, 35.2, 38.7 (a quarter of four are of nothing); 5384
+  // tokens of 4 + 2 heads of 256 10.1, 10.8, 14.6 (a quarter of two, five eighths of four).
+  const auto share = [&](int loads) {
     for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
-  }
+    return static_cast<uint64_t>(a.waves[0]) + a.waves[1];
+  };
+  const uint64_t single = share(1);
+  const auto full = [&](int loads) { return 8 * single >= 7 * loads * share(loads); };
+  int loads = 1;
+  if (single >= 1u << 16 && (full(4) || single >= 1u << 25)) loads = 4;
+  else if (single >= 1u << 13 && full(2)) loads = 2;
+  else share(1);
   if (static_cast<uint64_t>(a.waves[0]) + a.waves[1] >= (1u << 26))
     return fail(ECHO_EUNSUPPORTED, "qk heads: more waves than a launch holds (2^26)");
   const uint32_t grid = static_cast<uint32_t>((static_cast<uint64_t>(a.waves[0]) + a.waves[1] + HT / 64 - 1) / (HT / 64));

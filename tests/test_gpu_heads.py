@@ -64,6 +64,8 @@ FULL = [
     (4200, 37, 2, 64, 64, 0, False, "rms", "layer", True, True),
     (8300, 3, 17, 128, 64, 64, True, "layer", "rms", True, False),
     (9000, 1, 6, 96, 32, 8, False, "layer", "rms", True, True),
+    (4200, 32, 2, 64, 32, 16, True, "rms", "rms", True, False),
+    (8300, 32, 3, 128, 64, 0, False, "rms", "layer", True, True),
 ]
 
 
@@ -200,7 +202,7 @@ INDEXER = [
     (13, 3, 128, 0, False, 100),
     (6, 0, 64, 0, False, 9),
 ]
-INDEXER_FULL = [(2300, 64, 64, 0, False, 2301), (2300, 64, 64, 64, True, 2300)]
+INDEXER_FULL = [(2300, 64, 64, 0, False, 2301), (2300, 64, 64, 64, True, 2300), (4300, 64, 64, 0, True, 4310)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
