@@ -12,7 +12,7 @@
 //
 // All of it is latency: the bytes of a decode step fit in a few cache lines per request.  A step of
 // few tokens therefore runs as ONE workgroup and one launch, its prefix sums in LDS (256 requests
-// on MI355X: 4.6 us a step, 2048: 11.3).  A step of many tokens (chunked prefill: 16 bytes written
+// on MI355X: 4.5 us a step, 2048 of which 128 are finished: 10.2).  A step of many tokens (chunked prefill: 16 bytes written
 // per token) takes two launches: the plan (prefix sums, made by every workgroup for itself, and the
 // return of the finished requests' pages, shared out among them) and the fill of the maps from the
 // whole chip (61 requests with up to 8192 new tokens each: 4.0 + 5.5 us; with a launch of its own
