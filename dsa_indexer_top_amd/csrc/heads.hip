@@ -170,15 +170,18 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
         if (turns) x[i] = x[i] * c[i] + p * d[i];
       }
     }
-    const float amax = FP8 ? group_amax<G>(x) : 0.f;
+    Fp8Scale sc = {};
+    u32x2 code = {0, 0};
+    if (FP8) {                                       // by all lanes, live or not
+      sc = fp8_scale(group_amax<G>(x));
+      code = quantise8<sizeof(T) == 4>(x, sc);
+    }
     if (!live[u]) continue;
     const int32_t t = tok + u * tok_step, h = head + u * head_step;
     if (!FP8) {
       if (in_row) store8(static_cast<T *>(s.y) + t * s.yt + (h * s.yh + j * VEC), x);
       continue;
     }
-    const Fp8Scale sc = fp8_scale(amax);
-    const u32x2 code = quantise8(x, sc.inv);
     if (!is_k) {
       const int64_t row = static_cast<int64_t>(t) * s.heads + h;
       // 8 bytes a lane: past the caches a prefill chunk's codes leave faster (32768 tokens: 175.6 us

@@ -1,7 +1,7 @@
 // Quantisation to FP8 E4M3FN with one fp32 scale per row and block of 128 columns.
 //
 //   scale[r][b] = max(amax_{c in block b} |x[r][c]| / 448, 2^-126)
-//   y[r][c]     = x[r][c] / scale[r][c / 128], rounded to the nearest E4M3FN number
+//   y[r][c]     = fl(x[r][c] / scale[r][c / 128]), rounded to the nearest E4M3FN number
 //
 // One pass: a block is 16 lanes of 8 elements, its largest magnitude a four-step DPP butterfly,
 // so a value is read once and its code written once.  Bound by HBM (32768 x 4096 bf16 on MI355X: 73 us,
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int6
     float v[VEC];
     unpack8(raw[u], v);
     const Fp8Scale s = fp8_scale(group_amax<16>(v));
-    const u32x2 code = quantise8(v, s.inv);
+    const u32x2 code = quantise8<sizeof(T) == 4>(v, s);
     if (left[u] < 0) continue;
     if (j == 0) scale[row[u] * s_row + blk[u] * s_blk] = s.scale;
     uint8_t *p = y + row[u] * ldy + static_cast<int>(blk[u]) * 128 + j * VEC;

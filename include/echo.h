@@ -624,8 +624,8 @@ int echo_page_step(const echo_page_args *a, void *ws, size_t ws_bytes, void *str
 
 /*
  * FP8 codes of a matrix, with one scale per row and block of 128 columns (the last block may be
- * short): scale = max(largest |x| of the block / 448, 2^-126), y = x / scale rounded to the nearest
- * E4M3FN number.  x has type x_type and row stride ldx, y row stride ldy (both in elements);
+ * short): scale = max(largest |x| of the block / 448, 2^-126), y = the fp32 quotient x / scale rounded to
+ * the nearest E4M3FN number (ties to even).  x has type x_type and row stride ldx, y row stride ldy (both in elements);
  * scale[r * scale_row + b * scale_blk].  What the codes of a block with a NaN or an infinity
  * stand for is NaN.  x and scale are aligned to their types, y to nothing; rows of x on 16 bytes
  * and of y on 8 are fastest.  ECHO_EINVAL for negative sizes, NULL pointers, an unknown type and

@@ -1,8 +1,8 @@
 """FP8 in blocks of 128: echo_quant_fp8 and echo_matmul_fp8 against the oracle in float64.
 
 Tolerances (u = 2^-24).  Scales are one division of fp32 numbers: equal to numpy's.  A code is the
-E4M3FN number nearest to x * fl(448 / amax) rounded, within 3 roundings of x / scale (the two
-divisions and the product): it may be off the nearest number's distance by 4 u |x / scale|.  A
+E4M3FN number nearest to the fp32 quotient x / scale, bit for bit (the last tests here); against the
+quotient in 64 bits it may be off the nearest number's distance by its rounding, 4 u |x / scale| at most.  A
 product sums up to 128 terms in a block, nb blocks and 8 partial sums in fp32; should the matrix
 core cut instead of rounding, each step is off by 2 u: (128 + nb + 8 + 3) * 2 u times the sum of
 the terms' magnitudes, plus half a step of the output's type.
@@ -270,3 +270,87 @@ def test_product_full_size_tiles_exact(m, n, k, kind):
     spread = lambda s: s.double().repeat_interleave(128, 1)[:, :k]
     want = (av * spread(sa)).cuda() @ (bv * spread(sb.repeat_interleave(128, 0)[:n])).cuda().t()
     assert torch.equal(c, want.to(TYPES[kind]))
+
+
+# ---------------------------------------------------------------- codes bit for bit
+def fp32_codes(x, scale):
+    """The fp32 quotient of value and scale (one IEEE division) rounded to the nearest code."""
+    with np.errstate(invalid="ignore"):
+        q = x.astype(np.float32) / np.repeat(scale, 128, 1)[:, :x.shape[1]]
+    return torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+def quotients_at_ties(rng, n):
+    """Blocks whose values over their scale lie on, and a few units in the last place beside, the
+    numbers halfway between two codes; scales from 2^-126 to 2^118."""
+    finite = np.unique(E4M3FN_TABLE[np.isfinite(E4M3FN_TABLE)])
+    ties = ((finite[1:] + finite[:-1]) / 2).astype(np.float32)
+    x = np.zeros((n, 128), np.float32)
+    for r in range(n):
+        d = np.float32(2.0 ** rng.integers(-126, 118) * rng.uniform(1, 2))
+        if r % 3 == 0:                                # few bits, so that products with a tie are exact
+            d = np.float32(2.0 ** rng.integers(-126, 118) * rng.integers(8, 16) / 8 * (1 + rng.integers(-4, 5) * 2.0 ** -23))
+        x[r, 0] = np.float32(448) * d
+        d = x[r, 0] / np.float32(448)
+        v = (rng.choice(ties, 127).astype(np.float64) * d).astype(np.float32)
+        steps = rng.integers(-3, 4, 127).astype(np.int32)
+        v = np.where(np.abs(v) > 1e-44, (v.view(np.int32) + steps).view(np.float32), v)
+        x[r, 1:] = np.clip(v, -x[r, 0], x[r, 0])
+    return x
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,cols", [(70, 1024), (9, 391), (520, 1000)])
+def test_quant_codes_are_the_rounded_quotients(rows, cols, kind):
+    rng = np.random.default_rng(rows)
+    x = torch.from_numpy(rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)) * 2)).to(TYPES[kind])
+    x[1] = -x[0].abs()
+    x[2, ::2], x[2, 1::2] = 0.0, -0.0
+    y = torch.empty((rows, cols), dtype=torch.uint8, device="cuda")
+    scale = torch.empty((rows, -(-cols // 128)), device="cuda")
+    B.quant_fp8(x.cuda(), y, scale)
+    assert np.array_equal(host(y), fp32_codes(x.float().numpy(), host(scale)))
+
+
+def test_quant_codes_beside_ties():
+    x = quotients_at_ties(np.random.default_rng(31), 600)
+    x = np.concatenate([x, np.full((1, 128), 1e-45, np.float32), np.linspace(-1e-38, 1e-38, 128, dtype=np.float32)[None],
+                        np.full((1, 128), 3.4e38, np.float32)])
+    y = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+    scale = torch.empty((len(x), 1), device="cuda")
+    B.quant_fp8(torch.from_numpy(x).cuda(), y, scale)
+    assert np.array_equal(host(scale)[:, 0], np.maximum(np.abs(x).max(1), np.float32(448 * 2.0 ** -126)) / np.float32(448))
+    assert np.array_equal(host(y), fp32_codes(x, host(scale)))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_indexer_codes_are_the_quantisers(kind):
+    """Heads that are neither normed nor turned: the codes of echo_quant_fp8, one scale a head."""
+    rng = np.random.default_rng(7)
+    n, h = 11, 5
+    x = torch.from_numpy(rng.standard_normal((n, h + 1, 128)) * np.exp(rng.standard_normal((n, h + 1, 1)) * 2)).to(TYPES[kind])
+    if kind == "fp32":
+        x.view(-1, 128)[:] = torch.from_numpy(quotients_at_ties(rng, n * (h + 1)))
+    x = x.cuda()
+    codes, scale = torch.empty((n * (h + 1), 128), dtype=torch.uint8, device="cuda"), torch.empty((n * (h + 1), 1), device="cuda")
+    B.quant_fp8(x.view(-1, 128), codes, scale)
+    q8, w_out = torch.empty((n, h, 128), dtype=torch.uint8, device="cuda"), torch.empty((n, h), device="cuda")
+    k8, k_scale = torch.empty((n, 128), dtype=torch.uint8, device="cuda"), torch.empty(n, device="cuda")
+    B.indexer_qk(x[:, :h], x[:, h:], torch.ones((n, h), device="cuda"), q8, w_out, k8, k_scale,
+                 dev(np.arange(n, dtype=np.int64)), torch.zeros(n, dtype=torch.int32, device="cuda"), None)
+    codes, scale = host(codes).reshape(n, h + 1, 128), host(scale).reshape(n, h + 1)
+    assert np.array_equal(host(q8), codes[:, :h]) and np.array_equal(host(w_out), scale[:, :h])
+    assert np.array_equal(host(k8), codes[:, h]) and np.array_equal(host(k_scale), scale[:, h])
+
+
+def test_quant_codes_of_all_significands():
+    """Every fp16 significand over every other's scale (bf16 has fewer), in random binades."""
+    rng = np.random.default_rng(17)
+    x = np.zeros((1024, 9, 128), np.float32)
+    x[:, :, 0] = (8 + np.arange(1024) / 128)[:, None]
+    x[:, :, 1:] = (1 + np.resize(np.arange(1024), 9 * 127) / 1024).reshape(9, 127) * 2.0 ** rng.integers(-9, 3, (1024, 9, 127))
+    x = torch.from_numpy(x.reshape(1024, -1)).half()
+    y = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+    scale = torch.empty((1024, 9), device="cuda")
+    B.quant_fp8(x.cuda(), y, scale)
+    assert np.array_equal(host(y), fp32_codes(x.float().numpy(), host(scale)))
