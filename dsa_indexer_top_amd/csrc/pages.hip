@@ -328,7 +328,9 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
   if (p->page_size < 16 || p->page_size > 65536 || (p->page_size & (p->page_size - 1)))
     return fail(ECHO_EUNSUPPORTED, "echo_page_step: page size %d is not a power of two in [16, 65536]", p->page_size);
   if (p->n_rows > 65535) return fail(ECHO_EUNSUPPORTED, "echo_page_step: %d requests, more than 65535", p->n_rows);
-  if (p->n_rows == 0 && p->max_new == 0) return ECHO_OK;
+  // Without requests and room for tokens a step still has its count and row_begin[0] to write, unless
+  // the call keeps no place for the second apart from the first (arrays may not overlap).
+  if (p->n_rows == 0 && p->max_new == 0 && p->count_out == p->count_in && p->row_begin == p->count_out) return ECHO_OK;
   if (!p->free_list || !p->count_in || !p->count_out || !p->row_begin || !p->status ||
       (p->n_rows && (!p->len_in || !p->new_len || !p->page_table || !p->len_out)) ||
       (p->max_new && (!p->slot || !p->pos)))

@@ -591,7 +591,8 @@ int echo_host_free(void *host);
  * overlap.  Entries of page_table that no page of step 2 takes, and the stack above *count_out
  * except for what step 1 pushed, are left as they were.  A step that cannot be done whole is not
  * done at all: ECHO_ST_NO_PAGES and/or ECHO_ST_BAD_LEN are ORed into *status, lengths and count
- * are copied through, row_begin is 0 and every map entry -1.  The pages in the tables of the
+ * are copied through, row_begin is 0 and every map entry -1.  A step of no requests (n_rows = 0) copies
+ * the count and sets row_begin[0] = 0, whatever max_new is.  The pages in the tables of the
  * requests and on the stack are the caller's: all distinct and in [0, n_pages).
  * Sizes: page_table [n_rows, max_pages], free_list [n_pages], row_begin [n_rows + 1], slot / row /
  * pos [max_new].  Workspace: echo_page_workspace_bytes; two steps that may run at the same time

@@ -225,3 +225,32 @@ def test_captured_steps_advance_on_every_replay(max_new):
         check(got, want, step)
         lens, table, free, count = want["lens"], want["table"], want["free_list"], want["count"]
     g.close()
+
+
+@pytest.mark.parametrize("max_new", [0, 3, 9000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_batch_of_no_requests_keeps_the_count(max_new, in_place):
+    """The batch has drained: the stack's height and row_begin are written all the same, also where
+    the maps have no room either, eagerly and in a replayed graph."""
+    e = np.zeros(0, np.int32)
+    got = run_step(e, e, None, np.zeros((0, 4), np.int32), np.arange(5, dtype=np.int32), 5, 16, max_new, in_place)
+    assert got["count"] == 5 and list(got["row_begin"]) == [0] and got["status"] == 0
+    assert (got["slot"] == -1).all() and (got["pos"] == -1).all()
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    free, count, begin = torch.arange(5, dtype=torch.int32).cuda(), z(1), torch.full((1,), -9, dtype=torch.int32).cuda()
+    out = count if in_place else z(1)
+    slot, pos, status = z(max_new).long(), z(max_new), z(1)
+    ws = torch.empty(B.page_workspace_bytes(0, max_new), dtype=torch.uint8, device="cuda")
+    lens, new, table = z(0), z(0), z(0, 4)
+    main = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = B.CapturedGraph(lambda st: B.page_step(lens, new, table, 16, free, count, lens, out, begin, slot, None, pos,
+                                               status, ws, stream=st), main)
+    for n in (4, 2, 5):
+        count.fill_(n)
+        begin.fill_(-9)
+        torch.cuda.synchronize()
+        g.launch(main)
+        torch.cuda.synchronize()
+        assert int(host(out)[0]) == n and int(host(begin)[0]) == 0
+    g.close()
