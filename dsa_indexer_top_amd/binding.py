@@ -110,6 +110,7 @@ _SIGS = {
                                   I32, P]),
     "echo_qk_norm_rope": (C.c_int, [P, P, I64, I64, P, I64, I64, P]),
     "echo_indexer_qk": (C.c_int, [P, P, I64, F32, P, P, P, P, P, I64, P]),
+    "echo_newest_queries": (C.c_int, [P, P, P, P, I32, I32, I32, P, P, P, P]),
     "echo_host_alloc": (C.c_int, [SZ, C.c_int, C.POINTER(P), C.POINTER(P)]),
     "echo_host_free": (C.c_int, [P]),
 }
@@ -355,7 +356,7 @@ def _calls():
         L = lib()
         m.setup(EchoError, torch._C._cuda_getCurrentRawStream if DEVICE_TYPE == "cuda" else (lambda dev: 0),
                 *(C.cast(getattr(L, "echo_" + n), P).value for n in (
-                    "last_error", "page_step", "quant_fp8", "matmul_fp8", "qk_norm_rope", "indexer_qk")))
+                    "last_error", "page_step", "quant_fp8", "matmul_fp8", "qk_norm_rope", "indexer_qk", "newest_queries")))
         _tensor_calls = m
     return _tensor_calls
 
@@ -405,6 +406,12 @@ def indexer_qk(q, k, w, q8, w_out, k_cache, k_scale, slot, pos, cos_sin, w_mul=1
     _calls().indexer_qk(q, k, pos, cos_sin, rot_begin, interleaved, eps, q_norm, q_weight, q_bias, k_norm,
                         k_weight, k_bias, _handle(stream), DEVICE_TYPE != "cuda", w, q8, w_out, k_cache,
                         k_scale, slot, w_mul)
+
+
+def newest_queries(q8, w, row_begin, key_len, q_out, w_out, len_out, stream=None):
+    """Each request's newest query of a step: q8 [tokens, heads, 128] and w [tokens, heads] by token, row_begin
+    from page_step, to q_out [rows, heads, 128], w_out [rows, heads] and len_out [rows] (0: no token)."""
+    _calls().newest_queries(q8, w, row_begin, key_len, q_out, w_out, len_out, _handle(stream), DEVICE_TYPE != "cuda")
 
 
 class CapturedGraph:

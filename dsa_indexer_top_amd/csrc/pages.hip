@@ -311,6 +311,23 @@ __global__ __launch_bounds__(PF_T) void page_fill_kernel(PageArgs a, int32_t *ws
   }
 }
 
+// A workgroup per request copies its newest token's query and weights (8 KB of 64 heads: launch bound).
+__global__ __launch_bounds__(PF_T) void newest_kernel(const uint8_t *__restrict__ q8, const float *__restrict__ w,
+                                                      const int32_t *__restrict__ row_begin,
+                                                      const int32_t *__restrict__ len, int32_t n_tok, int32_t heads,
+                                                      uint8_t *__restrict__ q_out, float *__restrict__ w_out,
+                                                      int32_t *__restrict__ len_out) {
+  const int32_t r = blockIdx.x, begin = row_begin[r], end = row_begin[r + 1];
+  const bool got = begin >= 0 && begin < end && end <= n_tok;
+  if (threadIdx.x == 0) len_out[r] = got ? len[r] : 0;
+  if (!got) return;
+  const int64_t from = static_cast<int64_t>(end - 1) * heads, to = static_cast<int64_t>(r) * heads;
+  const u32x2 *src = reinterpret_cast<const u32x2 *>(q8 + from * D);
+  u32x2 *dst = reinterpret_cast<u32x2 *>(q_out + to * D);
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(heads) * (D / 8); i += PF_T) dst[i] = src[i];
+  for (int32_t h = threadIdx.x; h < heads; h += PF_T) w_out[to + h] = w[from + h];
+}
+
 }  // namespace echo
 
 using namespace echo;
@@ -357,4 +374,22 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
   if (lds) page_fill_kernel<true><<<fill, PF_T, 0, st>>>(a, w);
   else page_fill_kernel<false><<<fill, PF_T, 0, st>>>(a, w);
   return check_launch("page_step");
+}
+
+extern "C" int echo_newest_queries(const uint8_t *q8, const float *w, const int32_t *row_begin, const int32_t *len,
+                                   int32_t n_rows, int32_t n_tok, int32_t n_q_heads, uint8_t *q_out, float *w_out,
+                                   int32_t *len_out, void *stream) {
+  if (n_rows < 0 || n_tok < 0 || n_q_heads < 0) return fail(ECHO_EINVAL, "echo_newest_queries: negative size");
+  if (n_rows == 0) return ECHO_OK;
+  const bool rows = n_tok && n_q_heads;
+  if (!row_begin || !len || !len_out || (rows && (!q8 || !w)) || (n_q_heads && (!q_out || !w_out)))
+    return fail(ECHO_EINVAL, "echo_newest_queries: NULL pointer");
+  const auto off = [](const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+  if (off(q8, 8) || off(q_out, 8))
+    return fail(ECHO_EUNSUPPORTED, "echo_newest_queries: q8 or q_out is not 8-byte aligned");
+  if (off(w, 4) || off(w_out, 4) || off(row_begin, 4) || off(len, 4) || off(len_out, 4))
+    return fail(ECHO_EINVAL, "echo_newest_queries: a pointer is not aligned to its type");
+  newest_kernel<<<static_cast<uint32_t>(n_rows), PF_T, 0, S(stream)>>>(q8, w, row_begin, len, n_tok, n_q_heads, q_out,
+                                                                      w_out, len_out);
+  return check_launch("newest_queries");
 }

@@ -22,6 +22,7 @@ decltype(&echo_quant_fp8) g_quant = nullptr;
 decltype(&echo_matmul_fp8) g_matmul = nullptr;
 decltype(&echo_qk_norm_rope) g_rope = nullptr;
 decltype(&echo_indexer_qk) g_indexer = nullptr;
+decltype(&echo_newest_queries) g_newest = nullptr;
 
 struct Refused {};                  // a Python error is set
 
@@ -345,10 +346,36 @@ PyObject *indexer_qk(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
   });
 }
 
+PyObject *newest_queries(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, 9, [&] {
+    const char *fn = "echo_newest_queries";
+    const at::Tensor *q8 = tensor(fn, "q8", o[0]), *hw = tensor(fn, "w", o[1]), *begin = tensor(fn, "row_begin", o[2]),
+                     *len = tensor(fn, "key_len", o[3]), *q_out = tensor(fn, "q_out", o[4]),
+                     *w_out = tensor(fn, "w_out", o[5]), *len_out = tensor(fn, "len_out", o[6]);
+    const Where w(fn, q8);
+    if (!is_codes(q8->scalar_type()) || q8->dim() != 3 || q8->size(2) != ECHO_D_INDEX)
+      refuse(fn, "q8 is not FP8 codes [tokens, heads, %d]", ECHO_D_INDEX);
+    const int64_t n_tok = q8->size(0), heads = q8->size(1), n = len->numel();
+    want(w, "q8", q8, q8->scalar_type(), -1);
+    want(w, "w", hw, at::kFloat, n_tok * heads);
+    want(w, "row_begin", begin, at::kInt, n + 1);
+    want(w, "key_len", len, at::kInt, n);
+    if (!is_codes(q_out->scalar_type())) refuse(fn, "q_out is not FP8 codes");
+    want(w, "q_out", q_out, q_out->scalar_type(), n * heads * ECHO_D_INDEX);
+    want(w, "w_out", w_out, at::kFloat, n * heads);
+    want(w, "len_out", len_out, at::kInt, n);
+    check(fn, g_newest(static_cast<const uint8_t *>(address(q8)), static_cast<const float *>(address(hw)),
+                       static_cast<const int32_t *>(address(begin)), static_cast<const int32_t *>(address(len)),
+                       count32(fn, n), count32(fn, n_tok), count32(fn, heads), static_cast<uint8_t *>(address(q_out)),
+                       static_cast<float *>(address(w_out)), static_cast<int32_t *>(address(len_out)),
+                       w.stream(o[7], o[8] == Py_True)));
+  });
+}
+
 // (EchoError, raw_stream, addresses of echo_last_error, echo_page_step, echo_quant_fp8,
-// echo_matmul_fp8, echo_qk_norm_rope, echo_indexer_qk)
+// echo_matmul_fp8, echo_qk_norm_rope, echo_indexer_qk, echo_newest_queries)
 PyObject *setup(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
-  return guarded(n_args, 8, [&] {
+  return guarded(n_args, 9, [&] {
     auto fn = [&](int i) { return reinterpret_cast<void *>(integer(o[i])); };
     Py_INCREF(o[0]);
     Py_INCREF(o[1]);
@@ -360,12 +387,13 @@ PyObject *setup(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
     g_matmul = reinterpret_cast<decltype(g_matmul)>(fn(5));
     g_rope = reinterpret_cast<decltype(g_rope)>(fn(6));
     g_indexer = reinterpret_cast<decltype(g_indexer)>(fn(7));
+    g_newest = reinterpret_cast<decltype(g_newest)>(fn(8));
   });
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(setup), CALL(page_step), CALL(quant_fp8), CALL(matmul_fp8), CALL(qk_norm_rope),
-                         CALL(indexer_qk), {nullptr, nullptr, 0, nullptr}};
+                         CALL(indexer_qk), CALL(newest_queries), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -383,8 +383,9 @@ class PagedIndexerRunner:
     step() enqueues, on one stream and without looking at a length on the host: the step's page maps;
     the hidden states to FP8 and through the key, head-weight and query projections; the key's layer
     norm, both rotations and the FP8 forms, the keys going to their pages.  score() then scores
-    every request's newest query against its pages and selects its top-k, for a step that gave each
-    request one token.  Weights are (codes, scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden],
+    every request's newest query against its pages and selects its top-k; a request that got no token
+    in the step (padding, a finished one, every one of a step that was refused) has no query and
+    selects nothing.  Weights are (codes, scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden],
     ww [64, hidden].  No arithmetic of the method lives here."""
 
     def __init__(self, n_rows, page_size, max_pages, n_pages, max_new, topk, wq, wk, ww, cos_sin,
@@ -406,7 +407,7 @@ class PagedIndexerRunner:
         # one step
         self.new_len = torch.zeros(n_rows, dtype=i32, device=dev)
         self.done = torch.zeros(n_rows, dtype=u8, device=dev)
-        self.row_begin = torch.empty(n_rows + 1, dtype=i32, device=dev)
+        self.row_begin = torch.zeros(n_rows + 1, dtype=i32, device=dev)
         self.slot = torch.empty(max_new, dtype=torch.int64, device=dev)
         self.row = torch.empty(max_new, dtype=i32, device=dev)
         self.pos = torch.empty(max_new, dtype=i32, device=dev)
@@ -423,6 +424,10 @@ class PagedIndexerRunner:
         self.w = torch.empty((max_new, 64), dtype=f32, device=dev)
         self.q8 = torch.empty((max_new, 64, 128), dtype=u8, device=dev)
         self.w_out = torch.empty((max_new, 64), dtype=f32, device=dev)
+        # one query per request, and its keys
+        self.q_last = torch.zeros((n_rows, 64, 128), dtype=u8, device=dev)
+        self.w_last = torch.zeros((n_rows, 64), dtype=f32, device=dev)
+        self.score_len = torch.zeros(n_rows, dtype=i32, device=dev)
         self.scores = torch.empty((n_rows, self.max_len), dtype=f32, device=dev)
         self.idx = torch.empty((n_rows, topk), dtype=i32, device=dev)
         self.ws_topk = torch.empty(max(B.topk_workspace_bytes(n_rows, self.max_len), 256), dtype=u8, device=dev)
@@ -445,8 +450,10 @@ class PagedIndexerRunner:
                      k_bias=self.k_bias, eps=self.eps, stream=stream)
 
     def score(self, stream=None):
-        """Scores and top-k of the step's queries, one per request."""
-        r = self.n_rows
-        B.index_scores_paged(self.q8[:r], self.w_out[:r], self.k, self.k_scale, self.table, self.page_size,
-                             self.lens, self.max_len, self.scores, stream=stream)
-        B.topk(self.scores, self.lens, self.max_len, self.topk, self.idx, self.ws_topk, stream=stream)
+        """Scores and top-k of every request's newest query of the step; a row of idx is -1 throughout
+        for a request that got no token."""
+        B.newest_queries(self.q8, self.w_out, self.row_begin, self.lens, self.q_last, self.w_last, self.score_len,
+                         stream=stream)
+        B.index_scores_paged(self.q_last, self.w_last, self.k, self.k_scale, self.table, self.page_size,
+                             self.score_len, self.max_len, self.scores, stream=stream)
+        B.topk(self.scores, self.score_len, self.max_len, self.topk, self.idx, self.ws_topk, stream=stream)

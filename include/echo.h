@@ -569,8 +569,8 @@ int echo_host_free(void *host);
 /*
  * What a step needs before its scores: the page maps of a paged key cache, the FP8 products that
  * give the indexer's queries and keys, and their norms, rotation and FP8 form.  In the order of a
- * step: echo_page_step, echo_quant_fp8 and echo_matmul_fp8 (projections), echo_indexer_qk, then
- * echo_index_scores_paged.
+ * step: echo_page_step, echo_quant_fp8 and echo_matmul_fp8 (projections), echo_indexer_qk,
+ * echo_newest_queries, then echo_index_scores_paged.
  */
 
 /*
@@ -701,6 +701,19 @@ int echo_qk_norm_rope(const echo_qk_args *a, void *q_out, int64_t qo_tok_stride,
 int echo_indexer_qk(const echo_qk_args *a, const float *w, int64_t w_tok_stride, float w_mul, uint8_t *q8,
                     float *w_out, uint8_t *k_cache, float *k_scale, const int64_t *slot, int64_t n_slots,
                     void *stream);
+
+/*
+ * The queries to score after a step, one per request: where echo_page_step gave request r new tokens
+ * (row_begin[r] < row_begin[r + 1]), its newest one's query and folded weights, rows
+ * row_begin[r + 1] - 1 of q8 [n_tok, n_q_heads, 128] and w [n_tok, n_q_heads], go to rows r of q_out
+ * and w_out, and len_out[r] = len[r], its keys.  A request without new tokens (padding, a finished one,
+ * every one of a refused step) has no query: len_out[r] = 0 and its rows of q_out and w_out are left as
+ * they were.  So is one whose rows are not within [0, n_tok].  Outputs overlap no input; q8 and q_out
+ * are 8-byte aligned.  Pure enqueue; ECHO_EINVAL for negative sizes and NULL pointers.
+ */
+int echo_newest_queries(const uint8_t *q8, const float *w, const int32_t *row_begin, const int32_t *len,
+                        int32_t n_rows, int32_t n_tok, int32_t n_q_heads, uint8_t *q_out, float *w_out,
+                        int32_t *len_out, void *stream);
 
 /* Text of the last error on this thread ("" if none). */
 const char *echo_last_error(void);

@@ -237,3 +237,21 @@ def test_heads_tensor_checks(on_cpu):
     idx("k_cache", k_cache=f(32, 128))
     idx("slot", slot=i32(4))
     idx("slot", slot=f(5, dtype=torch.int64))
+
+
+def test_newest_queries_refusals(on_cpu):
+    def call(q8=F, w=F, begin=F, n=F, rows=4, tok=9, heads=64, qo=F, wo=F, lo=F):
+        return B.lib().echo_newest_queries(q8, w, begin, n, rows, tok, heads, qo, wo, lo, None)
+    assert call(rows=-1) == call(tok=-1) == call(heads=-1) == B.ECHO_EINVAL and "negative" in err()
+    for name in ("q8", "w", "begin", "n", "qo", "wo", "lo"):
+        assert call(**{name: None}) == B.ECHO_EINVAL and "NULL" in err(), name
+    assert call(q8=F + 4) == call(qo=F + 1) == B.ECHO_EUNSUPPORTED
+    assert call(w=F + 2) == call(wo=F + 1) == call(begin=F + 2) == call(n=F + 1) == call(lo=F + 3) == B.ECHO_EINVAL
+    assert call(rows=0) == B.ECHO_OK
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    ok = dict(q8=u8(9, 3, 128), w=torch.zeros(9, 3), row_begin=i32(5), key_len=i32(4), q_out=u8(4, 3, 128),
+              w_out=torch.zeros(4, 3), len_out=i32(4))
+    for bad in (dict(q8=u8(9, 3, 64)), dict(q8=torch.zeros(9, 3, 128)), dict(w=torch.zeros(9, 2)), dict(row_begin=i32(4)),
+                dict(key_len=i32(5)), dict(q_out=u8(3, 3, 128)), dict(w_out=torch.zeros(5, 3)), dict(len_out=i32(3)),
+                dict(q8=u8(18, 3, 128)[::2])):
+        refused("", B.newest_queries, **dict(ok, **bad))

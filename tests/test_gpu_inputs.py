@@ -173,3 +173,106 @@ def test_step_and_scores_as_one_graph():
         for row, n in enumerate(host(a.lens)):
             assert np.array_equal(host(a.scores)[row, :n], host(b.scores)[row, :n]), (i, row)
     g.close()
+
+
+def check_newest(r, book, new):
+    """Every request that got tokens is scored with its newest one's query, the rest select nothing."""
+    q, w, scores, idx = host(r.q8), host(r.w_out), host(r.scores), host(r.idx)
+    ends = np.cumsum(new)
+    for i, rows in enumerate(book.keys):
+        if not new[i]:
+            assert (idx[i] == -1).all(), i
+            continue
+        t = ends[i] - 1
+        k, sc = np.ascontiguousarray(rows[:, :128]), np.ascontiguousarray(rows[:, 128:]).view(np.float32)[:, 0]
+        begin, n = np.zeros(1, np.int64), np.array([len(rows)], np.int32)
+        want = oracle.index_scores(q[t:t + 1], w[t:t + 1], k, sc, begin, n)[0]
+        T = oracle.error_scale(q[t:t + 1], w[t:t + 1], k, sc, begin, n)[0]
+        got = scores[i, :len(rows)]
+        assert (np.abs(got - want) <= 1e-4 * T).all(), i
+        assert np.array_equal(idx[i], oracle.topk_row(got, r.topk)), i
+
+
+def test_scores_of_padded_and_ragged_batches():
+    """Rows without a token (padding, finished, none yet) and chunks of several: no request is scored
+    with another's query."""
+    rng = np.random.default_rng(24)
+    r = make_runner(rng, 4, 20, 64, 24)
+    book = Book(r)
+    for new, done in [([9, 0, 12, 30], [0, 0, 0, 0]), ([1, 0, 1, 1], [0, 0, 0, 0]), ([0, 5, 0, 1], [0, 0, 1, 0]),
+                      ([0, 0, 0, 0], [0, 0, 0, 0]), ([0, 1, 20, 1], [1, 0, 0, 0]), ([1, 1, 1, 1], [0, 0, 0, 0])]:
+        announce("padded step", new, done)
+        feed(r, rng, new, done)
+        r.step()
+        book.step(r, new, done)
+        r.score()
+        check_newest(r, book, new)
+
+
+def test_a_refused_step_selects_nothing():
+    """Too few pages: nothing is handed out, and no stale query is scored; the next step is whole."""
+    rng = np.random.default_rng(25)
+    r = make_runner(rng, 3, 4, 90, 8)
+    book = Book(r)
+    feed(r, rng, [20, 1, 3], [0, 0, 0])               # four pages of 16
+    r.step()
+    book.step(r, [20, 1, 3], [0, 0, 0])
+    r.score()
+    check_newest(r, book, [20, 1, 3])
+    feed(r, rng, [1, 30, 1], [0, 0, 0])
+    r.step()
+    r.score()
+    assert int(host(r.status)[0]) == B.ST_NO_PAGES and (host(r.idx) == -1).all()
+    assert np.array_equal(host(r.lens), book.state["lens"])
+    feed(r, rng, [1, 1, 1], [0, 0, 0])
+    r.step()
+    book.step(r, [1, 1, 1], [0, 0, 0])
+    r.score()
+    check_newest(r, book, [1, 1, 1])
+
+
+def test_padded_scores_in_a_graph():
+    """Steps with padding rows replayed from one graph: equal to eager steps of a second runner."""
+    a = make_runner(np.random.default_rng(6), 4, 20, 24, 16)
+    b = make_runner(np.random.default_rng(6), 4, 20, 24, 16)
+    main = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def both(stream):
+        a.step(stream)
+        a.score(stream)
+
+    g = B.CapturedGraph(both, main)
+    for i, (new, done) in enumerate([([5, 0, 9, 3], [0] * 4), ([1, 0, 0, 1], [0] * 4), ([0, 1, 1, 0], [0] * 4),
+                                     ([1, 1, 0, 1], [0, 0, 1, 0]), ([0, 0, 0, 0], [0] * 4)]):
+        for r in (a, b):
+            feed(r, np.random.default_rng(40 + i), new, done)
+        torch.cuda.synchronize()
+        g.launch(main)
+        torch.cuda.synchronize()
+        b.step()
+        b.score()
+        for name in ("lens", "table", "idx", "q_last", "w_last", "score_len"):
+            assert np.array_equal(host(getattr(a, name)), host(getattr(b, name))), (i, name)
+        assert ((host(a.idx) >= 0).any(1) == (np.array(new) > 0)).all()
+    g.close()
+
+
+@pytest.mark.parametrize("heads", [0, 1, 3, 64])
+def test_newest_queries_of_any_rows(heads):
+    """Requests without tokens, and rows that reach behind the tokens there are, have length 0 and
+    leave their outputs alone."""
+    rng = np.random.default_rng(heads)
+    n_tok = 11
+    q, w = rng.integers(0, 256, (n_tok, heads, 128), dtype=np.uint8), rng.standard_normal((n_tok, heads)).astype(np.float32)
+    begin = np.array([0, 0, 4, 5, 11, 11, 12, -3, -1], np.int32)
+    lens = rng.integers(1, 100, 8).astype(np.int32)
+    q_out = torch.full((8, heads, 128), 0xEE, dtype=torch.uint8, device="cuda")
+    w_out = torch.full((8, heads), -77.0, device="cuda")
+    len_out = torch.full((8,), -9, dtype=torch.int32, device="cuda")
+    B.newest_queries(dev(q), dev(w), dev(begin), dev(lens), q_out, w_out, len_out)
+    got = np.array([0, 1, 1, 1, 0, 0, 0, 0], bool)
+    assert np.array_equal(host(len_out), np.where(got, lens, 0))
+    last = begin[1:][got] - 1
+    assert np.array_equal(host(q_out)[got], q[last]) and np.array_equal(host(w_out)[got], w[last])
+    assert (host(q_out)[~got] == 0xEE).all() and (host(w_out)[~got] == -77).all()
