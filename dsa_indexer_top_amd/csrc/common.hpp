@@ -22,6 +22,24 @@ int check_launch(const char *what);
 
 inline hipStream_t S(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
+// Whether two of the items of `size` elements at i * si + j * sj, i < n and j < m, share an element.
+// Nested strides are told apart at once; where one dimension's items lie between the other's, the
+// nearest pair is looked for (sizes above 2^16 in both dimensions count as shared there).
+inline bool rows_overlap(int64_t n, int64_t si, int64_t m, int64_t sj, int64_t size) {
+  if ((n > 1 && si < size) || (m > 1 && sj < size)) return true;
+  if (n < 2 || m < 2) return false;
+  typedef __int128 wide;                                   // no product of strides and sizes overflows
+  if (sj >= static_cast<wide>(n - 1) * si + size || si >= static_cast<wide>(m - 1) * sj + size) return false;
+  if (n < m) { const int64_t c = n, s = si; n = m; si = sj; m = c; sj = s; }
+  if (m > 1 << 16) return true;
+  for (int64_t j = 1; j < m; ++j) {                        // items j apart in one dimension, i in the other
+    const wide d = static_cast<wide>(j) * sj, i = d / si;
+    if (i < n && d - i * si < size) return true;
+    if (i + 1 < n && (i + 1) * si - d < size) return true;
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------- ordering keys
 // Order-preserving map of a float to uint32: a < b  <=>  key(a) < key(b); -0.0 is folded onto
 // +0.0 first so the two compare equal (ties then go to the lower index).

@@ -349,10 +349,12 @@ extern "C" int echo_qk_norm_rope(const echo_qk_args *q, void *q_out, int64_t qo_
       (q->n_k_heads && (misaligned(k_out, 16) || ko_tok_stride % vec || ko_head_stride % vec)))
     return fail(ECHO_EUNSUPPORTED, "echo_qk_norm_rope: an output or its stride is not a multiple of 16 bytes");
   const auto overlaps = [&](int32_t heads, int64_t tok, int64_t head) {
-    return (heads > 1 && head < q->head_dim) || (heads > 0 && q->n_tok > 1 && tok < q->head_dim);
+    return heads > 0 && rows_overlap(q->n_tok, tok, heads, head, q->head_dim);
   };
-  if (overlaps(q->n_q_heads, qo_tok_stride, qo_head_stride) || overlaps(q->n_k_heads, ko_tok_stride, ko_head_stride))
-    return fail(ECHO_EINVAL, "echo_qk_norm_rope: output heads overlap");
+  if (overlaps(q->n_q_heads, qo_tok_stride, qo_head_stride))
+    return fail(ECHO_EINVAL, "echo_qk_norm_rope: the heads of q_out overlap");
+  if (overlaps(q->n_k_heads, ko_tok_stride, ko_head_stride))
+    return fail(ECHO_EINVAL, "echo_qk_norm_rope: the heads of k_out overlap");
   HeadArgs a = head_args(q);
   a.side[0].y = q_out; a.side[0].yt = qo_tok_stride; a.side[0].yh = qo_head_stride;
   a.side[1].y = k_out; a.side[1].yt = ko_tok_stride; a.side[1].yh = ko_head_stride;

@@ -255,3 +255,26 @@ def test_newest_queries_refusals(on_cpu):
                 dict(key_len=i32(5)), dict(q_out=u8(3, 3, 128)), dict(w_out=torch.zeros(5, 3)), dict(len_out=i32(3)),
                 dict(q8=u8(18, 3, 128)[::2])):
         refused("", B.newest_queries, **dict(ok, **bad))
+
+
+def shared(n, si, m, sj, size):
+    """Whether two of the items at i * si + j * sj share one of their `size` places, one by one."""
+    places = [i * si + j * sj + p for i in range(n) for j in range(m) for p in range(size)]
+    return len(set(places)) < len(places)
+
+
+def test_output_heads_that_overlap():
+    """Strides that step over a head each and meet together are refused, those whose heads lie between
+    one another are not (such a call gets as far as the key side, which overlaps here)."""
+    def q_overlaps(n, st, h, sh, dim=16):
+        a = qk_args(n_tok=n, n_q_heads=h, head_dim=dim, n_k_heads=2, rot_dim=0, cos_sin=0)
+        assert B.lib().echo_qk_norm_rope(a, F, st, sh, F, 1024, 0, None) == B.ECHO_EINVAL and "overlap" in err()
+        return "q_out" in err()
+    for n in (1, 2, 3, 5):
+        for h in (1, 2, 4):
+            for st in range(0, 104, 8):
+                for sh in range(0, 104, 8):
+                    assert q_overlaps(n, st, h, sh) == shared(n, st, h, sh, 16), (n, st, h, sh)
+    assert q_overlaps(4, 1 << 40, 8, 1 << 40) and q_overlaps(3, 3 << 39, 4, 1 << 40)
+    assert not q_overlaps(1 << 20, 1 << 40, 8, 1 << 61) and not q_overlaps(100, 1 << 40, 8, 16)
+    assert q_overlaps(4, -128, 8, 16) and q_overlaps(4, 128, 8, -16)
