@@ -99,8 +99,9 @@ extern "C" int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int
   if (n_cols > (1 << 30)) return fail(ECHO_EUNSUPPORTED, "echo_quant_fp8: more than 2^30 columns");
   const int64_t n_blk = (static_cast<int64_t>(n_cols) + 127) / 128;
   if (n_rows >= (1 << 30) / n_blk) return fail(ECHO_EUNSUPPORTED, "echo_quant_fp8: 2^30 blocks or more");
-  if ((n_rows > 1 && scale_row < 1) || (n_blk > 1 && scale_blk < 1))
-    return fail(ECHO_EINVAL, "echo_quant_fp8: scale stride below 1");
+  if (rows_overlap(n_rows, scale_row, n_blk, scale_blk, 1))
+    return fail(ECHO_EINVAL, "echo_quant_fp8: scales overlap (strides %lld and %lld)", static_cast<long long>(scale_row),
+                static_cast<long long>(scale_blk));
   const size_t size = x_type == ECHO_FP32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(x) % size || reinterpret_cast<uintptr_t>(scale) % 4)
     return fail(ECHO_EINVAL, "echo_quant_fp8: x or scale not aligned to its type");

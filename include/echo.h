@@ -630,7 +630,8 @@ int echo_page_step(const echo_page_args *a, void *ws, size_t ws_bytes, void *str
  * scale[r * scale_row + b * scale_blk].  What the codes of a block with a NaN or an infinity
  * stand for is NaN.  x and scale are aligned to their types, y to nothing; rows of x on 16 bytes
  * and of y on 8 are fastest.  ECHO_EINVAL for negative sizes, NULL pointers, an unknown type and
- * strides that make rows overlap; ECHO_EUNSUPPORTED above 2^30 columns or from 2^30 blocks on.  No rows or columns: ECHO_OK.
+ * strides that make rows or scales overlap; ECHO_EUNSUPPORTED above 2^30 columns or from 2^30 blocks on.
+ * No rows or columns: ECHO_OK.
  */
 int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols, int64_t ldx, uint8_t *y,
                    int64_t ldy, float *scale, int64_t scale_row, int64_t scale_blk, void *stream);

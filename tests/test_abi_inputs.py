@@ -278,3 +278,16 @@ def test_output_heads_that_overlap():
     assert q_overlaps(4, 1 << 40, 8, 1 << 40) and q_overlaps(3, 3 << 39, 4, 1 << 40)
     assert not q_overlaps(1 << 20, 1 << 40, 8, 1 << 61) and not q_overlaps(100, 1 << 40, 8, 16)
     assert q_overlaps(4, -128, 8, 16) and q_overlaps(4, 128, 8, -16)
+
+
+def test_scales_that_overlap():
+    """Scale strides are checked together; those that keep every scale apart get as far as the check of
+    the addresses, which are odd here."""
+    for rows in (1, 2, 3, 7):
+        for blocks in (1, 2, 4, 5):
+            for sr in range(0, 9):
+                for sb in range(0, 9):
+                    rc = B.lib().echo_quant_fp8(F, B.BF16, rows, 128 * blocks, 1024, F, 1024, F + 1, sr, sb, None)
+                    assert rc == B.ECHO_EINVAL
+                    assert ("overlap" in err()) == shared(rows, sr, blocks, sb, 1), (rows, blocks, sr, sb)
+                    assert "overlap" in err() or "aligned" in err()
