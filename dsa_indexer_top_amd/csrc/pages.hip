@@ -352,6 +352,11 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
       (p->n_rows && (!p->len_in || !p->new_len || !p->page_table || !p->len_out)) ||
       (p->max_new && (!p->slot || !p->pos)))
     return fail(ECHO_EINVAL, "echo_page_step: NULL pointer");
+  uintptr_t bits = reinterpret_cast<uintptr_t>(p->slot) % 8 ? 1 : 0;
+  const int32_t *const words[] = {p->len_in, p->new_len, p->page_table, p->free_list, p->count_in, p->len_out,
+                                  p->count_out, p->row_begin, p->row, p->pos, p->status};
+  for (const int32_t *q : words) bits |= reinterpret_cast<uintptr_t>(q) % 4;
+  if (bits) return fail(ECHO_EINVAL, "echo_page_step: an array is not aligned to its type");
   PageArgs a = {p->n_rows, __builtin_ctz(p->page_size), p->max_pages, p->n_pages, p->max_new, p->len_in, p->new_len,
                 p->done, p->page_table, p->free_list, p->count_in, p->len_out, p->count_out, p->row_begin, p->slot,
                 p->row, p->pos, p->status};
@@ -363,6 +368,7 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
   if (!ws || ws_bytes < echo_page_workspace_bytes(p->n_rows, p->max_new))
     return fail(ECHO_EWORKSPACE, "echo_page_step: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
                 echo_page_workspace_bytes(p->n_rows, p->max_new));
+  if (reinterpret_cast<uintptr_t>(ws) % 4) return fail(ECHO_EINVAL, "echo_page_step: workspace is not 4-byte aligned");
   int32_t *w = static_cast<int32_t *>(ws);
   const bool lds = p->n_rows <= PG_ONE_ROWS;
   if (lds)

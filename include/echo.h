@@ -596,9 +596,9 @@ int echo_host_free(void *host);
  * requests and on the stack are the caller's: all distinct and in [0, n_pages).
  * Sizes: page_table [n_rows, max_pages], free_list [n_pages], row_begin [n_rows + 1], slot / row /
  * pos [max_new].  Workspace: echo_page_workspace_bytes; two steps that may run at the same time
- * (two graphs, two streams) need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes and
- * NULL pointers, ECHO_EUNSUPPORTED for other page sizes and for more than 65535 requests,
- * ECHO_EWORKSPACE for a short workspace.
+ * (two graphs, two streams) need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, NULL
+ * pointers and arrays or a workspace not aligned to their types (4 bytes), ECHO_EUNSUPPORTED for other
+ * page sizes and for more than 65535 requests, ECHO_EWORKSPACE for a short workspace.
  */
 typedef struct {
   int32_t n_rows;

@@ -291,3 +291,17 @@ def test_scales_that_overlap():
                     assert rc == B.ECHO_EINVAL
                     assert ("overlap" in err()) == shared(rows, sr, blocks, sb, 1), (rows, blocks, sr, sb)
                     assert "overlap" in err() or "aligned" in err()
+
+
+def test_page_step_alignment(on_cpu):
+    """The workspace, where one is used, and every array are aligned to their types."""
+    call = lambda ws=F, **kw: B.lib().echo_page_step(page_args(**kw), ws, 1 << 20, None)
+    for n in (1, 2, 3):
+        assert call(ws=F + n, max_new=9000) == call(ws=F + n, n_rows=3000) == B.ECHO_EINVAL and "aligned" in err()
+    for name in ("len_in", "new_len", "page_table", "free_list", "count_in", "len_out", "count_out", "row_begin",
+                 "row", "pos", "status"):
+        assert call(**{name: F + 2}) == B.ECHO_EINVAL and "aligned" in err(), name
+    assert call(slot=F + 4) == B.ECHO_EINVAL
+    ws = torch.zeros(B.page_workspace_bytes(3, 9000) + 8, dtype=torch.uint8)[1:]
+    big = dict(slot=torch.zeros(9000, dtype=torch.int64), row=i32(9000), pos=i32(9000))
+    refused("aligned", B.page_step, **page_tensors(ws=ws, **big))
