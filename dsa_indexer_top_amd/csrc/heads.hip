@@ -304,7 +304,7 @@ static int check_heads(const char *fn, const echo_qk_args *q, bool *empty) {
     return fail(ECHO_EINVAL, "%s: the rotated part ends behind the head", fn);
   if (!(q->eps >= 0.f)) return fail(ECHO_EINVAL, "%s: eps below 0", fn);
   if (q->n_tok == 0 || (q->n_q_heads == 0 && q->n_k_heads == 0)) { *empty = true; return ECHO_OK; }
-  if (!q->pos || (q->n_q_heads && !q->q) || (q->n_k_heads && !q->k) || (q->rot_dim && !q->cos_sin))
+  if (!q->pos || (q->n_q_heads && !q->q) || (q->n_k_heads && !q->k) || (q->rot_dim && q->n_pos && !q->cos_sin))
     return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
   const int64_t most = 0x7FFFFFFF - 65536;
   if (static_cast<int64_t>(q->n_tok) * q->n_q_heads > most || static_cast<int64_t>(q->n_tok) * q->n_k_heads > most)
@@ -371,7 +371,7 @@ extern "C" int echo_indexer_qk(const echo_qk_args *q, const float *w, int64_t w_
   if (q->n_k_heads > 1) return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: %d key heads; a token has one key", q->n_k_heads);
   if (n_slots < 0) return fail(ECHO_EINVAL, "echo_indexer_qk: negative size");
   if (empty) return ECHO_OK;
-  if ((q->n_q_heads && (!w || !q8 || !w_out)) || (q->n_k_heads && (!k_cache || !k_scale || !slot)))
+  if ((q->n_q_heads && (!w || !q8 || !w_out)) || (q->n_k_heads && ((n_slots && (!k_cache || !k_scale)) || !slot)))
     return fail(ECHO_EINVAL, "echo_indexer_qk: NULL pointer");
   if (misaligned(q8, 8) || misaligned(k_cache, 8))
     return fail(ECHO_EUNSUPPORTED, "echo_indexer_qk: q8 or k_cache is not 8-byte aligned");

@@ -348,8 +348,8 @@ extern "C" int echo_page_step(const echo_page_args *p, void *ws, size_t ws_bytes
   // Without requests and room for tokens a step still has its count and row_begin[0] to write, unless
   // the call keeps no place for the second apart from the first (arrays may not overlap).
   if (p->n_rows == 0 && p->max_new == 0 && p->count_out == p->count_in && p->row_begin == p->count_out) return ECHO_OK;
-  if (!p->free_list || !p->count_in || !p->count_out || !p->row_begin || !p->status ||
-      (p->n_rows && (!p->len_in || !p->new_len || !p->page_table || !p->len_out)) ||
+  if ((p->n_pages && !p->free_list) || !p->count_in || !p->count_out || !p->row_begin || !p->status ||
+      (p->n_rows && (!p->len_in || !p->new_len || (p->max_pages && !p->page_table) || !p->len_out)) ||
       (p->max_new && (!p->slot || !p->pos)))
     return fail(ECHO_EINVAL, "echo_page_step: NULL pointer");
   uintptr_t bits = reinterpret_cast<uintptr_t>(p->slot) % 8 ? 1 : 0;

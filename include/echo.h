@@ -598,7 +598,8 @@ int echo_host_free(void *host);
  * pos [max_new].  Workspace: echo_page_workspace_bytes; two steps that may run at the same time
  * (two graphs, two streams) need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, NULL
  * pointers and arrays or a workspace not aligned to their types (4 bytes), ECHO_EUNSUPPORTED for other
- * page sizes and for more than 65535 requests, ECHO_EWORKSPACE for a short workspace.
+ * page sizes and for more than 65535 requests, ECHO_EWORKSPACE for a short workspace.  An array of no
+ * entries may be NULL.
  */
 typedef struct {
   int32_t n_rows;
@@ -671,7 +672,8 @@ int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t
  * up to 256, rot_dim (0: none, cos_sin may be NULL) a multiple of 16, rot_begin of 8; pointers and
  * strides of q, k, cos_sin, weights and outputs are multiples of 16 bytes; anything else is
  * ECHO_EUNSUPPORTED, as are more than 2^31 - 2^16 heads in all.  ECHO_EINVAL for negative sizes,
- * NULL pointers, an unknown type or norm, a rotated part behind the head's end, eps below 0 or NaN.
+ * NULL pointers (where there is something to read or write), an unknown type or norm, a rotated part
+ * behind the head's end, eps below 0 or NaN.
  */
 typedef struct {
   int32_t n_tok, n_q_heads, n_k_heads, head_dim;

@@ -289,3 +289,18 @@ def test_captured_heads_on_another_stream(n):
         for x, y in zip(a, b):
             assert np.array_equal(host(x), host(y)), step
     g.close()
+
+
+def test_no_positions_and_no_slots():
+    """A table of no positions makes every token padding; a cache of no rows takes no key."""
+    q, k = torch.ones((3, 2, 128), device="cuda"), torch.ones((3, 1, 128), device="cuda")
+    pos, slot = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    full = lambda *s: torch.full(s, -77.0, device="cuda")
+    codes = lambda *s: torch.full(s, 0xEE, dtype=torch.uint8, device="cuda")
+    qo, ko = full(3, 2, 128), full(3, 1, 128)
+    B.qk_norm_rope(q, k, qo, ko, pos, torch.zeros((0, 64), device="cuda"))
+    assert (f64(qo) == -77).all() and (f64(ko) == -77).all()
+    q8, w_out = codes(3, 2, 128), full(3, 2)
+    B.indexer_qk(q, k, torch.ones((3, 2), device="cuda"), q8, w_out, codes(0, 128), full(0), slot, pos, None)
+    assert (host(q8) == 0x7E).all()                   # 448: every value is the largest
+    assert np.array_equal(host(w_out), np.full((3, 2), np.float32(1) / np.float32(448)))

@@ -254,3 +254,22 @@ def test_a_batch_of_no_requests_keeps_the_count(max_new, in_place):
         torch.cuda.synchronize()
         assert int(host(out)[0]) == n and int(host(begin)[0]) == 0
     g.close()
+
+
+@pytest.mark.parametrize("max_new", [4, 9000])
+def test_no_pages_at_all(max_new):
+    """A pool without pages and tables without columns (tensors of no elements): steps that need none
+    go through, others are refused as any step that needs too many."""
+    z, none = np.zeros(3, np.int32), np.zeros(0, np.int32)
+    for table, free in ((np.zeros((3, 0), np.int32), none), (np.zeros((3, 2), np.int32), none),
+                        (np.zeros((3, 0), np.int32), np.arange(4, dtype=np.int32))):
+        n = len(free)
+        want = O.page_step(z, z, z, table, free, n, 16, max_new)
+        assert want["status"] == 0
+        check(run_step(z, z, z.astype(np.uint8), table, free, n, 16, max_new), want)
+        new = np.array([0, 1, 0], np.int32)
+        want = O.page_step(z, new, z, table, free, n, 16, max_new)
+        got = run_step(z, new, None, table, free, n, 16, max_new)
+        assert want["status"] and got["status"] & want["status"]
+        want["status"] = got["status"]
+        check(got, want)
