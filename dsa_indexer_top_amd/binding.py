@@ -9,8 +9,6 @@ used only to hold device memory and to name streams.  If the library is missing 
 import ctypes as C
 import os
 
-import torch
-
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libecho.so")
 
@@ -352,6 +350,7 @@ def _calls():
     """The native module, set up with this library's functions; raises if it has not been built."""
     global _tensor_calls
     if _tensor_calls is None:
+        import torch
         from . import _tensor_calls as m
         L = lib()
         m.setup(EchoError, torch._C._cuda_getCurrentRawStream if DEVICE_TYPE == "cuda" else (lambda dev: 0),
