@@ -68,13 +68,13 @@ def build(verbose=False):
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         calls = ex.submit(_tensor_calls)
         objs = list(ex.map(_compile, srcs))
-        calls.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp] + objs
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), p.stderr))
     os.replace(tmp, OUT)
+    calls.result()                           # its failure leaves the library, which needs neither it nor torch
     if verbose:
         print("built", OUT, CALLS)
     return OUT
