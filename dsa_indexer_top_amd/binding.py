@@ -106,6 +106,7 @@ _SIGS = {
     "echo_quant_fp8": (C.c_int, [P, I32, I64, I32, I64, P, I64, P, I64, I64, P]),
     "echo_matmul_fp8": (C.c_int, [P, I64, P, I64, I64, P, I64, P, I64, I64, I32, I32, I32, P, I64,
                                   I32, P]),
+    "echo_matmul_fp8_form": (C.c_char_p, [I32, I32, I32, I32]),
     "echo_qk_norm_rope": (C.c_int, [P, P, I64, I64, P, I64, I64, P]),
     "echo_indexer_qk": (C.c_int, [P, P, I64, F32, P, P, P, P, P, I64, P]),
     "echo_newest_queries": (C.c_int, [P, P, P, P, I32, I32, I32, P, P, P, P]),
@@ -385,6 +386,11 @@ def matmul_fp8(a, a_scale, b, b_scale, c, stream=None):
     """c [m, n] = a [m, k] times b [n, k] transposed, FP8 codes with fp32 scales: a_scale [m,
     ceil(k / 128)] and b_scale [ceil(n / 128), ceil(k / 128)], any strides."""
     _calls().matmul_fp8(a, a_scale, b, b_scale, c, _handle(stream), DEVICE_TYPE != "cuda")
+
+
+def matmul_fp8_form(m, n, k, c_type):
+    """Name of the kernel that a product of these sizes takes (echo_matmul_fp8_form)."""
+    return lib().echo_matmul_fp8_form(m, n, k, c_type).decode()
 
 
 def qk_norm_rope(q, k, q_out, k_out, pos, cos_sin, rot_begin=0, interleaved=False, q_norm=NORM_NONE,

@@ -646,44 +646,60 @@ static void launch_tiles(const MatArgs &a, hipStream_t st) {
   matmul_tile_kernel<T, BM, BN, WM, WN, STAGES><<<tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
 }
 
+// The kernels a product can take.
+enum Form { FEW_16_16, FEW_32_16, FEW_32_32, SPLIT_64, TILE_64, TILE_64_128, TILE_128_ONE, TILE_128, TILE_256 };
+static const char *const FORM_NAMES[] = {"few 16x16", "few 32x16", "few 32x32", "split 64x64", "tile 64x64",
+                                         "tile 64x128", "tile 128x128, 3 stages", "tile 128x128", "tile 256x256"};
+
+static uint32_t cdiv(int32_t x, int32_t y) { return static_cast<uint32_t>((static_cast<int64_t>(x) + y - 1) / y); }
+
+// The smallest tile that gives each of the 256 CUs at most one: below that, what a CU can load is what
+// takes the time.  All times are us on MI355X, in bf16 unless said.
+static Form form_of(int32_t m, int32_t n, int32_t k, bool fp32) {
+  const auto tiles = [&](int bm, int bn) { return static_cast<int64_t>(cdiv(m, bm)) * cdiv(n, bn); };
+  if (m <= 16 || tiles(16, 16) <= 256) return FEW_16_16;       // 116 x 100 x 6000: 6.4, split 64 x 64 tiles 10.5
+  if ((m <= 32 && n < 256 * 32) || tiles(32, 16) <= 256) return FEW_32_16;   // 64 x 2048 x 6000: 9.3, 10.6 and
+                                                               // 14.0 in 16 x 16 and 64 x 64
+  if (m <= 32 || tiles(32, 32) <= 256) return FEW_32_32;       // 512 x 512 x 6000: 12.5 and 16.5 in 64 x 64,
+                                                               // 600 x 530 x 2048, more than 256: 10.8 and 6.3
+  // The split form's waves share out the scale blocks (700 x 700 x 4000: 12.3, with shared stages 13.0; fp32
+  // 14.6 and 19.4) unless there are hardly more than waves (1000 x 1000 x 300: 4.5 and 4.2).
+  if (tiles(64, 64) <= 256) return k > 5 * 128 ? SPLIT_64 : TILE_64;
+  if (tiles(64, 128) <= 256) return TILE_64_128;               // 1728 x 640 x 5000: 21.3, 26.2 in 64 x 64
+  // fp32 results hold their operands as bf16: too many registers for the largest tile, and always
+  // two stages (2112 x 1024 x 2048: 20.6, 22.1 with three)
+  if (fp32) return TILE_128;
+  // One 128 x 128 tile a CU wants a third stage (2000 x 2000 x 5000: 31.7, 41.9 with two), more a
+  // second workgroup (2500 x 3000 x 5000: 50.5 with two stages, 59.7 with three).  From two a CU
+  // 256 x 256 tiles are faster (5117 x 2046 x 5000: 67.9 and 89.5) unless their last round leaves
+  // more than a quarter of the CUs without one (280 tiles, 5117 x 3582 x 2048: 58.7 and 50.7; 448
+  // tiles, 7165 x 4094 x 2048: 64.7 and 75.1).
+  if (tiles(128, 128) <= 256) return TILE_128_ONE;
+  const int64_t big = tiles(256, 256), rounds = (big + 255) / 256;
+  return tiles(128, 128) > 512 && (rounds == 1 || big >= rounds * 192) ? TILE_256 : TILE_128;
+}
+
 template <typename T>
 static int launch_matmul(const MatArgs &a, hipStream_t st) {
-  const auto cdiv = [](int32_t x, int32_t y) { return static_cast<uint32_t>((static_cast<int64_t>(x) + y - 1) / y); };
-  const auto tiles = [&](int bm, int bn) { return static_cast<int64_t>(cdiv(a.m, bm)) * cdiv(a.n, bn); };
   const auto few = [&](auto mt, auto nt) {
     constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value;
     matmul_few_kernel<T, MT, NT><<<dim3(cdiv(a.n, 16 * NT), cdiv(a.m, 16 * MT)), SW * 64, 0, st>>>(a);
   };
-  // The smallest tile that gives each of the 256 CUs at most one: below that, what a CU can load is
-  // what takes the time.  All times are us on MI355X, in bf16 unless said.
-  if (a.m <= 16 || tiles(16, 16) <= 256) {               // 116 x 100 x 6000: 6.4, split 64 x 64 tiles 10.5
-    few(Int<1>{}, Int<1>{});
-  } else if ((a.m <= 32 && a.n < 256 * 32) || tiles(32, 16) <= 256) {
-    few(Int<2>{}, Int<1>{});                             // 64 x 2048 x 6000: 9.3, 10.6 and 14.0 in 16 x 16 and 64 x 64
-  } else if (a.m <= 32 || tiles(32, 32) <= 256) {        // 512 x 512 x 6000: 12.5 and 16.5 in 64 x 64,
-    few(Int<2>{}, Int<2>{});                             // 600 x 530 x 2048, more than 256: 10.8 and 6.3
-  } else if (tiles(64, 64) <= 256) {
-    // Its waves share out the scale blocks (700 x 700 x 4000: 12.3, with shared stages 13.0; fp32 14.6
-    // and 19.4) unless there are hardly more than waves (1000 x 1000 x 300: 4.5 and 4.2).
-    if (a.k > 5 * 128) matmul_split_kernel<T, 4, 2><<<static_cast<uint32_t>(tiles(64, 64)), 256, 0, st>>>(a);
-    else launch_tiles<T, 64, 64, 32, 32, 4>(a, st);
-  } else if (tiles(64, 128) <= 256) {                    // 1728 x 640 x 5000: 21.3, 26.2 in 64 x 64
-    launch_tiles<T, 64, 128, 32, 64, 3>(a, st);
-  } else {
-    bool done = false;
-    if constexpr (sizeof(T) == 2) {
-      // One 128 x 128 tile a CU wants a third stage (2000 x 2000 x 5000: 31.7, 41.9 with two), more a
-      // second workgroup (2500 x 3000 x 5000: 50.5 with two stages, 59.7 with three).  From two a CU
-      // 256 x 256 tiles are faster (5117 x 2046 x 5000: 67.9 and 89.5) unless their last round leaves
-      // more than a quarter of the CUs without one (280 tiles, 5117 x 3582 x 2048: 58.7 and 50.7; 448
-      // tiles, 7165 x 4094 x 2048: 64.7 and 75.1).
-      const int64_t big = tiles(256, 256), rounds = (big + 255) / 256;
-      if ((done = tiles(128, 128) <= 256)) launch_tiles<T, 128, 128, 64, 64, 3>(a, st);
-      else if ((done = tiles(128, 128) > 512 && (rounds == 1 || big >= rounds * 192))) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
-    }
-    // fp32 results hold their operands as bf16: too many registers for the largest tile, and always
-    // two stages (2112 x 1024 x 2048: 20.6, 22.1 with three)
-    if (!done) launch_tiles<T, 128, 128, 64, 64, 2>(a, st);
+  constexpr bool FP32 = sizeof(T) == 4;
+  switch (form_of(a.m, a.n, a.k, FP32)) {
+    case FEW_16_16: few(Int<1>{}, Int<1>{}); break;
+    case FEW_32_16: few(Int<2>{}, Int<1>{}); break;
+    case FEW_32_32: few(Int<2>{}, Int<2>{}); break;
+    case SPLIT_64: matmul_split_kernel<T, 4, 2><<<cdiv(a.m, 64) * cdiv(a.n, 64), 256, 0, st>>>(a); break;
+    case TILE_64: launch_tiles<T, 64, 64, 32, 32, 4>(a, st); break;
+    case TILE_64_128: launch_tiles<T, 64, 128, 32, 64, 3>(a, st); break;
+    case TILE_128: launch_tiles<T, 128, 128, 64, 64, 2>(a, st); break;
+    case TILE_128_ONE:
+      if constexpr (!FP32) launch_tiles<T, 128, 128, 64, 64, 3>(a, st);
+      break;
+    case TILE_256:
+      if constexpr (!FP32) launch_tiles<T, 256, 256, 64, 128, 2>(a, st);
+      break;
   }
   return check_launch("matmul_fp8");
 }
@@ -691,6 +707,10 @@ static int launch_matmul(const MatArgs &a, hipStream_t st) {
 }  // namespace echo
 
 using namespace echo;
+
+extern "C" const char *echo_matmul_fp8_form(int32_t m, int32_t n, int32_t k, int32_t c_type) {
+  return m <= 0 || n <= 0 || k < 0 ? "" : FORM_NAMES[form_of(m, n, k, c_type == ECHO_FP32)];
+}
 
 extern "C" int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t as_row, int64_t as_blk,
                                const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk,

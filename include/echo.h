@@ -659,6 +659,10 @@ int echo_matmul_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t
                     const uint8_t *b, int64_t ldb, const float *b_scale, int64_t bs_row, int64_t bs_blk, int32_t m,
                     int32_t n, int32_t k, void *c, int64_t ldc, int32_t c_type, void *stream);
 
+/* The kernel that a product of these sizes takes, as text: "few ..." (exact for every type), "split ..."
+ * or "tile ..." with the outputs of a workgroup; "" for no outputs.  For profiles and tests. */
+const char *echo_matmul_fp8_form(int32_t m, int32_t n, int32_t k, int32_t c_type);
+
 /*
  * Norms of n_q_heads query heads and n_k_heads key heads of n_tok tokens, and the rotation of
  * rot_dim values of each head from rot_begin on by the token's angles, in one pass.  Row pos[t] of

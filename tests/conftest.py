@@ -19,7 +19,7 @@ def pytest_configure(config):
 # scoring launch with a host-gather wave), and the full-size stress step last, so that under -x the
 # first failure names the lowest broken piece and hides no result below it.  Other modules keep
 # their place before these; test_zz_* stay last.
-BOTTOM_UP = ("test_gpu_pages.py", "test_gpu_blockfp8.py", "test_gpu_heads.py",
+BOTTOM_UP = ("test_gpu_pages.py", "test_gpu_blockfp8.py", "test_gpu_products.py", "test_gpu_heads.py",
              "test_gpu_scores.py", "test_gpu_topk.py", "test_gpu_pool.py", "test_gpu_decode.py",
              "test_gpu_inputs.py", "test_gpu_prefill.py", "test_gpu_multistep.py", "test_gpu_interquery.py",
              "test_gpu_layers.py", "test_gpu_fused.py", "test_gpu_stress.py")

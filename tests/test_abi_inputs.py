@@ -305,3 +305,17 @@ def test_page_step_alignment(on_cpu):
     ws = torch.zeros(B.page_workspace_bytes(3, 9000) + 8, dtype=torch.uint8)[1:]
     big = dict(slot=torch.zeros(9000, dtype=torch.int64), row=i32(9000), pos=i32(9000))
     refused("aligned", B.page_step, **page_tensors(ws=ws, **big))
+
+
+def test_every_form_of_the_product_is_tested():
+    """The sizes of tests/test_gpu_products.py take the kernels they are meant for, and these are all
+    there are: a change of the rule that moves a case, or adds a kernel, shows here."""
+    from test_gpu_products import CODE, FORMS
+    for form, m, n, k, types in FORMS:
+        for t in types:
+            assert B.matmul_fp8_form(m, n, k, CODE[t]) == form, (m, n, k, t)
+    sizes = [1, 17, 33, 65, 200, 400, 700, 1100, 1500, 2000, 2500, 2900, 4097, 6000, 9000, 17000]
+    for t in CODE:
+        taken = {B.matmul_fp8_form(m, n, k, CODE[t]) for m in sizes for n in sizes for k in (0, 128, 640, 641, 9000)}
+        assert taken == {form for form, *_, types in FORMS if t in types}, t
+    assert B.matmul_fp8_form(0, 5, 5, B.BF16) == B.matmul_fp8_form(5, 0, 5, B.BF16) == ""
