@@ -1,6 +1,6 @@
 """Every kernel that echo_matmul_fp8 can take, by name (echo_matmul_fp8_form), against a float64 product:
-random operands of all codes, wide rows, scales with blocks as rows, results at even and odd addresses
-and NaN.
+random operands of all codes, wide rows, scales with blocks as rows, results at even and odd addresses,
+NaN, and K beyond what a wave holds of the weight scales at once.
 
 Tolerance, derived as in test_gpu_blockfp8.py: (128 + nb + 11) * 2 u times the sum of the terms'
 magnitudes T for sums in fp32 (u = 2^-24, nb blocks); for 16-bit results of the FP8 matrix core (the
@@ -119,3 +119,13 @@ def test_forms_full(form, m, n, k, kind):
 def test_forms_with_nan_full(form, m, n, k, kind):
     """Even rows; a NaN in one row of each operand, in the last block and the first, stays there."""
     product(form, m, n, k, kind, 0, n + 1 + n % 2, m + k, [(0, m - 1, k - 1), (1, n - 1, 0)])
+
+
+# 64 blocks' weight scales are in a wave's registers at a time: 8192 of K in the tiles, 4 x 8192 where four
+# waves share the blocks
+@pytest.mark.parametrize("form,m,n,k,kind", [
+    ("tile 64x128", 1090, 1100, 8500, "bf16"), ("tile 64x128", 1090, 1100, 8300, "fp32"),
+    ("split 64x64", 513, 530, 33100, "fp16"), ("split 64x64", 513, 530, 33100, "fp32"),
+    ("tile 128x128", 1701, 2051, 16500, "fp32"), ("tile 256x256", 2901, 2945, 8321, "bf16")])
+def test_long_sums_full(form, m, n, k, kind):
+    product(form, m, n, k, kind, 0, n, k)
