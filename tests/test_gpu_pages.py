@@ -273,3 +273,33 @@ def test_no_pages_at_all(max_new):
         assert want["status"] and got["status"] & want["status"]
         want["status"] = got["status"]
         check(got, want)
+
+
+@pytest.mark.parametrize("max_new", [4000, 5007, 5008, 5020])
+def test_too_many_tokens_in_two_launches(max_new):
+    """More new tokens than maps where the maps take two launches: refused whole, and the step that just
+    fits is done."""
+    rng = np.random.default_rng(12)
+    lens, table, free, count = make_state(rng, 6, 0, 16, 200, 400, lens=[16, 5, 0, 40, 64, 1])
+    new = np.array([3000, 2, 0, 2000, 0, 6], np.int32)
+    done = np.array([0, 0, 0, 1, 0, 0], np.uint8)
+    want = O.page_step(lens, new, done, table, free, count, 16, max_new)
+    assert (want["status"] == O.ST_BAD_LEN) == (max_new < 5008) and max_new > 3584
+    check(run_step(lens, new, done, table, free, count, 16, max_new), want, max_new)
+
+
+@pytest.mark.parametrize("n,chunk", [(2048, 3), (9001, 1), (65535, 1)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_requests_full(n, chunk, in_place):
+    """The plan of more requests than LDS holds, up to the most there may be, many of them finished."""
+    rng = np.random.default_rng(n)
+    lens, table, free, count = make_state(rng, n, 70, 16, 6, n)
+    new = rng.integers(0, chunk + 1, n).astype(np.int32)
+    done = (rng.random(n) < 0.2).astype(np.uint8)
+    cap = int(new.sum()) + 7
+    want = O.page_step(lens, new, done, table, free, count, 16, cap)
+    assert want["status"] == 0
+    check(run_step(lens, new, done, table, free, count, 16, cap, in_place), want, n)
+    want = O.page_step(lens, new, done, table, free, count, 16, cap - 8)
+    assert want["status"] == O.ST_BAD_LEN
+    check(run_step(lens, new, done, table, free, count, 16, cap - 8, in_place), want, n)
