@@ -139,26 +139,32 @@ template <int G> ECHO_DEV float group_amax(const float (&x)[VEC]) {
 constexpr float FP8_MAX = 448.f;
 constexpr float FP8_AMAX_MIN = 448.f * 1.17549435e-38f;     // 448 * 2^-126
 
-struct Fp8Scale { float scale, inv, hi, lo; };                 // inv: 1 / scale rounded, hi + lo: in two parts, lo >= 0
-ECHO_DEV Fp8Scale fp8_scale(float amax) {
-  const float a = amax < FP8_AMAX_MIN ? FP8_AMAX_MIN : amax;   // a NaN passes
-  const float scale = a / FP8_MAX, inv = 1.f / scale;
-  const float hi = fmaf(-scale, inv, 1.f) < 0.f ? __uint_as_float(__float_as_uint(inv) - 1u) : inv;
-  return Fp8Scale{scale, inv, hi, fmaf(-scale, hi, 1.f) * inv};
-}
 // Codes of eight values: the fp32 quotient x / scale rounded to the nearest code.  Quotients on the
 // border of two codes are common (one bf16 value in a thousand), so one that is off by its last bit
 // gives another code, as x times a rounded reciprocal did.  A block shares its scale, so its reciprocal
-// is made in two parts: x (hi + lo) is within 2^-45 of the quotient before its one rounding, which is then
-// the quotient's own for every pair of 16-bit x and largest x (tried for all).  Values with all of their
-// 24 bits (FULL) take one step more, q - (q scale - x) / scale, whose remainder is exact (Markstein).
-// Scales where a product or remainder could underflow, or that are infinite or NaN, divide.  On
-// MI355X 32768 tokens of indexer inputs take 157 us (149 with the rounded reciprocal alone, 166 with two
-// such steps from it, 193 with a division per value), 32768 x 4096 bf16 values 73 us (73, 73, 86).
+// is made in two parts, hi + lo: x (hi + lo) is within 2^-44 of the quotient before its one rounding, which
+// is then the quotient's own for every pair of 16-bit x and largest x (tried for all, with a first
+// reciprocal off by one unit either way).  Values with all of their 24 bits (FULL) take one step more,
+// q - (q scale - x) / scale, whose remainder is exact (Markstein).  The scale itself is a (1 / 448) with
+// that constant in two parts, equal to the division for every significand of a (tried for all).  Blocks
+// whose products or remainders could underflow, zeros and those with an infinity or a NaN divide.  On
+// MI355X 32768 tokens of indexer inputs take 152 us (149 with one rounded reciprocal, 157 with two divisions
+// a block, 193 with one per value), 32768 x 4096 bf16 values 72.6 (72.7, 73.0 and 85.7).
+struct Fp8Scale { float scale, inv, hi, lo; bool divide; };
+template <bool FULL>
+ECHO_DEV Fp8Scale fp8_scale(float amax) {                      // every lane of the wave calls
+  const float a = amax < FP8_AMAX_MIN ? FP8_AMAX_MIN : amax;   // a NaN passes
+  if (__ballot(!(a >= 0x1p-64f && a <= 0x1p64f))) return Fp8Scale{a / FP8_MAX, 0.f, 0.f, 0.f, true};
+  constexpr float C_HI = 1.f / FP8_MAX, C_LO = static_cast<float>(1.0 / 448.0 - static_cast<double>(C_HI));
+  const float scale = fmaf(a, C_HI, a * C_LO);
+  const float inv = FULL ? 1.f / scale : __builtin_amdgcn_rcpf(scale);         // rounded, or off by a unit
+  const float hi = __uint_as_float(__float_as_uint(inv) - 2u);                 // below 1 / scale: lo is positive
+  return Fp8Scale{scale, inv, hi, fmaf(-scale, hi, 1.f) * inv, false};
+}
 template <bool FULL>
 ECHO_DEV u32x2 quantise8(const float (&x)[VEC], const Fp8Scale &s) {
   float y[VEC];
-  if (!__ballot(!(s.scale >= 0x1p-64f && s.scale <= 0x1p64f))) {     // every lane of the wave calls
+  if (!s.divide) {                                                   // the same for the whole wave
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       y[i] = fmaf(x[i], s.hi, x[i] * s.lo);                          // a zero keeps its sign

@@ -173,7 +173,7 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
     Fp8Scale sc = {};
     u32x2 code = {0, 0};
     if (FP8) {                                       // by all lanes, live or not
-      sc = fp8_scale(group_amax<G>(x));
+      sc = fp8_scale<sizeof(T) == 4>(group_amax<G>(x));
       code = quantise8<sizeof(T) == 4>(x, sc);
     }
     if (!live[u]) continue;

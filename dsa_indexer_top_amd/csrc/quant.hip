@@ -42,7 +42,7 @@ __global__ __launch_bounds__(QT) void quant_kernel(const T *__restrict__ x, int6
   for (int u = 0; u < QU; ++u) {
     float v[VEC];
     unpack8(raw[u], v);
-    const Fp8Scale s = fp8_scale(group_amax<16>(v));
+    const Fp8Scale s = fp8_scale<sizeof(T) == 4>(group_amax<16>(v));
     const u32x2 code = quantise8<sizeof(T) == 4>(v, s);
     if (left[u] < 0) continue;
     if (j == 0) scale[row[u] * s_row + blk[u] * s_blk] = s.scale;

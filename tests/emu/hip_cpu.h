@@ -105,6 +105,16 @@ template <typename T> inline T atomicCAS(T *p, T expected, T v) {
   return expected;
 }
 
+// v_rcp_f32 is good to one unit in the last place: off by -1, 0 or 1 of them here, by the argument's bits
+inline float emu_amdgcn_rcpf(float x) {
+  unsigned u, v;
+  float r = 1.0f / x;
+  __builtin_memcpy(&u, &x, 4);
+  __builtin_memcpy(&v, &r, 4);
+  if ((v & 0x7F800000u) != 0x7F800000u && (v & 0x7F800000u) != 0) v += (u * 2654435761u >> 16) % 3 - 1;
+  __builtin_memcpy(&r, &v, 4);
+  return r;
+}
 template <typename T> inline T emu_nontemporal_load(const T *p) { return *p; }
 template <typename T> inline void emu_nontemporal_store(T v, T *p) { *p = v; }
 
