@@ -354,3 +354,29 @@ def test_quant_codes_of_all_significands():
     scale = torch.empty((1024, 9), device="cuda")
     B.quant_fp8(x.cuda(), y, scale)
     assert np.array_equal(host(y), fp32_codes(x.float().numpy(), host(scale)))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_quant_blocks_of_all_sizes_side_by_side(kind):
+    """Blocks of zeros, of tiny and huge values, infinities and NaN next to ordinary ones: every
+    block's codes are its own."""
+    rng = np.random.default_rng(12)
+    x = rng.standard_normal((64, 128 * 9)).reshape(64, 9, 128)
+    small, large = (2.0 ** -20, 2.0 ** 12) if kind == "fp16" else (2.0 ** -100, 2.0 ** 100)
+    x *= rng.choice([0.0, 1.0, 1.0, small, large], (64, 9, 1))
+    x[5, 2, 7], x[9, 0, 100], x[9, 8, 3] = np.nan, np.inf, -np.inf
+    x[20, 4] = -0.0
+    x = torch.from_numpy(x.reshape(64, -1)).to(TYPES[kind])
+    y = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+    scale = torch.empty((64, 9), device="cuda")
+    B.quant_fp8(x.cuda(), y, scale)
+    s = host(scale)
+    ok = np.isfinite(s)
+    bad = np.zeros((64, 9), bool)
+    bad[[5, 9, 9], [2, 0, 8]] = True
+    assert np.array_equal(~ok, bad)
+    want = fp32_codes(x.float().numpy(), s).reshape(64, 9, 128)
+    got = host(y).reshape(64, 9, 128)
+    assert np.array_equal(got[ok], want[ok])
+    amax = np.abs(x.float().numpy().reshape(64, 9, 128)[ok]).max(1)
+    assert np.array_equal(s[ok], np.maximum(amax, np.float32(448 * 2.0 ** -126)) / np.float32(448))
