@@ -386,6 +386,7 @@ extern "C" int echo_newest_queries(const uint8_t *q8, const float *w, const int3
                                    int32_t n_rows, int32_t n_tok, int32_t n_q_heads, uint8_t *q_out, float *w_out,
                                    int32_t *len_out, void *stream) {
   if (n_rows < 0 || n_tok < 0 || n_q_heads < 0) return fail(ECHO_EINVAL, "echo_newest_queries: negative size");
+  if (n_rows > 65535) return fail(ECHO_EUNSUPPORTED, "echo_newest_queries: %d requests, more than 65535", n_rows);
   if (n_rows == 0) return ECHO_OK;
   const bool rows = n_tok && n_q_heads;
   if (!row_begin || !len || !len_out || (rows && (!q8 || !w)) || (n_q_heads && (!q_out || !w_out)))

@@ -716,7 +716,8 @@ int echo_indexer_qk(const echo_qk_args *a, const float *w, int64_t w_tok_stride,
  * and w_out, and len_out[r] = len[r], its keys.  A request without new tokens (padding, a finished one,
  * every one of a refused step) has no query: len_out[r] = 0 and its rows of q_out and w_out are left as
  * they were.  So is one whose rows are not within [0, n_tok].  Outputs overlap no input; q8 and q_out
- * are 8-byte aligned.  Pure enqueue; ECHO_EINVAL for negative sizes and NULL pointers.
+ * are 8-byte aligned.  Pure enqueue; ECHO_EINVAL for negative sizes, NULL pointers and others not aligned
+ * to their types, ECHO_EUNSUPPORTED for more than 65535 requests.
  */
 int echo_newest_queries(const uint8_t *q8, const float *w, const int32_t *row_begin, const int32_t *len,
                         int32_t n_rows, int32_t n_tok, int32_t n_q_heads, uint8_t *q_out, float *w_out,

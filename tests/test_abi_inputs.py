@@ -247,7 +247,7 @@ def test_newest_queries_refusals(on_cpu):
         assert call(**{name: None}) == B.ECHO_EINVAL and "NULL" in err(), name
     assert call(q8=F + 4) == call(qo=F + 1) == B.ECHO_EUNSUPPORTED
     assert call(w=F + 2) == call(wo=F + 1) == call(begin=F + 2) == call(n=F + 1) == call(lo=F + 3) == B.ECHO_EINVAL
-    assert call(rows=0) == B.ECHO_OK
+    assert call(rows=65536) == B.ECHO_EUNSUPPORTED and call(rows=0) == B.ECHO_OK
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
     ok = dict(q8=u8(9, 3, 128), w=torch.zeros(9, 3), row_begin=i32(5), key_len=i32(4), q_out=u8(4, 3, 128),
               w_out=torch.zeros(4, 3), len_out=i32(4))
