@@ -184,8 +184,8 @@ ECHO_DEV void heads_wave(const HeadArgs &a, const HeadSide &s, bool is_k, uint32
     }
     if (!is_k) {
       const int64_t row = static_cast<int64_t>(t) * s.heads + h;
-      // 8 bytes a lane: past the caches a prefill chunk's codes leave faster (32768 tokens: 175.6 us
-      // with plain stores, 165.7 with these)
+      // 8 bytes a lane: past the caches a prefill chunk's codes leave faster (32768 tokens: 163 us with
+      // plain stores where these took 157; 1400 tokens 13.2 and 11.6)
       __builtin_nontemporal_store(code, reinterpret_cast<u32x2 *>(a.f.q8 + row * D + j * VEC));
       if (j == 0) a.f.w_out[row] = w[u] * sc.scale * a.f.w_mul;
     } else {
@@ -243,8 +243,8 @@ static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
   while (g * VEC < a.dim) g *= 2;
   // Several loads a wave, for their common angles and weights, where there are waves enough and few
   // of their loads are of nothing; fewer rows are over sooner spread thin.  On MI355X in us with one,
-  // two and four: indexer inputs of 64 tokens 3.3, 4.1, 6.2, of 1400 11.4, 10.5, 11.7, of 32768 197,
-  // 167, 152; 8191 tokens of 40 + 5 heads 41.3, 35.2, 38.7 (a quarter of four are of nothing); 5384
+  // two and four: indexer inputs of 64 tokens 4.9, 4.9, 6.6 a call, of 1400 12.5, 11.6, 13.0, of 8192 54,
+  // 47, 45, of 32768 201, 170, 157 (before scales without divisions, which take 5 off the last); 8191 tokens of 40 + 5 heads 41.3, 35.2, 38.7 (a quarter of four are of nothing); 5384
   // tokens of 4 + 2 heads of 256 10.1, 10.8, 14.6 (a quarter of two, five eighths of four).
   const auto share = [&](int loads) {
     for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);

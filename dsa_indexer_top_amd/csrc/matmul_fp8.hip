@@ -51,7 +51,7 @@ ECHO_DEV v8i load_operand(const uint8_t *__restrict__ blk, int g, int left) {
 // at 2^-13 of the largest one's power of two (measured: a product survives next to one 2^13 times
 // larger and is gone at 2^14, the groups are then summed in fp32).  For normally distributed
 // operands a sum is off by 1.6e-5 of its size, far below the half step of a bf16 (2^-9) or fp16
-// (2^-12) result, so those use it.  Results in fp32 convert the codes to bf16, which holds every
+// (2^-12) result, so those use it where there are many outputs.  Results in fp32 convert the codes to bf16, which holds every
 // E4M3FN number and multiplies exactly into fp32, and take four bf16 MFMAs at half the rate.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -133,8 +133,9 @@ ECHO_DEV void store_some(T *p, const u32x4 &v, int count) {
 // One workgroup per 16 * NT weight rows and 16 * MT activation rows; its 8 waves take the scale blocks
 // in turn and their sums are joined in LDS in wave order (four waves are 3% faster up to K = 1000, 20 to
 // 40% slower at 6000; sixteen up to 30% slower).  Reading the weights is what costs here (1 x 8192 x
-// 8192 on MI355X: 13.0 us = 5.2 TB/s; 1 x 8192 x 2048: 5.1 us, mostly the launch and one round
-// trip), so every output type gets the exact products.
+// 8192 on MI355X: 13.5 us = 5.0 TB/s), so every output type gets the exact products.  A wave fetches a
+// block once the one before has arrived: 1 x 8192 x 2048, two blocks a wave, is the launch, two trips to
+// memory in a row and the join (5.2 us).
 constexpr int SW = 8;
 template <typename T, int MT, int NT>
 __global__ __launch_bounds__(SW * 64) void matmul_few_kernel(MatArgs a) {

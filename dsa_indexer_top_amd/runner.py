@@ -385,8 +385,9 @@ class PagedIndexerRunner:
     norm, both rotations and the FP8 forms, the keys going to their pages.  score() then scores
     every request's newest query against its pages and selects its top-k; a request that got no token
     in the step (padding, a finished one, every one of a step that was refused) has no query and
-    selects nothing.  Weights are (codes, scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden],
-    ww [64, hidden].  No arithmetic of the method lives here."""
+    selects nothing.  A step costs what max_new tokens cost, however many it has.  Weights are (codes,
+    scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden], ww [64, hidden].  No arithmetic of the
+    method lives here."""
 
     def __init__(self, n_rows, page_size, max_pages, n_pages, max_new, topk, wq, wk, ww, cos_sin,
                  k_weight, k_bias, w_mul, eps=1e-6, interleaved=False):

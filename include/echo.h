@@ -643,14 +643,18 @@ int echo_quant_fp8(const void *x, int32_t x_type, int64_t n_rows, int32_t n_cols
  *             (sum over p in block t, p < k, of a[i][p] * b[j][p])
  * a [m, k] are activations with a scale per row and 128 columns, a_scale(i, t) =
  * a_scale[i * as_row + t * as_blk]; b [n, k] are weights with a scale per 128 rows and 128 columns,
- * b_scale[(j / 128) * bs_row + t * bs_blk].  Sums are kept in fp32 and rounded once to c's type
+ * b_scale[(j / 128) * bs_row + t * bs_blk].  The two scales are multiplied first, in fp32, so their
+ * product has to be a normal fp32 number.  Sums are kept in fp32 and rounded once to c's type
  * c_type (ECHO_BF16, ECHO_FP16 or ECHO_FP32); c[i * ldc + j].  Products are exact for ECHO_FP32
- * and for up to 32 rows of a; 16-bit results of more rows come from the FP8 matrix core, which cuts
+ * and for few outputs (up to 32 rows, or at most 256 tiles of 32 x 32: echo_matmul_fp8_form says
+ * "few"); other 16-bit results come from the FP8 matrix core, which cuts
  * each product at 2^-13 of the largest of its eight neighbours in k (about 1.6e-5 of a sum of
- * normally distributed terms, against the result's own 2^-9 or 2^-12).  a, b, lda and ldb are multiples of
- * 16 and every row, the last too, is readable up to k rounded up to 16; what stands behind k is
- * ignored.  c must not overlap an input.  The result does not depend on what runs beside it: no
- * atomics, no workspace.  m = 0 or n = 0: ECHO_OK; k = 0 writes zeros.  ECHO_EINVAL for negative
+ * normally distributed terms, against the result's own 2^-9 or 2^-12).  The kernel and with it the order
+ * of a sum go by m, n, k and the type, so a row's result may differ in its last bits with the number
+ * of rows beside it; for the same sizes it is the same bits always: no atomics, no workspace.  a, b, lda
+ * and ldb are multiples of 16 and every row, the last too, is readable up to k rounded up to 16; what
+ * stands behind k is ignored.  c must not overlap an input.  m = 0 or n = 0: ECHO_OK; k = 0 writes zeros.
+ * ECHO_EINVAL for negative
  * sizes, NULL pointers, an unknown type, lda or ldb below k, ldc below n, c not aligned to its type;
  * ECHO_EUNSUPPORTED for other alignments, lda, ldb or as_row above 2^22, negative scale strides, and
  * sizes beyond a launch (m or n above 2^26, 2^24 output tiles of 128 x 128).
@@ -675,7 +679,9 @@ const char *echo_matmul_fp8_form(int32_t m, int32_t n, int32_t k, int32_t c_type
  * whose pos is outside [0, n_pos) is padding: nothing of it is written.  head_dim is a multiple of 8
  * up to 256, rot_dim (0: none, cos_sin may be NULL) a multiple of 16, rot_begin of 8; pointers and
  * strides of q, k, cos_sin, weights and outputs are multiples of 16 bytes; anything else is
- * ECHO_EUNSUPPORTED, as are more than 2^31 - 2^16 heads in all.  ECHO_EINVAL for negative sizes,
+ * ECHO_EUNSUPPORTED, as are more than 2^31 - 2^16 query or key heads and more than a launch holds (2^26
+ * waves: 2^30 heads of 72 to 128 values, twice as many of half that size, half as many of twice).
+ * ECHO_EINVAL for negative sizes,
  * NULL pointers (where there is something to read or write), an unknown type or norm, a rotated part
  * behind the head's end, eps below 0 or NaN.
  */
