@@ -244,8 +244,9 @@ static int launch_heads(HeadArgs &a, bool next, hipStream_t st) {
   // Several loads a wave, for their common angles and weights, where there are waves enough and few
   // of their loads are of nothing; fewer rows are over sooner spread thin.  On MI355X in us with one,
   // two and four: indexer inputs of 64 tokens 4.9, 4.9, 6.6 a call, of 1400 12.5, 11.6, 13.0, of 8192 54,
-  // 47, 45, of 32768 201, 170, 157 (before scales without divisions, which take 5 off the last); 8191 tokens of 40 + 5 heads 41.3, 35.2, 38.7 (a quarter of four are of nothing); 5384
-  // tokens of 4 + 2 heads of 256 10.1, 10.8, 14.6 (a quarter of two, five eighths of four).
+  // 47, 45, of 32768 201, 170, 157 (before scales without divisions, which take 5 off the last); 8191
+  // tokens of 40 + 5 heads 41.3, 35.2, 38.7 (a quarter of four are of nothing); 5384 tokens of 4 + 2 heads
+  // of 256 10.1, 10.8, 14.6 (a quarter of two, five eighths of four).
   const auto share = [&](int loads) {
     for (int i = 0; i < 2; ++i) a.waves[i] = side_waves(a.side[i], a.n_tok, g, loads);
     return static_cast<uint64_t>(a.waves[0]) + a.waves[1];

@@ -325,7 +325,7 @@ __global__ __launch_bounds__(PF_T) void newest_kernel(const uint8_t *__restrict_
   const u32x2 *src = reinterpret_cast<const u32x2 *>(q8 + from * D);
   u32x2 *dst = reinterpret_cast<u32x2 *>(q_out + to * D);
   for (int64_t i = threadIdx.x; i < static_cast<int64_t>(heads) * (D / 8); i += PF_T) dst[i] = src[i];
-  for (int32_t h = threadIdx.x; h < heads; h += PF_T) w_out[to + h] = w[from + h];
+  for (int64_t h = threadIdx.x; h < heads; h += PF_T) w_out[to + h] = w[from + h];
 }
 
 }  // namespace echo
