@@ -110,6 +110,15 @@ _SIGS = {
     "echo_qk_norm_rope": (C.c_int, [P, P, I64, I64, P, I64, I64, P]),
     "echo_indexer_qk": (C.c_int, [P, P, I64, F32, P, P, P, P, P, I64, P]),
     "echo_newest_queries": (C.c_int, [P, P, P, P, I32, I32, I32, P, P, P, P]),
+    "echo_block_topk_workspace_bytes": (SZ, [I32, I32, I32]),
+    "echo_block_topk": (C.c_int, [P, I64, P, I32, I32, I32, I32, I32, I32, P, P, SZ, P]),
+    "echo_sparse_attention_workspace_bytes": (SZ, [I32, I32, I32]),
+    "echo_sparse_attention": (C.c_int, [P, P, I64, I64, P, P, SZ, P]),
+    "echo_prefix_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32]),
+    "echo_prefix_attention": (C.c_int, [P, P, I64, I64, P, P, SZ, P]),
+    "echo_attention_weights": (C.c_int, [P, P, P, I64, P]),
+    "echo_pool_weigh_workspace_bytes": (SZ, [I32]),
+    "echo_pool_weigh": (C.c_int, [P, P, P, I32, P, P, I64, P, I64, F32, P, SZ, P]),
     "echo_host_alloc": (C.c_int, [SZ, C.c_int, C.POINTER(P), C.POINTER(P)]),
     "echo_host_free": (C.c_int, [P]),
 }
@@ -356,7 +365,8 @@ def _calls():
         L = lib()
         m.setup(EchoError, torch._C._cuda_getCurrentRawStream if DEVICE_TYPE == "cuda" else (lambda dev: 0),
                 *(C.cast(getattr(L, "echo_" + n), P).value for n in (
-                    "last_error", "page_step", "quant_fp8", "matmul_fp8", "qk_norm_rope", "indexer_qk", "newest_queries")))
+                    "last_error", "page_step", "quant_fp8", "matmul_fp8", "qk_norm_rope", "indexer_qk", "newest_queries",
+                    "block_topk", "sparse_attention", "prefix_attention", "attention_weights", "pool_weigh")))
         _tensor_calls = m
     return _tensor_calls
 
@@ -417,6 +427,58 @@ def newest_queries(q8, w, row_begin, key_len, q_out, w_out, len_out, stream=None
     """Each request's newest query of a step: q8 [tokens, heads, 128] and w [tokens, heads] by token, row_begin
     from page_step, to q_out [rows, heads, 128], w_out [rows, heads] and len_out [rows] (0: no token)."""
     _calls().newest_queries(q8, w, row_begin, key_len, q_out, w_out, len_out, _handle(stream), DEVICE_TYPE != "cuda")
+
+
+# ---------------------------------------------------------------- behind the selection
+def block_topk_workspace_bytes(n_rows, max_len, block):
+    return lib().echo_block_topk_workspace_bytes(n_rows, max_len, block)
+
+
+def block_topk(scores, length, max_len, block, k, idx, ws, n_first=0, n_last=0, stream=None):
+    """The k blocks of `block` tokens with the highest scores of each row (a block's score is its tokens'
+    largest), the first n_first and last n_last kept whatever they score: idx [rows, k], ascending, -1 padded."""
+    _calls().block_topk(scores, length, max_len, block, k, idx, ws, n_first, n_last, _handle(stream), DEVICE_TYPE != "cuda")
+
+
+def sparse_attention_workspace_bytes(n_rows, n_heads, n_tok):
+    return lib().echo_sparse_attention_workspace_bytes(n_rows, n_heads, n_tok)
+
+
+def sparse_attention(q, kv, idx, out, scale, ws, lse=None, block=1, length=None, page_table=None, page_size=0, req=None,
+                     stream=None):
+    """Attention of q [rows, heads, 576] over the rows of kv [n_kv, 576] that idx [rows, k] lists: rows of kv
+    (topk_slot), or with page_table [requests, pages] positions, or blocks of `block` of either; out [rows, heads,
+    512], lse [rows, heads].  length [rows]: positions at and behind it are passed over; req [rows]: each row's request."""
+    _calls().sparse_attention(q, kv, idx, block, length, page_table, page_size, req, scale, _handle(stream),
+                              DEVICE_TYPE != "cuda", out, lse, ws)
+
+
+def prefix_attention_workspace_bytes(n_rows, n_heads, n_groups, max_prefix, max_own):
+    return lib().echo_prefix_attention_workspace_bytes(n_rows, n_heads, n_groups, max_prefix, max_own)
+
+
+def prefix_attention(q, kv, out, scale, group_begin, prefix_len, prefix_table, own_len, own_table, page_size, max_prefix,
+                     max_own, ws, lse=None, stream=None):
+    """Attention of q [rows, heads, 576] over each row's group's prefix and its own tokens, both paged in kv:
+    rows group_begin[g] .. group_begin[g + 1] share the first prefix_len[g] tokens of prefix_table[g]."""
+    _calls().prefix_attention(q, kv, out, scale, group_begin, prefix_len, prefix_table, own_len, own_table, page_size,
+                              max_prefix, max_own, ws, lse, _handle(stream), DEVICE_TYPE != "cuda")
+
+
+def attention_weights(q, kv, idx, lse, w, scale, block=1, length=None, page_table=None, page_size=0, req=None, stream=None):
+    """w [rows, k * block]: what each token listed in idx got from all heads in the sparse_attention that gave lse."""
+    _calls().attention_weights(q, kv, idx, block, length, page_table, page_size, req, scale, _handle(stream),
+                               DEVICE_TYPE != "cuda", lse, w)
+
+
+def pool_weigh_workspace_bytes(n_gpu):
+    return lib().echo_pool_weigh_workspace_bytes(n_gpu)
+
+
+def pool_weigh(free, priority, mass, slot, w, ws, decay=1.0, fresh=None, stream=None):
+    """Adds the weights w of the slots `slot` (same shape, -1: none) to mass [n_gpu] after decaying it, slots in
+    fresh from 0 on, and makes it the pool's eviction order (priority)."""
+    _calls().pool_weigh(free, priority, mass, slot, w, ws, decay, fresh, _handle(stream), DEVICE_TYPE != "cuda")
 
 
 class CapturedGraph:

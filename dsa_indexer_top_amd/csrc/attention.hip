@@ -1,0 +1,595 @@
+// Attention of query heads over rows of a latent cache (echo_sparse_attention,
+// echo_prefix_attention).  One row of 576 values per token serves all heads:
+//   s_t = scale * q . row_t,   out = sum_t softmax(s)_t row_t[0 .. 512),   lse = log sum_t exp s_t.
+//
+// A workgroup takes 16 MT query heads that share their tokens and a chunk of those tokens, in
+// tiles of 64.  A tile is 72 KB, loaded straight to LDS while the one before is multiplied; it is read
+// from memory once for all the heads and used twice, as rows (scores) and as columns (sum).
+//   scores   wave w multiplies tokens 16 w .. 16 w + 15 with all heads, whose 576 values it holds in
+//            registers: every row of the tile is read from LDS once in all.
+//   softmax  base 2, running maximum and sum per head; the maximum of a tile's four waves through LDS.
+//   sum      wave w adds up columns 128 w .. 128 w + 127 over all 64 tokens: it reads the weights of
+//            all waves from LDS and the columns with transposing reads.
+// Weights are rounded to the cache's type for the product, as the matrix core takes them (off by half a
+// step of the type each, which in a sum of many is what the result's own rounding is); scores, sums,
+// maxima and the results are fp32.
+//
+// A chunk's result goes straight to the outputs where it is the only one, otherwise unnormalised to
+// the workspace with its maximum and sum, and join_kernel adds the chunks up.
+#include <algorithm>
+
+#include "latent.cuh"
+
+namespace echo {
+
+constexpr int TILE = 64, WAVES = 4, COLS = VALUES / WAVES;       // tokens of a tile, columns of a wave
+constexpr int KSTEPS = LATENT / 32;
+
+// Tokens whose list entry, position or page leads nowhere read this row instead of the cache, so that
+// nothing of the cache's contents can get into a sum through a weight of 0.
+__device__ const uint32_t g_zero_row[LATENT / 2] = {};
+
+// A tile in LDS: the rows' first 512 values, 1024 bytes a row, then their last 64, 128 bytes a row.
+// Pieces of 16 bytes are exchanged within a row so that the reads of 16 rows at one piece (scores) and of
+// 8 rows at one 32-byte column group (sums) touch every bank once.
+constexpr int ROPE_AT = TILE * 1024, STAGE = TILE * LATENT * 2;
+ECHO_DEV constexpr int swap_v(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
+ECHO_DEV constexpr int swap_r(int row) { return (row >> 1) & 7; }
+
+struct AttArgs {
+  LatentArgs a;
+  // where chunks' results go
+  void *out;
+  int64_t o_row, o_head;
+  float *lse;
+  float *part, *part_ml;         // [query, parts, 512], [query, parts, 2]
+  int32_t chunk, n_chunks, parts, first_part;
+  // groups of rows that share a prefix (echo_prefix_attention)
+  const int32_t *group_begin, *prefix_len, *prefix_table;
+  int32_t n_groups, prefix_pages;
+};
+
+// Queries [q0, q1) (row * n_heads + head) over tokens [t0, t1) of `src`; part < 0: the only chunk.
+struct Work {
+  int64_t q0, q1;
+  Tokens src;
+  int32_t t0, t1, part;
+};
+
+template <int MT>
+struct Lds {
+  static constexpr int P = 2 * STAGE, MX = P + MT * 16 * TILE * 2, SIZE = MX + WAVES * MT * 16 * 4;
+  static_assert(SIZE <= 160 * 1024, "a workgroup's LDS");
+};
+
+// The wave's 16 rows of a tile to LDS; lane i and every 16th after it hold the cache row of the wave's row i.
+ECHO_DEV void fetch(const AttArgs &x, int32_t row, uint8_t *__restrict__ stage, int wv) {
+  const int l = lane_id();
+  const uint8_t *kv = reinterpret_cast<const uint8_t *>(x.a.kv);
+  const int64_t stride = x.a.kv_stride * 2;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int32_t r = __builtin_amdgcn_readlane(row, i);
+    const uint8_t *src = r < 0 ? reinterpret_cast<const uint8_t *>(g_zero_row) : kv + r * stride;
+    __builtin_amdgcn_global_load_lds((glb_void *)(src + ((l ^ swap_v(i)) << 4)), (lds_void *)(stage + (wv * 16 + i) * 1024), 16, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = 8 * i + (l >> 3);
+    const int32_t r = __shfl(row, at, 64);
+    const uint8_t *src = r < 0 ? reinterpret_cast<const uint8_t *>(g_zero_row) : kv + r * stride;
+    __builtin_amdgcn_global_load_lds((glb_void *)(src + 1024 + (((l & 7) ^ swap_r(at)) << 4)),
+                                     (lds_void *)(stage + ROPE_AT + (wv * 16 + 8 * i) * 128), 16, 0, 0);
+  }
+}
+
+template <typename T, int MT>
+struct Heads {
+  typedef typename Mma<T>::x8 x8;
+  x8 q[MT][KSTEPS];
+  v4f o[MT][COLS / 16];
+  float m[MT], sum[MT];          // running maximum (base 2); this lane's part of the sum of weights
+
+  // Scores of the wave's tokens, softmax step and sum over the tile's tokens.  `real`: which of the wave's
+  // 16 tokens there are.
+  ECHO_DEV void tile(const uint8_t *__restrict__ cur, uint8_t *__restrict__ pbuf, float *__restrict__ mx, float scale2,
+                     uint32_t real, int wv) {
+    const int l = lane_id(), j = l & 15, g = l >> 4;
+    v4f s[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const uint8_t *vrow = cur + (wv * 16 + j) * 1024, *rrow = cur + ROPE_AT + (wv * 16 + j) * 128;
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k) {
+      const x8 row = k < 16 ? read16<x8>(vrow + (((4 * k + g) ^ swap_v(j)) << 4))
+                            : read16<x8>(rrow + (((4 * (k - 16) + g) ^ swap_r(j)) << 4));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
+    }
+    // Lane (j, g) has head j's scores of tokens 4 g .. 4 g + 3 of the wave's 16.
+    const uint32_t mine = real >> (4 * g);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float top = NO_SCORE;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        s[i][v] *= scale2;
+        if (mine >> v & 1) top = fmaxf(top, s[i][v]);
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (g == 0) mx[wv * MT * 16 + i * 16 + j] = top;
+    }
+    meet();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, mx[w * MT * 16 + i * 16 + j]);
+      const float less = exp2_(m[i] - top);
+      m[i] = top;
+      v4f p;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) p[v] = mine >> v & 1 ? exp2_(s[i][v] - top) : 0.f;
+      sum[i] = sum[i] * less + ((p[0] + p[1]) + (p[2] + p[3]));
+#pragma unroll
+      for (int c = 0; c < COLS / 16; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[i][c][v] *= less;
+      // Weights by head: the 32 tokens of two waves as 4 groups of 8, group g the tokens 4 g .. 4 g + 3 of both.
+      *reinterpret_cast<u32x2 *>(pbuf + (i * 16 + j) * 128 + (((4 * (wv >> 1) + g) ^ swap_r(j)) << 4) + 8 * (wv & 1)) = pack4<T>(p);
+    }
+    meet();
+    const int r = 4 * g + (j >> 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x8 p[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) p[i] = read16<x8>(pbuf + (i * 16 + j) * 128 + (((4 * h + g) ^ swap_r(j)) << 4));
+#pragma unroll
+      for (int c = 0; c < COLS / 16; ++c) {
+        const int piece = (wv * (COLS / 8) + 2 * c + ((j >> 1) & 1)) ^ swap_v(r);
+        const uint8_t *at = cur + (32 * h + r) * 1024 + (piece << 4) + 8 * (j & 1);
+        struct { v4s lo, hi; } e;
+        e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
+        e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 16 * 1024));
+        const x8 col = __builtin_bit_cast(x8, e);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][c] = Mma<T>::mul(col, p[i], o[i][c]);
+      }
+    }
+  }
+};
+
+template <typename T, int MT>
+ECHO_DEV void attend(const AttArgs &x, const Work &w, uint8_t *__restrict__ lds) {
+  typedef Heads<T, MT> H;
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int l = lane_id(), j = l & 15, g = l >> 4;
+  H hd;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t qi = min(w.q0 + i * 16 + j, w.q1 - 1);
+    const int64_t r = qi / x.a.n_heads;
+    const uint16_t *q = x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head + 8 * g;
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k) hd.q[i][k] = read16<typename H::x8>(q + 32 * k);
+    hd.m[i] = NO_SCORE;
+    hd.sum[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < COLS / 16; ++c) hd.o[i][c] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  // Token of the lane in tile t; entries are loaded three tiles ahead, pages two, rows one.
+  const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
+  const auto token = [&](int t) { return w.t0 + t * TILE + wv * 16 + j; };
+  const auto entry = [&](int t) { return token(t) < w.t1 ? w.src.entry(token(t)) : -1; };
+  const auto position = [&](int t, int32_t e) -> int64_t { return token(t) < w.t1 ? w.src.position(token(t), e) : -1; };
+  int64_t pos = position(0, entry(0)), pos1 = position(1, entry(1));
+  int32_t row = w.src.row(pos, w.src.page(pos));
+  int32_t page1 = w.src.page(pos1), e2 = entry(2);
+  uint32_t real = static_cast<uint32_t>(__ballot(row >= 0)) & 0xFFFFu;
+  if (n > 0) fetch(x, row, lds, wv);
+  for (int t = 0; t < n; ++t) {
+    uint8_t *cur = lds + (t & 1) * STAGE, *nxt = lds + ((t + 1) & 1) * STAGE;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(WAIT_VM0);
+    meet();                                                // tile t is there for all; tile t - 1 has been used
+    uint32_t real1 = 0;
+    if (t + 1 < n) {
+      row = w.src.row(pos1, page1);
+      real1 = static_cast<uint32_t>(__ballot(row >= 0)) & 0xFFFFu;
+      fetch(x, row, nxt, wv);
+      pos1 = position(t + 2, e2);
+      page1 = w.src.page(pos1);
+      e2 = entry(t + 3);
+    }
+    hd.tile(cur, lds + Lds<MT>::P, reinterpret_cast<float *>(lds + Lds<MT>::MX), x.a.scale2, real, wv);
+    real = real1;
+  }
+  // The sums of a head: four lane groups, four waves.
+  float *mx = reinterpret_cast<float *>(lds + Lds<MT>::MX);
+  meet();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    float s = hd.sum[i];
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (g == 0) mx[wv * MT * 16 + i * 16 + j] = s;
+  }
+  meet();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t qi = w.q0 + i * 16 + j;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) s += mx[v * MT * 16 + i * 16 + j];
+    if (qi >= w.q1) continue;
+    const int col = wv * COLS + 4 * g;
+    if (w.part < 0) {
+      const int64_t r = qi / x.a.n_heads;
+      const float inv = s == 0.f ? 0.f : 1.f / s;
+      T *out = static_cast<T *>(x.out) + r * x.o_row + (qi - r * x.a.n_heads) * x.o_head + col;
+#pragma unroll
+      for (int c = 0; c < COLS / 16; ++c) *reinterpret_cast<u32x2 *>(out + 16 * c) = pack4<T>(hd.o[i][c] * inv);
+      if (x.lse && wv == 0 && g == 0) x.lse[qi] = s == 0.f ? -INFINITY : (hd.m[i] + log2_(s)) * LN2;
+    } else {
+      const int64_t p = qi * x.parts + w.part;
+      float *out = x.part + p * VALUES + col;
+#pragma unroll
+      for (int c = 0; c < COLS / 16; ++c) *reinterpret_cast<v4f *>(out + 16 * c) = hd.o[i][c];
+      if (wv == 0 && g == 0) {
+        x.part_ml[2 * p] = hd.m[i];
+        x.part_ml[2 * p + 1] = s;
+      }
+    }
+  }
+}
+
+// The tokens that a query row lists (or, without a list, its own).  Workgroups go to the 8 XCDs in turn, each
+// with an L2 of its own: the head tiles of a chunk follow each other by 8, so that they share the one that the
+// chunk's rows are in.
+template <typename T, int MT>
+__global__ __launch_bounds__(WAVES * 64, 1) void rows_kernel(AttArgs x, uint32_t units, uint32_t head_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<MT>::SIZE];
+  const uint32_t eight = blockIdx.x / (8 * head_tiles), in = blockIdx.x - eight * 8 * head_tiles;
+  const uint32_t u = eight * 8 + (in & 7), ht = in >> 3;
+  if (u >= units) return;
+  const int32_t r = static_cast<int32_t>(u / x.n_chunks), c = static_cast<int32_t>(u - static_cast<uint32_t>(r) * x.n_chunks);
+  Work w;
+  w.src = x.a.tokens(r);
+  w.t0 = c * x.chunk;
+  w.t1 = min(w.t0 + x.chunk, x.a.n_tok);
+  if (!x.a.idx) {
+    w.src.list = nullptr;
+    w.t1 = static_cast<int32_t>(min<int64_t>(w.t1, max<int64_t>(w.src.limit, 0)));
+    if (w.t0 >= w.t1 && x.parts > 0) return;               // join_kernel goes by the length too
+  }
+  w.q0 = static_cast<int64_t>(r) * x.a.n_heads + ht * (16 * MT);
+  w.q1 = static_cast<int64_t>(r + 1) * x.a.n_heads;
+  w.part = x.parts > 0 ? x.first_part + c : -1;
+  attend<T, MT>(x, w, lds);
+}
+
+ECHO_DEV int32_t clamp_row(int32_t r, int32_t n) { return r < 0 ? 0 : r > n ? n : r; }
+
+// The prefixes: tile `tile` of the groups' query tiles in order, chunk `c`.
+template <typename T, int MT>
+__global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32_t tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<MT>::SIZE];
+  const int32_t c = blockIdx.x % x.n_chunks;
+  uint32_t tile = blockIdx.x / x.n_chunks;
+  int32_t gi = 0, r0 = 0, r1 = 0;
+  for (; gi < x.n_groups; ++gi) {
+    r0 = clamp_row(x.group_begin[gi], x.a.n_rows);
+    r1 = clamp_row(x.group_begin[gi + 1], x.a.n_rows);
+    if (r1 < r0) r1 = r0;
+    const uint32_t has = static_cast<uint32_t>((static_cast<int64_t>(r1 - r0) * x.a.n_heads + 16 * MT - 1) / (16 * MT));
+    if (tile < has) break;
+    tile -= has;
+  }
+  if (gi == x.n_groups) return;
+  Work w;
+  w.src = Tokens{nullptr, x.prefix_table + static_cast<int64_t>(gi) * x.prefix_pages, x.prefix_len[gi], 0, x.a.pshift, x.prefix_pages, x.a.n_kv};
+  w.t0 = c * x.chunk;
+  w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.chunk, x.a.n_tok), w.src.limit));
+  if (w.t0 >= w.t1) return;
+  w.q0 = static_cast<int64_t>(r0) * x.a.n_heads + static_cast<int64_t>(tile) * (16 * MT);
+  w.q1 = static_cast<int64_t>(r1) * x.a.n_heads;
+  w.part = c;
+  attend<T, MT>(x, w, lds);
+}
+
+// ---------------------------------------------------------------- joining chunks
+struct JoinArgs {
+  const float *part, *ml;
+  void *out;
+  int64_t o_row, o_head;
+  float *lse;
+  int32_t n_rows, n_heads, parts;
+  // numbers of parts: all, or by length
+  const int32_t *len, *group_begin, *prefix_len;
+  int32_t n_groups, prefix_chunk, max_prefix, prefix_parts, own_chunk, max_own;
+};
+
+// One wave per query, 8 columns a lane.
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs x) {
+  const int64_t qi = blockIdx.x * 4ll + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  if (qi >= static_cast<int64_t>(x.n_rows) * x.n_heads) return;
+  const int32_t r = static_cast<int32_t>(qi / x.n_heads), l = lane_id();
+  int32_t n0 = x.parts, skip = 0, n1 = 0;                  // parts [0, n0) and [skip, skip + n1)
+  if (x.own_chunk) {
+    n0 = 0;
+    for (int32_t gi = 0; gi < x.n_groups; ++gi) {
+      const int32_t b = clamp_row(x.group_begin[gi], x.n_rows), e = clamp_row(x.group_begin[gi + 1], x.n_rows);
+      if (r >= b && r < e) {
+        n0 = (max(0, min(x.prefix_len[gi], x.max_prefix)) + x.prefix_chunk - 1) / x.prefix_chunk;
+        break;
+      }
+    }
+    skip = x.prefix_parts;
+    n1 = (max(0, min(x.len[r], x.max_own)) + x.own_chunk - 1) / x.own_chunk;
+  }
+  const int64_t p0 = qi * x.parts;
+  float m = NO_SCORE, sum = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int32_t i = 0; i < n0 + n1; ++i) {
+    const int64_t p = p0 + (i < n0 ? i : skip + i - n0);
+    const float pm = x.ml[2 * p], ps = x.ml[2 * p + 1];
+    const float top = fmaxf(m, pm), was = exp2_(m - top), is = exp2_(pm - top);
+    const v4f a = *reinterpret_cast<const v4f *>(x.part + p * VALUES + 8 * l), b = *reinterpret_cast<const v4f *>(x.part + p * VALUES + 8 * l + 4);
+    sum = sum * was + ps * is;
+    m = top;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      o[v] = o[v] * was + a[v] * is;
+      o[4 + v] = o[4 + v] * was + b[v] * is;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int v = 0; v < 8; ++v) o[v] *= inv;
+  T *out = static_cast<T *>(x.out) + r * x.o_row + (qi - static_cast<int64_t>(r) * x.n_heads) * x.o_head + 8 * l;
+  store8(out, o);
+  if (x.lse && l == 0) x.lse[qi] = sum == 0.f ? -INFINITY : (m + log2_(sum)) * LN2;
+}
+
+// ---------------------------------------------------------------- host
+// Head tiles of 16, 32 or 64 queries: the smallest that holds `queries`.
+int head_tile(int64_t queries) { return queries <= 16 ? 1 : queries <= 32 ? 2 : 4; }
+
+// Chunks of n_tok tokens for `tiles` query tiles, and their tokens: as many as give each CU one workgroup.
+constexpr int CUS = 256;
+int32_t chunk_of(int64_t tiles, int64_t n_tok) {
+  const int64_t n = (n_tok + TILE - 1) / TILE;
+  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>(n, CUS / std::max<int64_t>(tiles, 1)));
+  return static_cast<int32_t>((n + chunks - 1) / std::max<int64_t>(chunks, 1)) * TILE;
+}
+int32_t chunks_of(int64_t n_tok, int32_t chunk) { return chunk ? static_cast<int32_t>((n_tok + chunk - 1) / chunk) : 0; }
+constexpr int64_t PART_BYTES = (VALUES + 2) * 4;
+constexpr int64_t MAX_GROUPS = 1 << 24;                    // workgroups of 256 threads in a launch
+constexpr int32_t MAX_HEADS = 1024, MAX_TOKENS = 1 << 28;
+
+struct RowsPlan { int mt; int64_t head_tiles; int32_t chunk, n_chunks; };
+RowsPlan rows_plan(int32_t n_rows, int32_t n_heads, int64_t n_tok) {
+  RowsPlan p;
+  p.mt = head_tile(n_heads);
+  p.head_tiles = (n_heads + 16 * p.mt - 1) / (16 * p.mt);
+  p.chunk = chunk_of(n_rows * p.head_tiles, n_tok);
+  p.n_chunks = std::max(1, chunks_of(n_tok, p.chunk));
+  return p;
+}
+int64_t sparse_ws(int32_t n_rows, int32_t n_heads, int64_t n_tok) {
+  const int32_t c = rows_plan(n_rows, n_heads, n_tok).n_chunks;
+  return c > 1 ? static_cast<int64_t>(n_rows) * n_heads * c * PART_BYTES : 0;
+}
+
+struct PrefixPlan { RowsPlan own; int mt; int64_t tiles; int32_t chunk, prefix_parts, own_parts; };
+PrefixPlan prefix_plan(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_t max_prefix, int32_t max_own) {
+  PrefixPlan p;
+  p.own = rows_plan(n_rows, n_heads, max_own);
+  p.own_parts = max_own > 0 ? p.own.n_chunks : 0;
+  const int64_t queries = static_cast<int64_t>(n_rows) * n_heads;
+  const int64_t groups = std::min(n_groups, n_rows);
+  p.mt = head_tile(groups ? queries / groups : queries);
+  p.tiles = groups ? queries / (16 * p.mt) + groups : 0;   // at least what the groups' last, partly filled tiles take
+  p.chunk = chunk_of(std::max<int64_t>(1, queries / (16 * p.mt)), max_prefix);
+  p.prefix_parts = groups && max_prefix > 0 ? chunks_of(max_prefix, p.chunk) : 0;
+  return p;
+}
+
+template <typename T>
+int launch_rows(const AttArgs &x, const RowsPlan &p, hipStream_t st) {
+  const uint32_t units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(p.n_chunks), ht = static_cast<uint32_t>(p.head_tiles);
+  const uint32_t grid = (units + 7) / 8 * 8 * ht;
+  switch (p.mt) {
+    case 1: rows_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
+    case 2: rows_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
+    default: rows_kernel<T, 4><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
+  }
+  return check_launch("attention");
+}
+template <typename T>
+int launch_prefix(const AttArgs &x, const PrefixPlan &p, hipStream_t st) {
+  const uint32_t tiles = static_cast<uint32_t>(p.tiles), grid = tiles * static_cast<uint32_t>(p.prefix_parts);
+  switch (p.mt) {
+    case 1: prefix_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
+    case 2: prefix_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
+    default: prefix_kernel<T, 4><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
+  }
+  return check_launch("prefix attention");
+}
+template <typename T>
+int launch_join(const JoinArgs &j, hipStream_t st) {
+  const int64_t q = static_cast<int64_t>(j.n_rows) * j.n_heads;
+  join_kernel<T><<<static_cast<uint32_t>((q + 3) / 4), 256, 0, st>>>(j);
+  return check_launch("attention join");
+}
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Queries and cache of either call.
+int check_cache(const char *fn, int32_t n_rows, int32_t n_heads, int32_t type, float scale, const void *q, int64_t q_row,
+                int64_t q_head, const void *kv, int64_t kv_stride, int32_t n_kv) {
+  if (n_rows < 0 || n_heads < 0 || n_kv < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+  if (type != ECHO_BF16 && type != ECHO_FP16) return fail(ECHO_EINVAL, "%s: type %d", fn, type);
+  if (!(scale >= -1.0e38f && scale <= 1.0e38f)) return fail(ECHO_EINVAL, "%s: scale outside [-1e38, 1e38]", fn);
+  if (n_heads > MAX_HEADS || n_rows > 1 << 22) return fail(ECHO_EUNSUPPORTED, "%s: more than %d heads or 2^22 rows", fn, MAX_HEADS);
+  if (n_rows == 0 || n_heads == 0) return ECHO_OK;
+  if (!q || (n_kv && !kv)) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
+  if (q_row < 0 || q_head < 0 || kv_stride < 0 || (n_kv > 1 && kv_stride < LATENT)) return fail(ECHO_EINVAL, "%s: a stride below 0 or below the row", fn);
+  if (!aligned(q, 16) || !aligned(kv, 16) || q_row % 8 || q_head % 8 || (n_kv > 1 && kv_stride % 8))
+    return fail(ECHO_EUNSUPPORTED, "%s: q, kv or their strides are not multiples of 16 bytes", fn);
+  return ECHO_OK;
+}
+int check_out(const char *fn, int32_t n_rows, int32_t n_heads, const void *out, int64_t o_row, int64_t o_head, const float *lse) {
+  if (!out) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
+  if (o_row < 0 || o_head < 0 || rows_overlap(n_rows, o_row, n_heads, o_head, VALUES)) return fail(ECHO_EINVAL, "%s: heads of out overlap", fn);
+  if (!aligned(out, 16) || (n_rows > 1 && o_row % 8) || (n_heads > 1 && o_head % 8))
+    return fail(ECHO_EUNSUPPORTED, "%s: out or its strides are not multiples of 16 bytes", fn);
+  if (!aligned(lse, 4)) return fail(ECHO_EINVAL, "%s: lse is not aligned to its type", fn);
+  return ECHO_OK;
+}
+int check_pages(const char *fn, const int32_t *table, int32_t page_size, int32_t max_pages) {
+  if (max_pages < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)))
+    return fail(ECHO_EUNSUPPORTED, "%s: page size %d is not a power of two in [16, 65536]", fn, page_size);
+  if (max_pages && !table) return fail(ECHO_EINVAL, "%s: NULL page table", fn);
+  if (!aligned(table, 4)) return fail(ECHO_EINVAL, "%s: a page table is not aligned to its type", fn);
+  return ECHO_OK;
+}
+int check_ws(const char *fn, const void *ws, size_t bytes, int64_t need) {
+  if (need <= 0) return ECHO_OK;
+  if (!ws || bytes < static_cast<size_t>(need)) return fail(ECHO_EWORKSPACE, "%s: a workspace of %lld bytes is needed", fn, static_cast<long long>(need));
+  if (!aligned(ws, 16)) return fail(ECHO_EINVAL, "%s: the workspace is not aligned to 16 bytes", fn);
+  return ECHO_OK;
+}
+
+// echo_latent_args, checked, as the kernels take them.
+int latent_args(const char *fn, const echo_latent_args *a, LatentArgs *x) {
+  if (!a) return fail(ECHO_EINVAL, "%s: NULL arguments", fn);
+  int rc = check_cache(fn, a->n_rows, a->n_heads, a->type, a->scale, a->q, a->q_row_stride, a->q_head_stride, a->kv, a->kv_stride, a->n_kv);
+  if (rc != ECHO_OK) return rc;
+  if (a->k < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+  if (a->block < 1 || a->block > 65536 || (a->block & (a->block - 1)))
+    return fail(ECHO_EUNSUPPORTED, "%s: block %d is not a power of two in [1, 65536]", fn, a->block);
+  if (static_cast<int64_t>(a->k) * a->block > MAX_TOKENS) return fail(ECHO_EUNSUPPORTED, "%s: more than 2^28 tokens a row", fn);
+  if (a->page_size) {
+    if (a->n_tables < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+    rc = check_pages(fn, a->page_table, a->page_size, a->n_tables ? a->max_pages : 0);
+    if (rc != ECHO_OK) return rc;
+    if (a->max_pages < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+  }
+  if (a->n_rows && a->n_heads && a->k && !a->idx) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
+  if (a->idx_stride < 0) return fail(ECHO_EINVAL, "%s: a stride below 0", fn);
+  if (!aligned(a->idx, 4) || !aligned(a->len, 4) || !aligned(a->req, 4)) return fail(ECHO_EINVAL, "%s: an array is not aligned to its type", fn);
+  const auto log2 = [](int32_t v) { int s = 0; while ((1 << s) < v) ++s; return s; };
+  *x = LatentArgs{static_cast<const uint16_t *>(a->q), a->q_row_stride, a->q_head_stride, static_cast<const uint16_t *>(a->kv), a->kv_stride,
+                  a->idx, a->idx_stride, a->len, a->page_size ? a->page_table : nullptr, a->req, a->n_rows, a->n_heads, a->n_kv,
+                  a->k * a->block, log2(a->block), a->page_size ? log2(a->page_size) : 0, a->page_size && a->n_tables ? a->max_pages : 0,
+                  a->n_tables, a->scale * LOG2E};
+  if (a->page_size && !x->table) x->n_kv = 0;              // pages, but none of them: no tokens
+  return ECHO_OK;
+}
+
+}  // namespace echo
+
+using namespace echo;
+
+extern "C" size_t echo_sparse_attention_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_tok) {
+  if (n_rows < 1 || n_heads < 1 || n_tok < 0 || n_heads > MAX_HEADS) return 0;
+  return static_cast<size_t>(sparse_ws(n_rows, n_heads, n_tok));
+}
+
+extern "C" int echo_sparse_attention(const echo_latent_args *a, void *out, int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                                     void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "echo_sparse_attention";
+  AttArgs x = {};
+  int rc = latent_args(fn, a, &x.a);
+  if (rc != ECHO_OK || a->n_rows == 0 || a->n_heads == 0) return rc;
+  rc = check_out(fn, a->n_rows, a->n_heads, out, out_row_stride, out_head_stride, lse);
+  if (rc != ECHO_OK) return rc;
+  const RowsPlan p = rows_plan(a->n_rows, a->n_heads, x.a.n_tok);
+  if ((static_cast<int64_t>(a->n_rows) * p.n_chunks + 8) * p.head_tiles >= MAX_GROUPS)
+    return fail(ECHO_EUNSUPPORTED, "%s: more rows, heads and tokens than a launch holds", fn);
+  const int64_t need = sparse_ws(a->n_rows, a->n_heads, x.a.n_tok);
+  rc = check_ws(fn, ws, ws_bytes, need);
+  if (rc != ECHO_OK) return rc;
+  const int64_t queries = static_cast<int64_t>(a->n_rows) * a->n_heads;
+  x.out = out; x.o_row = out_row_stride; x.o_head = out_head_stride; x.lse = lse;
+  x.chunk = p.chunk; x.n_chunks = p.n_chunks;
+  if (p.n_chunks > 1) {
+    x.parts = p.n_chunks;
+    x.part = static_cast<float *>(ws);
+    x.part_ml = x.part + queries * p.n_chunks * VALUES;
+  }
+  rc = a->type == ECHO_BF16 ? launch_rows<bf16_t>(x, p, S(stream)) : launch_rows<fp16_t>(x, p, S(stream));
+  if (rc != ECHO_OK || p.n_chunks == 1) return rc;
+  JoinArgs j = {};
+  j.part = x.part; j.ml = x.part_ml; j.out = out; j.o_row = out_row_stride; j.o_head = out_head_stride; j.lse = lse;
+  j.n_rows = a->n_rows; j.n_heads = a->n_heads; j.parts = p.n_chunks;
+  return a->type == ECHO_BF16 ? launch_join<bf16_t>(j, S(stream)) : launch_join<fp16_t>(j, S(stream));
+}
+
+extern "C" size_t echo_prefix_attention_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_t max_prefix, int32_t max_own) {
+  if (n_rows < 1 || n_heads < 1 || n_groups < 0 || max_prefix < 0 || max_own < 0 || n_heads > MAX_HEADS) return 0;
+  const PrefixPlan p = prefix_plan(n_rows, n_heads, n_groups, max_prefix, max_own);
+  return static_cast<size_t>(static_cast<int64_t>(n_rows) * n_heads * (p.prefix_parts + p.own_parts) * PART_BYTES);
+}
+
+extern "C" int echo_prefix_attention(const echo_prefix_args *a, void *out, int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                                     void *ws, size_t ws_bytes, void *stream) {
+  const char *fn = "echo_prefix_attention";
+  if (!a) return fail(ECHO_EINVAL, "%s: NULL arguments", fn);
+  int rc = check_cache(fn, a->n_rows, a->n_heads, a->type, a->scale, a->q, a->q_row_stride, a->q_head_stride, a->kv, a->kv_stride, a->n_kv);
+  if (rc != ECHO_OK) return rc;
+  if (a->n_groups < 0 || a->max_prefix < 0 || a->max_own < 0) return fail(ECHO_EINVAL, "%s: negative size", fn);
+  if (a->n_groups > 65536 || a->max_prefix > MAX_TOKENS || a->max_own > MAX_TOKENS)
+    return fail(ECHO_EUNSUPPORTED, "%s: more than 65536 groups or 2^28 tokens", fn);
+  rc = check_pages(fn, a->prefix_table, a->page_size, a->n_groups ? a->prefix_pages : 0);
+  if (rc == ECHO_OK) rc = check_pages(fn, a->own_table, a->page_size, a->n_rows ? a->own_pages : 0);
+  if (rc != ECHO_OK) return rc;
+  if (a->n_rows == 0 || a->n_heads == 0) return ECHO_OK;
+  if ((a->n_groups && (!a->group_begin || !a->prefix_len)) || !a->own_len) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
+  if (!aligned(a->group_begin, 4) || !aligned(a->prefix_len, 4) || !aligned(a->own_len, 4)) return fail(ECHO_EINVAL, "%s: an array is not aligned to its type", fn);
+  rc = check_out(fn, a->n_rows, a->n_heads, out, out_row_stride, out_head_stride, lse);
+  if (rc != ECHO_OK) return rc;
+  const PrefixPlan p = prefix_plan(a->n_rows, a->n_heads, a->n_groups, a->max_prefix, a->max_own);
+  const int64_t queries = static_cast<int64_t>(a->n_rows) * a->n_heads;
+  if (p.tiles * std::max(1, p.prefix_parts) >= MAX_GROUPS || (static_cast<int64_t>(a->n_rows) * p.own.n_chunks + 8) * p.own.head_tiles >= MAX_GROUPS ||
+      queries / 4 >= MAX_GROUPS)
+    return fail(ECHO_EUNSUPPORTED, "%s: more rows, heads and tokens than a launch holds", fn);
+  const int32_t parts = p.prefix_parts + p.own_parts;
+  rc = check_ws(fn, ws, ws_bytes, queries * parts * PART_BYTES);
+  if (rc != ECHO_OK) return rc;
+  int shift = 0;
+  while ((1 << shift) < a->page_size) ++shift;
+  AttArgs x = {};
+  x.a = LatentArgs{static_cast<const uint16_t *>(a->q), a->q_row_stride, a->q_head_stride, static_cast<const uint16_t *>(a->kv), a->kv_stride,
+                   nullptr, 0, a->own_len, a->own_table, nullptr, a->n_rows, a->n_heads, a->n_kv, a->max_own, 0, shift, a->own_pages, a->n_rows,
+                   a->scale * LOG2E};
+  x.out = out; x.o_row = out_row_stride; x.o_head = out_head_stride; x.lse = lse;
+  x.parts = parts;
+  x.part = static_cast<float *>(ws);
+  x.part_ml = x.part + queries * parts * VALUES;
+  const bool bf = a->type == ECHO_BF16;
+  if (p.prefix_parts) {
+    AttArgs y = x;
+    y.a.n_tok = a->max_prefix;
+    y.chunk = p.chunk; y.n_chunks = p.prefix_parts;
+    y.group_begin = a->group_begin; y.prefix_len = a->prefix_len; y.prefix_table = a->prefix_table;
+    y.n_groups = a->n_groups; y.prefix_pages = a->prefix_pages;
+    rc = bf ? launch_prefix<bf16_t>(y, p, S(stream)) : launch_prefix<fp16_t>(y, p, S(stream));
+    if (rc != ECHO_OK) return rc;
+  }
+  if (p.own_parts) {
+    x.chunk = p.own.chunk; x.n_chunks = p.own_parts; x.first_part = p.prefix_parts;
+    rc = bf ? launch_rows<bf16_t>(x, p.own, S(stream)) : launch_rows<fp16_t>(x, p.own, S(stream));
+    if (rc != ECHO_OK) return rc;
+  }
+  const JoinArgs j = {x.part, x.part_ml, out, out_row_stride, out_head_stride, lse, a->n_rows, a->n_heads, parts, a->own_len, a->group_begin,
+                      a->prefix_len, p.prefix_parts ? a->n_groups : 0, std::max(p.chunk, TILE), a->max_prefix, p.prefix_parts,
+                      std::max(p.own.chunk, TILE), a->max_own};
+  return bf ? launch_join<bf16_t>(j, S(stream)) : launch_join<fp16_t>(j, S(stream));
+}

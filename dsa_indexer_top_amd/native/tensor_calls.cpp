@@ -1,4 +1,4 @@
-// Tensor calls of the operators in front of the scores: checks of the tensors (types, shapes,
+// Tensor calls of the operators in front of the scores and behind the selection: checks of the tensors (types, shapes,
 // strides, devices) and the C ABI call, natively.  A step of a few tokens runs in 4 to 6 us on the
 // GPU; the same checks in Python took 6 to 11 us a call.  No arithmetic of the operators lives here:
 // the functions of libecho.so are called through the addresses that binding.py hands over.
@@ -23,6 +23,11 @@ decltype(&echo_matmul_fp8) g_matmul = nullptr;
 decltype(&echo_qk_norm_rope) g_rope = nullptr;
 decltype(&echo_indexer_qk) g_indexer = nullptr;
 decltype(&echo_newest_queries) g_newest = nullptr;
+decltype(&echo_block_topk) g_blocks = nullptr;
+decltype(&echo_sparse_attention) g_sparse = nullptr;
+decltype(&echo_prefix_attention) g_prefix = nullptr;
+decltype(&echo_attention_weights) g_weights = nullptr;
+decltype(&echo_pool_weigh) g_weigh = nullptr;
 
 struct Refused {};                  // a Python error is set
 
@@ -372,10 +377,187 @@ PyObject *newest_queries(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
   });
 }
 
+PyObject *block_topk(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, 11, [&] {
+    const char *fn = "echo_block_topk";
+    const at::Tensor *scores = tensor(fn, "scores", o[0]), *len = tensor(fn, "length", o[1]), *idx = tensor(fn, "idx", o[5]),
+                     *ws = tensor(fn, "ws", o[6]);
+    const int32_t max_len = integer32(fn, "max_len", o[2]), k = integer32(fn, "k", o[4]);
+    if (scores->scalar_type() != at::kFloat || scores->dim() != 2) refuse(fn, "scores is not an fp32 matrix");
+    const Where w(fn, scores);
+    const int64_t n = scores->size(0);
+    if (max_len > scores->size(1)) refuse(fn, "max_len is above the width of scores");
+    const int64_t ld = row_stride(fn, "scores", *scores);
+    want(w, "length", len, at::kInt, n);
+    want(w, "idx", idx, at::kInt, n * k);
+    want(w, "ws", ws, ws->scalar_type(), -1);
+    check(fn, g_blocks(static_cast<const float *>(address(scores)), ld, static_cast<const int32_t *>(address(len)), count32(fn, n), max_len,
+                       integer32(fn, "block", o[3]), integer32(fn, "n_first", o[7]), integer32(fn, "n_last", o[8]), k,
+                       static_cast<int32_t *>(address(idx)), address(ws), ws->nbytes(), w.stream(o[9], o[10] == Py_True)));
+  });
+}
+
+// q [rows, heads, 576] and kv [n, 576] of one 16-bit type.
+int32_t latent_type(const Where &w, const at::Tensor &q, const at::Tensor &kv) {
+  const char *fn = w.fn;
+  const int32_t kind = float_type(q.scalar_type());
+  if (kind < 0 || kind == ECHO_FP32 || kv.scalar_type() != q.scalar_type()) refuse(fn, "q and kv are not of one type, bf16 or fp16");
+  if (q.dim() != 3 || q.size(2) != ECHO_ROW_ELEMS || kv.dim() != 2 || kv.size(1) != ECHO_ROW_ELEMS)
+    refuse(fn, "q is not [rows, heads, %d] or kv not [n, %d]", ECHO_ROW_ELEMS, ECHO_ROW_ELEMS);
+  w.same("kv", &kv);
+  return kind;
+}
+void latent_out(const Where &w, const at::Tensor &q, const at::Tensor &out, const at::Tensor *lse, int64_t &row, int64_t &head) {
+  if (out.scalar_type() != q.scalar_type() || out.dim() != 3 || out.size(0) != q.size(0) || out.size(1) != q.size(1) || out.size(2) != ECHO_VALUE_ELEMS)
+    refuse(w.fn, "out is not [rows, heads, %d] of q's type", ECHO_VALUE_ELEMS);
+  w.same("out", &out);
+  head_strides(w.fn, "out", out, row, head);
+  want(w, "lse", lse, at::kFloat, q.size(0) * q.size(1));
+}
+
+constexpr int LATENT = 11;          // arguments of latent_args: q, kv, idx, block, length, page_table, page_size, req, scale, stream, any
+echo_latent_args latent_args(const Where &w, PyObject *const *o) {
+  const char *fn = w.fn;
+  const at::Tensor *q = tensor(fn, "q", o[0]), *kv = tensor(fn, "kv", o[1]), *idx = tensor(fn, "idx", o[2]), *len = tensor(fn, "length", o[4], true),
+                   *table = tensor(fn, "page_table", o[5], true), *req = tensor(fn, "req", o[7], true);
+  echo_latent_args a = {};
+  a.type = latent_type(w, *q, *kv);
+  const int64_t n = q->size(0);
+  if (idx->scalar_type() != at::kInt || idx->dim() != 2 || idx->size(0) != n) refuse(fn, "idx is not int32 [rows, k]");
+  w.same("idx", idx);
+  want(w, "length", len, at::kInt, n);
+  want(w, "req", req, at::kInt, n);
+  if (table) {
+    if (table->dim() != 2) refuse(fn, "page_table is not [requests, pages]");
+    want(w, "page_table", table, at::kInt, -1);
+    if (!req && table->size(0) != n) refuse(fn, "page_table has no row for each row of q, and no req is given");
+    a.page_table = static_cast<const int32_t *>(address(table));
+    a.page_size = integer32(fn, "page_size", o[6]);
+    if (a.page_size == 0) refuse(fn, "a page_table without a page_size");
+    a.n_tables = count32(fn, table->size(0));
+    a.max_pages = count32(fn, table->size(1));
+  } else if (req || integer(o[6]) != 0) {
+    refuse(fn, "req or page_size without a page_table");
+  }
+  a.n_rows = count32(fn, n);
+  a.n_heads = count32(fn, q->size(1));
+  a.scale = static_cast<float>(number(o[8]));
+  a.q = address(q);
+  head_strides(fn, "q", *q, a.q_row_stride, a.q_head_stride);
+  a.kv = address(kv);
+  a.kv_stride = row_stride(fn, "kv", *kv);
+  a.n_kv = count32(fn, kv->size(0));
+  a.k = count32(fn, idx->size(1));
+  a.block = integer32(fn, "block", o[3]);
+  a.idx = static_cast<const int32_t *>(address(idx));
+  a.idx_stride = row_stride(fn, "idx", *idx);
+  a.len = static_cast<const int32_t *>(address(len));
+  a.req = static_cast<const int32_t *>(address(req));
+  return a;
+}
+
+// o: the latent arguments (the last two are the stream and any), then out, lse, ws
+PyObject *sparse_attention(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, LATENT + 3, [&] {
+    const char *fn = "echo_sparse_attention";
+    const at::Tensor *q = tensor(fn, "q", o[0]), *out = tensor(fn, "out", o[LATENT]), *lse = tensor(fn, "lse", o[LATENT + 1], true),
+                     *ws = tensor(fn, "ws", o[LATENT + 2], true);
+    const Where w(fn, q);
+    const echo_latent_args a = latent_args(w, o);
+    int64_t row, head;
+    latent_out(w, *q, *out, lse, row, head);
+    if (ws) want(w, "ws", ws, ws->scalar_type(), -1);
+    check(fn, g_sparse(&a, address(out), row, head, static_cast<float *>(address(lse)), address(ws), ws ? ws->nbytes() : 0,
+                       w.stream(o[LATENT - 2], o[LATENT - 1] == Py_True)));
+  });
+}
+
+// o: the latent arguments, then lse, w
+PyObject *attention_weights(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, LATENT + 2, [&] {
+    const char *fn = "echo_attention_weights";
+    const at::Tensor *q = tensor(fn, "q", o[0]), *lse = tensor(fn, "lse", o[LATENT]), *out = tensor(fn, "w", o[LATENT + 1]);
+    const Where w(fn, q);
+    const echo_latent_args a = latent_args(w, o);
+    want(w, "lse", lse, at::kFloat, q->size(0) * q->size(1));
+    if (out->scalar_type() != at::kFloat || out->dim() != 2 || out->size(0) != a.n_rows || out->size(1) != static_cast<int64_t>(a.k) * a.block)
+      refuse(fn, "w is not fp32 [rows, k * block]");
+    w.same("w", out);
+    check(fn, g_weights(&a, static_cast<const float *>(address(lse)), static_cast<float *>(address(out)), row_stride(fn, "w", *out),
+                        w.stream(o[LATENT - 2], o[LATENT - 1] == Py_True)));
+  });
+}
+
+PyObject *prefix_attention(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, 16, [&] {
+    const char *fn = "echo_prefix_attention";
+    const at::Tensor *q = tensor(fn, "q", o[0]), *kv = tensor(fn, "kv", o[1]), *out = tensor(fn, "out", o[2]), *begin = tensor(fn, "group_begin", o[4]),
+                     *plen = tensor(fn, "prefix_len", o[5]), *ptab = tensor(fn, "prefix_table", o[6]), *olen = tensor(fn, "own_len", o[7]),
+                     *otab = tensor(fn, "own_table", o[8]), *ws = tensor(fn, "ws", o[12], true), *lse = tensor(fn, "lse", o[13], true);
+    const Where w(fn, q);
+    echo_prefix_args a = {};
+    a.type = latent_type(w, *q, *kv);
+    const int64_t n = q->size(0), groups = plen->numel();
+    want(w, "prefix_len", plen, at::kInt, groups);
+    want(w, "group_begin", begin, at::kInt, groups + 1);
+    want(w, "own_len", olen, at::kInt, n);
+    if (ptab->dim() != 2 || ptab->size(0) != groups || otab->dim() != 2 || otab->size(0) != n)
+      refuse(fn, "prefix_table has no row for each group or own_table none for each row of q");
+    want(w, "prefix_table", ptab, at::kInt, -1);
+    want(w, "own_table", otab, at::kInt, -1);
+    int64_t row, head;
+    latent_out(w, *q, *out, lse, row, head);
+    if (ws) want(w, "ws", ws, ws->scalar_type(), -1);
+    a.n_rows = count32(fn, n);
+    a.n_heads = count32(fn, q->size(1));
+    a.scale = static_cast<float>(number(o[3]));
+    a.q = address(q);
+    head_strides(fn, "q", *q, a.q_row_stride, a.q_head_stride);
+    a.kv = address(kv);
+    a.kv_stride = row_stride(fn, "kv", *kv);
+    a.n_kv = count32(fn, kv->size(0));
+    a.page_size = integer32(fn, "page_size", o[9]);
+    a.n_groups = count32(fn, groups);
+    a.max_prefix = integer32(fn, "max_prefix", o[10]);
+    a.prefix_pages = count32(fn, ptab->size(1));
+    a.max_own = integer32(fn, "max_own", o[11]);
+    a.own_pages = count32(fn, otab->size(1));
+    a.group_begin = static_cast<const int32_t *>(address(begin));
+    a.prefix_len = static_cast<const int32_t *>(address(plen));
+    a.prefix_table = static_cast<const int32_t *>(address(ptab));
+    a.own_len = static_cast<const int32_t *>(address(olen));
+    a.own_table = static_cast<const int32_t *>(address(otab));
+    check(fn, g_prefix(&a, address(out), row, head, static_cast<float *>(address(lse)), address(ws), ws ? ws->nbytes() : 0,
+                       w.stream(o[14], o[15] == Py_True)));
+  });
+}
+
+PyObject *pool_weigh(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
+  return guarded(n_args, 10, [&] {
+    const char *fn = "echo_pool_weigh";
+    const at::Tensor *free_ = tensor(fn, "free", o[0]), *priority = tensor(fn, "priority", o[1]), *mass = tensor(fn, "mass", o[2]),
+                     *slot = tensor(fn, "slot", o[3]), *hw = tensor(fn, "w", o[4]), *ws = tensor(fn, "ws", o[5]), *fresh = tensor(fn, "fresh", o[7], true);
+    const Where w(fn, free_);
+    const int64_t n = free_->numel(), entries = slot->numel();
+    want(w, "free", free_, free_->scalar_type() == at::kBool ? at::kBool : at::kByte, n);
+    want(w, "priority", priority, at::kInt, n);
+    want(w, "mass", mass, at::kFloat, n);
+    want(w, "slot", slot, at::kInt, entries);
+    want(w, "w", hw, at::kFloat, entries);
+    want(w, "fresh", fresh, at::kInt, -1);
+    want(w, "ws", ws, ws->scalar_type(), -1);
+    check(fn, g_weigh(static_cast<const uint8_t *>(address(free_)), static_cast<int32_t *>(address(priority)), static_cast<float *>(address(mass)),
+                      count32(fn, n), static_cast<const int32_t *>(address(slot)), static_cast<const float *>(address(hw)), entries,
+                      static_cast<const int32_t *>(address(fresh)), fresh ? fresh->numel() : 0, static_cast<float>(number(o[6])), address(ws),
+                      ws->nbytes(), w.stream(o[8], o[9] == Py_True)));
+  });
+}
+
 // (EchoError, raw_stream, addresses of echo_last_error, echo_page_step, echo_quant_fp8,
-// echo_matmul_fp8, echo_qk_norm_rope, echo_indexer_qk, echo_newest_queries)
+// echo_matmul_fp8, echo_qk_norm_rope, echo_indexer_qk, echo_newest_queries, echo_block_topk,
+// echo_sparse_attention, echo_prefix_attention, echo_attention_weights, echo_pool_weigh)
 PyObject *setup(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
-  return guarded(n_args, 9, [&] {
+  return guarded(n_args, 14, [&] {
     auto fn = [&](int i) { return reinterpret_cast<void *>(integer(o[i])); };
     Py_INCREF(o[0]);
     Py_INCREF(o[1]);
@@ -388,12 +570,18 @@ PyObject *setup(PyObject *, PyObject *const *o, Py_ssize_t n_args) {
     g_rope = reinterpret_cast<decltype(g_rope)>(fn(6));
     g_indexer = reinterpret_cast<decltype(g_indexer)>(fn(7));
     g_newest = reinterpret_cast<decltype(g_newest)>(fn(8));
+    g_blocks = reinterpret_cast<decltype(g_blocks)>(fn(9));
+    g_sparse = reinterpret_cast<decltype(g_sparse)>(fn(10));
+    g_prefix = reinterpret_cast<decltype(g_prefix)>(fn(11));
+    g_weights = reinterpret_cast<decltype(g_weights)>(fn(12));
+    g_weigh = reinterpret_cast<decltype(g_weigh)>(fn(13));
   });
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(setup), CALL(page_step), CALL(quant_fp8), CALL(matmul_fp8), CALL(qk_norm_rope),
-                         CALL(indexer_qk), CALL(newest_queries), {nullptr, nullptr, 0, nullptr}};
+                         CALL(indexer_qk), CALL(newest_queries), CALL(block_topk), CALL(sparse_attention),
+                         CALL(prefix_attention), CALL(attention_weights), CALL(pool_weigh), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -41,6 +41,7 @@ extern "C" {
 #define ECHO_H_INDEX 64
 #define ECHO_D_INDEX 128
 #define ECHO_ROW_ELEMS 576 /* MLA latent row: 512 compressed + 64 RoPE values (bf16 bits) */
+#define ECHO_VALUE_ELEMS 512 /* its compressed values: what attention sums */
 #define ECHO_INF 0x7FFFFFFF
 #define ECHO_MAX_TOPK 4096
 #define ECHO_FUSED_MAX_RANGE 8192      /* tokens per range of the fused prefetch, at most */
@@ -728,6 +729,134 @@ int echo_indexer_qk(const echo_qk_args *a, const float *w, int64_t w_tok_stride,
 int echo_newest_queries(const uint8_t *q8, const float *w, const int32_t *row_begin, const int32_t *len,
                         int32_t n_rows, int32_t n_tok, int32_t n_q_heads, uint8_t *q_out, float *w_out,
                         int32_t *len_out, void *stream);
+
+/*
+ * Behind the selection: attention over the latent rows that were selected, over blocks of a paged
+ * cache or over a shared prefix, and the weight each token got there as the pool's eviction order.
+ * A latent row (ECHO_ROW_ELEMS values) is one token's key for every head, its first ECHO_VALUE_ELEMS
+ * values are the token's value.  In the order of a step: echo_decode_select (topk_slot, rows in
+ * gpu_kv) or echo_topk / echo_block_topk (positions or blocks of a paged cache),
+ * echo_sparse_attention, echo_attention_weights, echo_pool_weigh.
+ */
+
+/*
+ * The k blocks of `block` consecutive tokens that each row's scores select: block b < ceil(len[r] /
+ * block) scores the largest of scores[r * ld + t] over its tokens t < len[r]; the first n_first and the
+ * last n_last blocks of the row score +infinity.  Then as echo_topk over the blocks: the highest k, ties
+ * to the lower block, written to idx[r * k ..] in ascending order, -1 padded.  len[r] above max_len
+ * is clamped, below 0 is 0.  NaN scores are outside the contract.  block is a power of two in [16, 65536],
+ * 1 <= k <= ECHO_MAX_TOPK, ld >= max_len.  Workspace: echo_block_topk_workspace_bytes; calls that may run
+ * at the same time need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, ld < max_len, NULL
+ * pointers and arrays not aligned to their types; ECHO_EUNSUPPORTED for other blocks or k and for more than
+ * a launch holds (2^22 rows, 2^26 waves of 256 tokens or, where larger, a block); ECHO_EWORKSPACE.
+ */
+size_t echo_block_topk_workspace_bytes(int32_t n_rows, int32_t max_len, int32_t block);
+int echo_block_topk(const float *scores, int64_t ld, const int32_t *len, int32_t n_rows, int32_t max_len, int32_t block,
+                    int32_t n_first, int32_t n_last, int32_t k, int32_t *idx, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Queries of n_rows tokens and the cache rows each of them attends to.  Row r lists entries idx[r *
+ * idx_stride + i], i < k, each of them `block` (a power of two, 1 to 65536) consecutive positions
+ * from entry * block on; a negative entry lists nothing, and an entry listed twice counts twice.  A position at or behind
+ * len[r] (len may be NULL: none) is passed over.  Position p is row p of the cache, or, with page_size
+ * != 0, row page_table[t * max_pages + p / page_size] * page_size + p % page_size with t = req[r] (req
+ * may be NULL: r), page_size a power of two in [16, 65536].  A position whose page lies behind
+ * max_pages, a t outside [0, n_tables) and a row outside [0, n_kv) are passed over too: nothing
+ * outside the arrays is read, and nothing of a row that is passed over gets into a result, NaN or not.
+ */
+typedef struct {
+  int32_t n_rows, n_heads;   /* up to 2^22 rows, 1024 heads */
+  int32_t type;              /* ECHO_BF16 or ECHO_FP16: q, kv and the output */
+  float scale;               /* of the scores; |scale| <= 1e38 */
+  const void *q;             /* [n_rows, n_heads, 576], strides in elements */
+  int64_t q_row_stride, q_head_stride;
+  const void *kv;            /* [n_kv, 576] */
+  int64_t kv_stride;
+  int32_t n_kv;
+  int32_t k, block;
+  const int32_t *idx;
+  int64_t idx_stride;
+  const int32_t *len;        /* [n_rows] or NULL */
+  const int32_t *page_table; /* [n_tables, max_pages], with page_size != 0 */
+  int32_t page_size, max_pages, n_tables;
+  const int32_t *req;        /* [n_rows] or NULL */
+} echo_latent_args;
+
+/*
+ * out[r][h] = sum over row r's tokens t of p_t * kv[t][0 .. 512), p = softmax of the scores scale *
+ * (q[r][h] . kv[t]); lse[r * n_heads + h] = log sum exp of the scores (natural, lse may be NULL).  A
+ * row without a token gives zeros and -infinity.  Products are exact in fp32; scores, maxima and sums
+ * are fp32; the weights are rounded to the type for the second product (half a step each), the result
+ * once.  Scores behind fp32's range, and infinities or NaN in rows that are attended to, give what the formula gives
+ * in fp32.  The same call gives the same bits always (no atomics); how a row's tokens are cut into
+ * chunks, and with it the last bits, goes by n_rows, n_heads and k * block.  q, kv and out and their
+ * strides are multiples of 16 bytes; out's heads overlap nothing.  Workspace:
+ * echo_sparse_attention_workspace_bytes with n_tok = k * block (0 where no row is cut); calls that
+ * may run at the same time need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, NULL
+ * pointers, other types, overlapping heads of out, arrays not aligned to their types; ECHO_EUNSUPPORTED
+ * for alignments, blocks, page sizes and sizes outside these limits (k * block up to 2^28, 2^24 workgroups);
+ * ECHO_EWORKSPACE.  No rows or heads: ECHO_OK.
+ */
+size_t echo_sparse_attention_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_tok);
+int echo_sparse_attention(const echo_latent_args *a, void *out, int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a batch whose requests share prefixes: rows [group_begin[g], group_begin[g + 1]) attend
+ * to the first prefix_len[g] positions of row g of prefix_table and then to the first own_len[r]
+ * positions of row r of own_table, as one softmax; a row in no group has its own tokens only.
+ * A prefix is read once for up to 64 heads of all the rows in its group.  Both tables go into the same cache, in
+ * pages of page_size tokens.  group_begin is ascending in [0, n_rows] (other values: rows of
+ * unspecified content, nothing read or written elsewhere).  Lengths above max_prefix and max_own are
+ * clamped, below 0 are 0; what lies outside tables or cache is passed over, as above.  Results, errors,
+ * alignments and workspace as echo_sparse_attention; ECHO_EUNSUPPORTED for more than 65536 groups too.
+ */
+typedef struct {
+  int32_t n_rows, n_heads, type;
+  float scale;
+  const void *q;             /* [n_rows, n_heads, 576] */
+  int64_t q_row_stride, q_head_stride;
+  const void *kv;            /* [n_kv, 576] */
+  int64_t kv_stride;
+  int32_t n_kv, page_size;
+  int32_t n_groups, max_prefix, prefix_pages, max_own, own_pages;
+  const int32_t *group_begin;   /* [n_groups + 1] */
+  const int32_t *prefix_len;    /* [n_groups] */
+  const int32_t *prefix_table;  /* [n_groups, prefix_pages] */
+  const int32_t *own_len;       /* [n_rows] */
+  const int32_t *own_table;     /* [n_rows, own_pages] */
+} echo_prefix_args;
+size_t echo_prefix_attention_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_t max_prefix,
+                                             int32_t max_own);
+int echo_prefix_attention(const echo_prefix_args *a, void *out, int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * What each listed token got from all heads of its row in an attention that gave lse [n_rows, n_heads]:
+ * w[r * w_stride + i] = sum over h of exp(scale * (q[r][h] . kv[t]) - lse[r][h]) for token i < k * block
+ * of row r's list, 0 where a token is passed over.  fp32 throughout.  Limits and errors as
+ * echo_sparse_attention, ECHO_EINVAL for no heads and for rows of w that overlap.
+ */
+int echo_attention_weights(const echo_latent_args *a, const float *lse, float *w, int64_t w_stride, void *stream);
+
+/*
+ * Eviction by accumulated attention weight.  mass [n_gpu] holds each pool slot's weight so far:
+ *     mass[s] = decay * (fresh ? 0 : mass[s]) + the sum of w[i] over the entries with slot[i] = s,
+ * where a slot is fresh if fresh [n_fresh] lists it (the step's miss_slot: it holds another token now), and
+ * gpu_priority[s] = the bits of mass[s] as an integer, which keep its order, so that the pool step
+ * (echo_pool_lookup_alloc, echo_decode_select) evicts the unprotected slots of the smallest
+ * accumulated weight first, ties to the lower slot.  Free slots get mass 0 and priority -1.  Entries and
+ * fresh slots outside [0, n_gpu) (-1: padding) are passed over.  A slot's weights are added up in
+ * units of 2^-32, each clamped to [0, 1024] (NaN: 0), so their order does not matter, and a slot may be listed
+ * any number of times; the sum is rounded to fp32 and added to the product in fp32.  A mass below 0 or
+ * NaN counts as 0.  0 <= decay <= 1.  Up to 2^22 slots, 2^21 entries and 2^21 fresh slots
+ * (ECHO_EUNSUPPORTED).  Workspace: echo_pool_weigh_workspace_bytes, 8-byte aligned; calls that
+ * may run at the same time need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, NULL pointers,
+ * decay outside its range, arrays not aligned to their types; ECHO_EWORKSPACE.  The arrays overlap nothing.
+ */
+size_t echo_pool_weigh_workspace_bytes(int32_t n_gpu);
+int echo_pool_weigh(const uint8_t *gpu_free, int32_t *gpu_priority, float *mass, int32_t n_gpu, const int32_t *slot, const float *w,
+                    int64_t n_entries, const int32_t *fresh, int64_t n_fresh, float decay, void *ws, size_t ws_bytes, void *stream);
 
 /* Text of the last error on this thread ("" if none). */
 const char *echo_last_error(void);

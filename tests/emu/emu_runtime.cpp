@@ -446,22 +446,28 @@ static void op_mfma(const unsigned char *in, unsigned char *out, size_t, size_t,
   }
 }
 
-// 16x16x32 bf16 MFMA: lane l supplies row l%16 of A and column l%16 of B for K elements
+// 16x16x32 bf16 and fp16 MFMA: lane l supplies row l%16 of A and column l%16 of B for K elements
 // [8 (l/16), 8 (l/16) + 8); the result as above.
 static float bf16_value(const unsigned char *p) {
   unsigned short h;
   memcpy(&h, p, 2);
   return __uint_as_float(static_cast<unsigned>(h) << 16);
 }
+static float fp16_value(const unsigned char *p) {
+  _Float16 h;
+  memcpy(&h, p, 2);
+  return static_cast<float>(h);
+}
 struct MfmaBf16In { unsigned char a[16], b[16]; v4f_emu c; };
-static void op_mfma_bf16(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
+template <float (*VALUE)(const unsigned char *)>
+static void op_mfma_16bit(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
   static float A[16][32], B[32][16];
   for (int l = 0; l < 64; ++l) {
     MfmaBf16In x;
     memcpy(&x, in + l * SLOT, sizeof x);
     for (int q = 0; q < 8; ++q) {
-      A[l % 16][8 * (l / 16) + q] = bf16_value(x.a + 2 * q);
-      B[8 * (l / 16) + q][l % 16] = bf16_value(x.b + 2 * q);
+      A[l % 16][8 * (l / 16) + q] = VALUE(x.a + 2 * q);
+      B[8 * (l / 16) + q][l % 16] = VALUE(x.b + 2 * q);
     }
   }
   for (int l = 0; l < 64; ++l) {
@@ -475,6 +481,13 @@ static void op_mfma_bf16(const unsigned char *in, unsigned char *out, size_t, si
     }
     memcpy(out + l * SLOT, &r, 16);
   }
+}
+
+// Of each 16 lanes' four 16-bit values: lane j gets value j % 4 of lanes j / 4, 4 + j / 4, 8 + j / 4 and 12 + j / 4.
+static void op_transpose(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
+  for (int l = 0; l < 64; ++l)
+    for (int i = 0; i < 4; ++i)
+      memcpy(out + l * SLOT + 2 * i, in + ((l & ~15) + 4 * i + (l & 15) / 4) * SLOT + 2 * (l & 3), 2);
 }
 
 }  // namespace emu
@@ -574,7 +587,22 @@ v4f_emu emu_amdgcn_mfma_f32_16x16x32_bf16(v8bf_emu a, v8bf_emu b, v4f_emu c, int
   memcpy(x.b, &b, 16);
   x.c = c;
   v4f_emu r;
-  wave_op(&x, sizeof x, &r, 16, op_mfma_bf16, nullptr);
+  wave_op(&x, sizeof x, &r, 16, op_mfma_16bit<bf16_value>, nullptr);
+  return r;
+}
+v4f_emu emu_amdgcn_mfma_f32_16x16x32_f16(v8h_emu a, v8h_emu b, v4f_emu c, int, int, int) {
+  MfmaBf16In x;
+  memcpy(x.a, &a, 16);
+  memcpy(x.b, &b, 16);
+  x.c = c;
+  v4f_emu r;
+  wave_op(&x, sizeof x, &r, 16, op_mfma_16bit<fp16_value>, nullptr);
+  return r;
+}
+v4s_emu emu_amdgcn_ds_read_tr16_b64_v4i16(const v4s_emu *p) {
+  const v4s_emu mine = *p;                                // read here: under the sanitizers
+  v4s_emu r;
+  wave_op(&mine, 8, &r, 8, op_transpose, nullptr);
   return r;
 }
 

@@ -145,6 +145,14 @@ typedef __bf16 v2bf_emu __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf_emu __attribute__((ext_vector_type(8)));
 v2bf_emu emu_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned src, float scale, bool high);
 v4f_emu emu_amdgcn_mfma_f32_16x16x32_bf16(v8bf_emu a, v8bf_emu b, v4f_emu c, int, int, int);
+typedef _Float16 v8h_emu __attribute__((ext_vector_type(8)));
+v4f_emu emu_amdgcn_mfma_f32_16x16x32_f16(v8h_emu a, v8h_emu b, v4f_emu c, int, int, int);
+// transposing LDS read: of 16 lanes' 8 bytes each, lane j gets element j % 4 of lanes j / 4, 4 + j / 4, ..
+typedef short v4s_emu __attribute__((ext_vector_type(4)));
+v4s_emu emu_amdgcn_ds_read_tr16_b64_v4i16(const v4s_emu *p);
+// 2^x and log2 x; results below the smallest normal number are 0
+inline float emu_amdgcn_exp2f(float x) { const float r = std::exp2(x); return r < 1.17549435e-38f ? 0.f : r; }
+inline float emu_amdgcn_logf(float x) { return std::log2(x); }
 // global memory straight to LDS: the wave's base plus the lane's place (done at once here)
 inline void emu_amdgcn_global_load_lds(const void *g, void *lds, unsigned size, int, unsigned) {
   memcpy(static_cast<char *>(lds) + emu::ctx()->lane * size, g, size);
