@@ -2,14 +2,19 @@
 // echo_prefix_attention).  One row of 576 values per token serves all heads:
 //   s_t = scale * q . row_t,   out = sum_t softmax(s)_t row_t[0 .. 512),   lse = log sum_t exp s_t.
 //
-// A workgroup takes 16 MT query heads that share their tokens and a chunk of those tokens, in
-// tiles of 64.  A tile is 72 KB, loaded straight to LDS while the one before is multiplied; it is read
-// from memory once for all the heads and used twice, as rows (scores) and as columns (sum).
-//   scores   wave w multiplies tokens 16 w .. 16 w + 15 with all heads, whose 576 values it holds in
-//            registers: every row of the tile is read from LDS once in all.
-//   softmax  base 2, running maximum and sum per head; the maximum of a tile's four waves through LDS.
-//   sum      wave w adds up columns 128 w .. 128 w + 127 over all 64 tokens: it reads the weights of
-//            all waves from LDS and the columns with transposing reads.
+// A workgroup takes 32 QT queries that share their tokens (heads of one row, or of the rows behind one
+// prefix) and a chunk of those tokens, in tiles of 32.  Its four waves:
+//   scores   wave w multiplies 16 of the tile's tokens (w % 2) with 16 QT of the queries (w / 2), whose 576 values
+//            stay in registers; the rows come from LDS.
+//   softmax  base 2, relative to a maximum per query that all waves know.  It is raised only when a score exceeds
+//            it by 2^8: weights up to 2^8 are as exact as those up to 1, and neither the waves' maxima have to be
+//            exchanged nor the sums multiplied but then.  The weights go to LDS.
+//   sum      wave w adds up columns 128 w .. 128 w + 127 of all queries over all 32 tokens: the weights from
+//            LDS, the rows' columns from LDS through transposing reads.
+// A wave multiplies the scores of tile t + 1 while the weights of tile t are summed, so one barrier a tile
+// is enough and the vector unit's exponentials run beside the matrix core.  Rows go from the cache straight to
+// LDS, two to three tiles (74 to 110 KB) ahead.
+//
 // Weights are rounded to the cache's type for the product, as the matrix core takes them (off by half a
 // step of the type each, which in a sum of many is what the result's own rounding is); scores, sums,
 // maxima and the results are fp32.
@@ -22,8 +27,10 @@
 
 namespace echo {
 
-constexpr int TILE = 64, WAVES = 4, COLS = VALUES / WAVES;       // tokens of a tile, columns of a wave
-constexpr int KSTEPS = LATENT / 32;
+constexpr int WAVES = 4, TILE = 32, STAGES = 4;            // tokens of a tile, tiles in LDS
+constexpr int KSTEPS = LATENT / 32, COLS = VALUES / WAVES; // products of a score, columns of a wave
+constexpr int LOADS = TILE / WAVES + 1;                    // a wave's loads of a tile
+constexpr float SLACK = 8.f;
 
 // Tokens whose list entry, position or page leads nowhere read this row instead of the cache, so that
 // nothing of the cache's contents can get into a sum through a weight of 0.
@@ -31,9 +38,9 @@ __device__ const uint32_t g_zero_row[LATENT / 2] = {};
 
 // A tile in LDS: the rows' first 512 values, 1024 bytes a row, then their last 64, 128 bytes a row.
 // Pieces of 16 bytes are exchanged within a row so that the reads of 16 rows at one piece (scores) and of
-// 8 rows at one 32-byte column group (sums) touch every bank once.
+// four rows at 64 bytes (sums) touch every bank once.
 constexpr int ROPE_AT = TILE * 1024, STAGE = TILE * LATENT * 2;
-ECHO_DEV constexpr int swap_v(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
+ECHO_DEV constexpr int swap_v(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
 ECHO_DEV constexpr int swap_r(int row) { return (row >> 1) & 7; }
 
 struct AttArgs {
@@ -56,190 +63,286 @@ struct Work {
   int32_t t0, t1, part;
 };
 
-template <int MT>
 struct Lds {
-  static constexpr int P = 2 * STAGE, MX = P + MT * 16 * TILE * 2, SIZE = MX + WAVES * MT * 16 * 4;
-  static_assert(SIZE <= 160 * 1024, "a workgroup's LDS");
+  uint8_t stage[STAGES][STAGE];
+  uint8_t p[2][64 * TILE * 2];   // weights by query: 4 pieces of 8 tokens
+  float m[64], top[2][64];       // maxima; a tile's, or at the end the sums
+  int32_t raise[2];              // t + 1: tile t (by t % 2) has a score far above its maximum
 };
+static_assert(sizeof(Lds) <= 160 * 1024, "a workgroup's LDS");
 
-// The wave's 16 rows of a tile to LDS; lane i and every 16th after it hold the cache row of the wave's row i.
+// The wave's 8 rows of a tile to LDS; lane i holds the cache row of the tile's row i.
 ECHO_DEV void fetch(const AttArgs &x, int32_t row, uint8_t *__restrict__ stage, int wv) {
   const int l = lane_id();
-  const uint8_t *kv = reinterpret_cast<const uint8_t *>(x.a.kv);
+  const uint8_t *kv = reinterpret_cast<const uint8_t *>(x.a.kv), *zero = reinterpret_cast<const uint8_t *>(g_zero_row);
   const int64_t stride = x.a.kv_stride * 2;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int32_t r = __builtin_amdgcn_readlane(row, i);
-    const uint8_t *src = r < 0 ? reinterpret_cast<const uint8_t *>(g_zero_row) : kv + r * stride;
-    __builtin_amdgcn_global_load_lds((glb_void *)(src + ((l ^ swap_v(i)) << 4)), (lds_void *)(stage + (wv * 16 + i) * 1024), 16, 0, 0);
+  for (int i = 0; i < TILE / WAVES; ++i) {
+    const int at = wv * (TILE / WAVES) + i;
+    const int32_t r = __builtin_amdgcn_readlane(row, at);
+    const uint8_t *src = r < 0 ? zero : kv + r * stride;
+    __builtin_amdgcn_global_load_lds((glb_void *)(src + ((l ^ swap_v(at)) << 4)), (lds_void *)(stage + at * 1024), 16, 0, 0);
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = 8 * i + (l >> 3);
-    const int32_t r = __shfl(row, at, 64);
-    const uint8_t *src = r < 0 ? reinterpret_cast<const uint8_t *>(g_zero_row) : kv + r * stride;
-    __builtin_amdgcn_global_load_lds((glb_void *)(src + 1024 + (((l & 7) ^ swap_r(at)) << 4)),
-                                     (lds_void *)(stage + ROPE_AT + (wv * 16 + 8 * i) * 128), 16, 0, 0);
-  }
+  const int at = wv * (TILE / WAVES) + (l >> 3);
+  const int32_t r = __shfl(row, at, 64);
+  const uint8_t *src = r < 0 ? zero : kv + r * stride;
+  __builtin_amdgcn_global_load_lds((glb_void *)(src + 1024 + (((l & 7) ^ swap_r(at)) << 4)), (lds_void *)(stage + ROPE_AT + wv * 1024), 16, 0, 0);
 }
 
-template <typename T, int MT>
-struct Heads {
+template <typename T, int QT>
+struct Waves {
   typedef typename Mma<T>::x8 x8;
-  x8 q[MT][KSTEPS];
-  v4f o[MT][COLS / 16];
-  float m[MT], sum[MT];          // running maximum (base 2); this lane's part of the sum of weights
+  x8 q[QT][KSTEPS];              // 16 QT queries: lane (j, g) values of query 16 i + j
+  v4f s[QT];                     // a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
+  float m[QT], sum[QT], tile_sum[QT];
+  v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
+  int wv, qb, th;                // qb: the wave's first query for scores
 
-  // Scores of the wave's tokens, softmax step and sum over the tile's tokens.  `real`: which of the wave's
-  // 16 tokens there are.
-  ECHO_DEV void tile(const uint8_t *__restrict__ cur, uint8_t *__restrict__ pbuf, float *__restrict__ mx, float scale2,
-                     uint32_t real, int wv) {
+  // Scores of a tile and their weights; `real`: the tile's tokens that there are.
+  ECHO_DEV void scores(const uint8_t *__restrict__ stage, float scale2, uint32_t real) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-    v4f s[MT];
+    const uint8_t *vrow = stage + (th * 16 + j) * 1024, *rrow = stage + ROPE_AT + (th * 16 + j) * 128;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const uint8_t *vrow = cur + (wv * 16 + j) * 1024, *rrow = cur + ROPE_AT + (wv * 16 + j) * 128;
+    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k) {
-      const x8 row = k < 16 ? read16<x8>(vrow + (((4 * k + g) ^ swap_v(j)) << 4))
+      const x8 row = k < 16 ? read16<x8>(vrow + (((k + 16 * g) ^ swap_v(j)) << 4))
                             : read16<x8>(rrow + (((4 * (k - 16) + g) ^ swap_r(j)) << 4));
 #pragma unroll
-      for (int i = 0; i < MT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
+      for (int i = 0; i < QT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
     }
-    // Lane (j, g) has head j's scores of tokens 4 g .. 4 g + 3 of the wave's 16.
-    const uint32_t mine = real >> (4 * g);
+    const uint32_t mine = real >> (16 * th + 4 * g);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      float top = NO_SCORE;
+    for (int v = 0; v < 4; ++v) {
+      const float none = mine >> v & 1 ? 0.f : -INFINITY;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        s[i][v] *= scale2;
-        if (mine >> v & 1) top = fmaxf(top, s[i][v]);
-      }
+      for (int i = 0; i < QT; ++i) s[i][v] = fmaf(s[i][v], scale2, none);
+    }
+  }
+  ECHO_DEV void weigh(uint8_t *__restrict__ p) {
+    const int l = lane_id(), j = l & 15, g = l >> 4;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      v4f w;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) w[v] = exp2_(s[i][v] - m[i]);
+      tile_sum[i] = (w[0] + w[1]) + (w[2] + w[3]);
+      const int at = qb + 16 * i + j;
+      *reinterpret_cast<u32x2 *>(p + at * 64 + (((2 * th + (g >> 1)) ^ ((at >> 2) & 3)) << 4) + 8 * (g & 1)) = pack4<T>(w);
+    }
+  }
+  // Keeps the sums where the matrix core adds them up: an empty statement that takes and gives accumulation registers.
+  ECHO_DEV void pin() {
+#pragma unroll
+    for (int i = 0; i < QT; ++i)
+#pragma unroll
+      for (int c = 0; c < COLS / 32; ++c) asm volatile("" : "+a"(o[i][c]));
+  }
+  ECHO_DEV static float top_of(const v4f &s) { return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])); }
+  ECHO_DEV bool far_above() const {
+    bool f = false;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) f |= top_of(s[i]) > m[i] + SLACK;
+    return __ballot(f) != 0;
+  }
+  // Every wave: maxima up to those of the tile, sums and weights on the new scale.
+  ECHO_DEV void raise(Lds &lds, uint8_t *__restrict__ p) {
+    const int l = lane_id(), j = l & 15, g = l >> 4;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      float top = top_of(s[i]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      if (g == 0) mx[wv * MT * 16 + i * 16 + j] = top;
+      if (g == 0) lds.top[th][qb + 16 * i + j] = top;
     }
     meet();
+    pin();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      float top = m[i];
+    for (int i = 0; i < QT; ++i) {
+      const int at = 32 * i + (l & 31);
+      const float was = lds.m[at], less = exp2_(was - fmaxf(was, fmaxf(lds.top[0][at], lds.top[1][at])));
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, mx[w * MT * 16 + i * 16 + j]);
-      const float less = exp2_(m[i] - top);
-      m[i] = top;
-      v4f p;
+      for (int c = 0; c < COLS / 32; ++c)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) p[v] = mine >> v & 1 ? exp2_(s[i][v] - top) : 0.f;
-      sum[i] = sum[i] * less + ((p[0] + p[1]) + (p[2] + p[3]));
+        for (int v = 0; v < 16; ++v) o[i][c][v] *= less;
+    }
+    pin();
+    float to[QT];
 #pragma unroll
-      for (int c = 0; c < COLS / 16; ++c)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[i][c][v] *= less;
-      // Weights by head: the 32 tokens of two waves as 4 groups of 8, group g the tokens 4 g .. 4 g + 3 of both.
-      *reinterpret_cast<u32x2 *>(pbuf + (i * 16 + j) * 128 + (((4 * (wv >> 1) + g) ^ swap_r(j)) << 4) + 8 * (wv & 1)) = pack4<T>(p);
+    for (int i = 0; i < QT; ++i) {
+      const int at = qb + 16 * i + j;
+      to[i] = fmaxf(m[i], fmaxf(lds.top[0][at], lds.top[1][at]));
+      sum[i] *= exp2_(m[i] - to[i]);
+      m[i] = to[i];
     }
     meet();
-    const int r = 4 * g + (j >> 2);
+    if (th == 0 && g == 0)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x8 p[MT];
+      for (int i = 0; i < QT; ++i) lds.m[qb + 16 * i + j] = to[i];
+    weigh(p);
+    meet();
+  }
+  // Product k takes tokens 16 k + 8 h .. + 7.
+  ECHO_DEV void add(const uint8_t *__restrict__ stage, const uint8_t *__restrict__ p) {
+    const int l = lane_id(), j = l & 31, h = l >> 5;
+    const int r = 8 * h + ((l & 15) >> 2);
+    x8 w[QT][2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) p[i] = read16<x8>(pbuf + (i * 16 + j) * 128 + (((4 * h + g) ^ swap_r(j)) << 4));
+    for (int i = 0; i < QT; ++i)
 #pragma unroll
-      for (int c = 0; c < COLS / 16; ++c) {
-        const int piece = (wv * (COLS / 8) + 2 * c + ((j >> 1) & 1)) ^ swap_v(r);
-        const uint8_t *at = cur + (32 * h + r) * 1024 + (piece << 4) + 8 * (j & 1);
+      for (int k = 0; k < 2; ++k) w[i][k] = read16<x8>(p + (32 * i + j) * 64 + (((2 * k + h) ^ ((j >> 2) & 3)) << 4));
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         struct { v4s lo, hi; } e;
-        e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
-        e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 16 * 1024));
+        const int piece = wv * (COLS / 8) + 4 * c + 2 * ((l >> 4) & 1) + ((l >> 1) & 1);
+        const uint8_t *at = stage + (16 * k + r) * 1024 + 8 * (l & 1);
+        e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + ((piece ^ swap_v(r)) << 4)));
+        e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 4 * 1024 + ((piece ^ swap_v(r + 4)) << 4)));
         const x8 col = __builtin_bit_cast(x8, e);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) o[i][c] = Mma<T>::mul(col, p[i], o[i][c]);
+        for (int i = 0; i < QT; ++i) o[i][c] = Mma<T>::mul(col, w[i][k], o[i][c]);
       }
-    }
   }
 };
 
-template <typename T, int MT>
-ECHO_DEV void attend(const AttArgs &x, const Work &w, uint8_t *__restrict__ lds) {
-  typedef Heads<T, MT> H;
+template <typename T, int QT>
+ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int l = lane_id(), j = l & 15, g = l >> 4;
-  H hd;
+  Waves<T, QT> a;
+  a.wv = wv;
+  a.qb = (wv >> 1) * 16 * QT;
+  a.th = wv & 1;
+  // A negative scale goes into the queries' signs, no scale makes them 0: a masked product then stays at -infinity.
+  const uint32_t flip = x.a.scale2 < 0.f ? 0x80008000u : 0u, keep = x.a.scale2 == 0.f ? 0u : ~0u;
+  const float scale2 = x.a.scale2 == 0.f ? 1.f : fabsf(x.a.scale2);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t qi = min(w.q0 + i * 16 + j, w.q1 - 1);
-    const int64_t r = qi / x.a.n_heads;
-    const uint16_t *q = x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head + 8 * g;
+  for (int i = 0; i < QT; ++i) {
+    const int64_t qi = min(w.q0 + a.qb + 16 * i + j, w.q1 - 1), r = qi / x.a.n_heads;
+    const uint16_t *q = x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head;
 #pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) hd.q[i][k] = read16<typename H::x8>(q + 32 * k);
-    hd.m[i] = NO_SCORE;
-    hd.sum[i] = 0.f;
+    for (int k = 0; k < KSTEPS; ++k) {
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(q + 8 * (k < 16 ? k + 16 * g : 64 + 4 * (k - 16) + g));
+      a.q[i][k] = __builtin_bit_cast(typename Mma<T>::x8, (v & keep) ^ flip);
+    }
+    a.m[i] = NO_SCORE;
+    a.sum[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < COLS / 16; ++c) hd.o[i][c] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < COLS / 32; ++c) a.o[i][c] = v16f{};
   }
-  // Token of the lane in tile t; entries are loaded three tiles ahead, pages two, rows one.
+  if (threadIdx.x < 64) lds.m[threadIdx.x] = NO_SCORE;
+  if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
+  // Tile t's token of the lane; entries are loaded first, pages from them, rows from those.
   const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
-  const auto token = [&](int t) { return w.t0 + t * TILE + wv * 16 + j; };
+  const auto token = [&](int t) { return w.t0 + t * TILE + (l & 31); };
   const auto entry = [&](int t) { return token(t) < w.t1 ? w.src.entry(token(t)) : -1; };
   const auto position = [&](int t, int32_t e) -> int64_t { return token(t) < w.t1 ? w.src.position(token(t), e) : -1; };
-  int64_t pos = position(0, entry(0)), pos1 = position(1, entry(1));
-  int32_t row = w.src.row(pos, w.src.page(pos));
-  int32_t page1 = w.src.page(pos1), e2 = entry(2);
-  uint32_t real = static_cast<uint32_t>(__ballot(row >= 0)) & 0xFFFFu;
-  if (n > 0) fetch(x, row, lds, wv);
-  for (int t = 0; t < n; ++t) {
-    uint8_t *cur = lds + (t & 1) * STAGE, *nxt = lds + ((t + 1) & 1) * STAGE;
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(WAIT_VM0);
-    meet();                                                // tile t is there for all; tile t - 1 has been used
-    uint32_t real1 = 0;
-    if (t + 1 < n) {
-      row = w.src.row(pos1, page1);
-      real1 = static_cast<uint32_t>(__ballot(row >= 0)) & 0xFFFFu;
-      fetch(x, row, nxt, wv);
-      pos1 = position(t + 2, e2);
-      page1 = w.src.page(pos1);
-      e2 = entry(t + 3);
-    }
-    hd.tile(cur, lds + Lds<MT>::P, reinterpret_cast<float *>(lds + Lds<MT>::MX), x.a.scale2, real, wv);
-    real = real1;
+  const auto there = [&](int32_t row) { return static_cast<uint32_t>(__ballot(row >= 0)); };
+  uint32_t real[3];                                        // of tiles t + 1, t + 2, t + 3
+  int64_t pos[4];
+  int32_t page[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) pos[t] = position(t, entry(t));
+  int32_t e_next = entry(4);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) page[t] = w.src.page(pos[t]);
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const int32_t row = w.src.row(pos[t], page[t]);
+    real[t] = there(row);
+    if (t < n) fetch(x, row, lds.stage[t], wv);
   }
-  // The sums of a head: four lane groups, four waves.
-  float *mx = reinterpret_cast<float *>(lds + Lds<MT>::MX);
+  int64_t pos1 = pos[3];
+  int32_t page1 = page[3];
+  // Tile t of this wave's loads is in LDS; `later` tiles have been asked for after it.
+  const auto arrived = [&](int later) {
+    asm volatile("" ::: "memory");
+    if (later >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * LOADS));
+    else if (later == 1) __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));
+    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    meet();
+  };
+  // Scores and weights of tile t, which is there.
+  const auto score = [&](int t, uint32_t have) {
+    a.scores(lds.stage[t % STAGES], scale2, have);
+    a.weigh(lds.p[t & 1]);
+    if (a.far_above() && l == 0) lds.raise[t & 1] = t + 1;
+  };
+  if (n > 0) {
+    arrived(min(n - 1, 2));
+    score(0, real[0]);
+    for (int t = 0; t < n; ++t) {
+      // Tile t + 1 and the weights of tile t are there for all; every wave is done with tile t - 1.
+      arrived(t + 2 < n ? 1 : 0);
+      if (lds.raise[t & 1] == t + 1) a.raise(lds, lds.p[t & 1]);
+#pragma unroll
+      for (int i = 0; i < QT; ++i) a.sum[i] += a.tile_sum[i];
+      const uint32_t have = real[1];
+      if (t + 3 < n) {
+        const int32_t row = w.src.row(pos1, page1);
+        real[1] = real[2];
+        real[2] = there(row);
+        pos1 = position(t + 4, e_next);
+        page1 = w.src.page(pos1);
+        e_next = entry(t + 5);
+        fetch(x, row, lds.stage[(t + 3) % STAGES], wv);
+      } else {
+        real[1] = real[2];
+      }
+      if (t + 1 < n) score(t + 1, have);
+      a.add(lds.stage[t % STAGES], lds.p[t & 1]);
+    }
+  }
+  a.pin();
+  // The sums of a query: four lane groups, two waves.
   meet();
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    float s = hd.sum[i];
+  for (int i = 0; i < QT; ++i) {
+    float s = a.sum[i];
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
-    if (g == 0) mx[wv * MT * 16 + i * 16 + j] = s;
+    if (g == 0) lds.top[a.th][a.qb + 16 * i + j] = s;
   }
   meet();
+  const int h = l >> 5;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t qi = w.q0 + i * 16 + j;
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) s += mx[v * MT * 16 + i * 16 + j];
-    if (qi >= w.q1) continue;
-    const int col = wv * COLS + 4 * g;
+  for (int i = 0; i < QT; ++i) {
+    const int at = 32 * i + (l & 31);
+    const int64_t qi = w.q0 + at;
+    const float sum = lds.top[0][at] + lds.top[1][at], m = lds.m[at];
     if (w.part < 0) {
-      const int64_t r = qi / x.a.n_heads;
-      const float inv = s == 0.f ? 0.f : 1.f / s;
-      T *out = static_cast<T *>(x.out) + r * x.o_row + (qi - r * x.a.n_heads) * x.o_head + col;
+      const int64_t r = min(qi, w.q1 - 1) / x.a.n_heads;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T *out = static_cast<T *>(x.out) + r * x.o_row + (min(qi, w.q1 - 1) - r * x.a.n_heads) * x.o_head + wv * COLS + 8 * h;
+      // Halves of the wave exchange: a lane gets 8 consecutive columns, the lower half the first 8 of 16.
 #pragma unroll
-      for (int c = 0; c < COLS / 16; ++c) *reinterpret_cast<u32x2 *>(out + 16 * c) = pack4<T>(hd.o[i][c] * inv);
-      if (x.lse && wv == 0 && g == 0) x.lse[qi] = s == 0.f ? -INFINITY : (hd.m[i] + log2_(s)) * LN2;
-    } else {
+      for (int c = 0; c < COLS / 32; ++c)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          u32x2 u[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int v = 8 * b + 4 * e;
+            u[e] = pack4<T>(v4f{a.o[i][c][v], a.o[i][c][v + 1], a.o[i][c][v + 2], a.o[i][c][v + 3]} * inv);
+          }
+          const auto lo = __builtin_amdgcn_permlane32_swap(u[0][0], u[1][0], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(u[0][1], u[1][1], false, false);
+          if (qi < w.q1) *reinterpret_cast<u32x4 *>(out + 32 * c + 16 * b) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+      if (x.lse && wv == 0 && h == 0 && qi < w.q1) x.lse[qi] = sum == 0.f ? -INFINITY : (m + log2_(sum)) * LN2;
+    } else if (qi < w.q1) {
       const int64_t p = qi * x.parts + w.part;
-      float *out = x.part + p * VALUES + col;
+      float *out = x.part + p * VALUES + wv * COLS + 4 * h;
 #pragma unroll
-      for (int c = 0; c < COLS / 16; ++c) *reinterpret_cast<v4f *>(out + 16 * c) = hd.o[i][c];
-      if (wv == 0 && g == 0) {
-        x.part_ml[2 * p] = hd.m[i];
-        x.part_ml[2 * p + 1] = s;
+      for (int c = 0; c < COLS / 32; ++c)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<v4f *>(out + 32 * c + 8 * b) = v4f{a.o[i][c][4 * b], a.o[i][c][4 * b + 1], a.o[i][c][4 * b + 2], a.o[i][c][4 * b + 3]};
+      if (wv == 0 && h == 0) {
+        x.part_ml[2 * p] = m;
+        x.part_ml[2 * p + 1] = sum;
       }
     }
   }
@@ -248,9 +351,9 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, uint8_t *__restrict__ lds)
 // The tokens that a query row lists (or, without a list, its own).  Workgroups go to the 8 XCDs in turn, each
 // with an L2 of its own: the head tiles of a chunk follow each other by 8, so that they share the one that the
 // chunk's rows are in.
-template <typename T, int MT>
+template <typename T, int QT>
 __global__ __launch_bounds__(WAVES * 64, 1) void rows_kernel(AttArgs x, uint32_t units, uint32_t head_tiles) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<MT>::SIZE];
+  __shared__ __attribute__((aligned(16))) Lds lds;
   const uint32_t eight = blockIdx.x / (8 * head_tiles), in = blockIdx.x - eight * 8 * head_tiles;
   const uint32_t u = eight * 8 + (in & 7), ht = in >> 3;
   if (u >= units) return;
@@ -264,18 +367,18 @@ __global__ __launch_bounds__(WAVES * 64, 1) void rows_kernel(AttArgs x, uint32_t
     w.t1 = static_cast<int32_t>(min<int64_t>(w.t1, max<int64_t>(w.src.limit, 0)));
     if (w.t0 >= w.t1 && x.parts > 0) return;               // join_kernel goes by the length too
   }
-  w.q0 = static_cast<int64_t>(r) * x.a.n_heads + ht * (16 * MT);
+  w.q0 = static_cast<int64_t>(r) * x.a.n_heads + ht * (32 * QT);
   w.q1 = static_cast<int64_t>(r + 1) * x.a.n_heads;
   w.part = x.parts > 0 ? x.first_part + c : -1;
-  attend<T, MT>(x, w, lds);
+  attend<T, QT>(x, w, lds);
 }
 
 ECHO_DEV int32_t clamp_row(int32_t r, int32_t n) { return r < 0 ? 0 : r > n ? n : r; }
 
 // The prefixes: tile `tile` of the groups' query tiles in order, chunk `c`.
-template <typename T, int MT>
+template <typename T, int QT>
 __global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32_t tiles) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<MT>::SIZE];
+  __shared__ __attribute__((aligned(16))) Lds lds;
   const int32_t c = blockIdx.x % x.n_chunks;
   uint32_t tile = blockIdx.x / x.n_chunks;
   int32_t gi = 0, r0 = 0, r1 = 0;
@@ -283,7 +386,7 @@ __global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32
     r0 = clamp_row(x.group_begin[gi], x.a.n_rows);
     r1 = clamp_row(x.group_begin[gi + 1], x.a.n_rows);
     if (r1 < r0) r1 = r0;
-    const uint32_t has = static_cast<uint32_t>((static_cast<int64_t>(r1 - r0) * x.a.n_heads + 16 * MT - 1) / (16 * MT));
+    const uint32_t has = static_cast<uint32_t>((static_cast<int64_t>(r1 - r0) * x.a.n_heads + 32 * QT - 1) / (32 * QT));
     if (tile < has) break;
     tile -= has;
   }
@@ -293,10 +396,10 @@ __global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32
   w.t0 = c * x.chunk;
   w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.chunk, x.a.n_tok), w.src.limit));
   if (w.t0 >= w.t1) return;
-  w.q0 = static_cast<int64_t>(r0) * x.a.n_heads + static_cast<int64_t>(tile) * (16 * MT);
+  w.q0 = static_cast<int64_t>(r0) * x.a.n_heads + static_cast<int64_t>(tile) * (32 * QT);
   w.q1 = static_cast<int64_t>(r1) * x.a.n_heads;
   w.part = c;
-  attend<T, MT>(x, w, lds);
+  attend<T, QT>(x, w, lds);
 }
 
 // ---------------------------------------------------------------- joining chunks
@@ -356,8 +459,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs x) {
 }
 
 // ---------------------------------------------------------------- host
-// Head tiles of 16, 32 or 64 queries: the smallest that holds `queries`.
-int head_tile(int64_t queries) { return queries <= 16 ? 1 : queries <= 32 ? 2 : 4; }
+// Groups of 32 queries in a workgroup.
+int head_tile(int64_t queries) { return queries <= 32 ? 1 : 2; }
 
 // Chunks of n_tok tokens for `tiles` query tiles, and their tokens: as many as give each CU one workgroup.
 constexpr int CUS = 256;
@@ -375,7 +478,7 @@ struct RowsPlan { int mt; int64_t head_tiles; int32_t chunk, n_chunks; };
 RowsPlan rows_plan(int32_t n_rows, int32_t n_heads, int64_t n_tok) {
   RowsPlan p;
   p.mt = head_tile(n_heads);
-  p.head_tiles = (n_heads + 16 * p.mt - 1) / (16 * p.mt);
+  p.head_tiles = (n_heads + 32 * p.mt - 1) / (32 * p.mt);
   p.chunk = chunk_of(n_rows * p.head_tiles, n_tok);
   p.n_chunks = std::max(1, chunks_of(n_tok, p.chunk));
   return p;
@@ -393,8 +496,8 @@ PrefixPlan prefix_plan(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_
   const int64_t queries = static_cast<int64_t>(n_rows) * n_heads;
   const int64_t groups = std::min(n_groups, n_rows);
   p.mt = head_tile(groups ? queries / groups : queries);
-  p.tiles = groups ? queries / (16 * p.mt) + groups : 0;   // at least what the groups' last, partly filled tiles take
-  p.chunk = chunk_of(std::max<int64_t>(1, queries / (16 * p.mt)), max_prefix);
+  p.tiles = groups ? queries / (32 * p.mt) + groups : 0;   // at least what the groups' last, partly filled tiles take
+  p.chunk = chunk_of(std::max<int64_t>(1, queries / (32 * p.mt)), max_prefix);
   p.prefix_parts = groups && max_prefix > 0 ? chunks_of(max_prefix, p.chunk) : 0;
   return p;
 }
@@ -405,8 +508,7 @@ int launch_rows(const AttArgs &x, const RowsPlan &p, hipStream_t st) {
   const uint32_t grid = (units + 7) / 8 * 8 * ht;
   switch (p.mt) {
     case 1: rows_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
-    case 2: rows_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
-    default: rows_kernel<T, 4><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
+    default: rows_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
   }
   return check_launch("attention");
 }
@@ -415,8 +517,7 @@ int launch_prefix(const AttArgs &x, const PrefixPlan &p, hipStream_t st) {
   const uint32_t tiles = static_cast<uint32_t>(p.tiles), grid = tiles * static_cast<uint32_t>(p.prefix_parts);
   switch (p.mt) {
     case 1: prefix_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
-    case 2: prefix_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
-    default: prefix_kernel<T, 4><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
+    default: prefix_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
   }
   return check_launch("prefix attention");
 }

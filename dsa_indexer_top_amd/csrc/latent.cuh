@@ -2,8 +2,9 @@
 // and where the tokens of a list, a block list or a paged request are.
 //
 // v_mfma_f32_16x16x32: lane l = 16 g + j supplies row j of the first operand and column j of the
-// second for eight products, and receives rows 4 g .. 4 g + 3 of column j of the result.  Which eight
-// of the 32 products a lane group takes does not matter as long as both operands agree.
+// second for eight products, and receives rows 4 g .. 4 g + 3 of column j of the result.
+// v_mfma_f32_32x32x16: lane l = 32 h + j likewise, and rows 8 b + 4 h + e of column j as element 4 b + e.
+// Which eight products a lane group takes does not matter as long as both operands agree.
 #pragma once
 
 #include "float_types.cuh"
@@ -17,6 +18,7 @@ constexpr float NO_SCORE = -3.0e38f;             // a running maximum before the
                                                  // differences of two of them are 0
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) void lds_void;
@@ -29,10 +31,12 @@ template <typename T> struct Mma;
 template <> struct Mma<bf16_t> {
   typedef bf16x8 x8;
   ECHO_DEV static v4f mul(x8 a, x8 b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+  ECHO_DEV static v16f mul(x8 a, x8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 };
 template <> struct Mma<fp16_t> {
   typedef fp16x8 x8;
   ECHO_DEV static v4f mul(x8 a, x8 b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+  ECHO_DEV static v16f mul(x8 a, x8 b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 };
 
 template <typename X8, typename P>
@@ -52,8 +56,9 @@ ECHO_DEV u32x2 pack4(const v4f &v) {
 ECHO_DEV float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 ECHO_DEV float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
-// s_waitcnt: every vector memory operation done; every LDS operation done.
-constexpr int WAIT_VM0 = 0x0F70, WAIT_LDS0 = 0xC07F;
+// s_waitcnt: at most n vector memory operations under way; every LDS operation done.
+constexpr int vmcnt(int n) { return (n & 15) | 0x0F70 | (n >> 4) << 14; }
+constexpr int WAIT_VM0 = vmcnt(0), WAIT_LDS0 = 0xC07F;
 
 // The workgroup's waves meet, their LDS operations done.  Loads under way stay under way, which
 // __syncthreads() would wait for.

@@ -483,6 +483,33 @@ static void op_mfma_16bit(const unsigned char *in, unsigned char *out, size_t, s
   }
 }
 
+// 32x32x16: lane l supplies row l%32 of A and column l%32 of B for K elements [8 (l/32), 8 (l/32) + 8) and
+// receives rows 8 (v/4) + 4 (l/32) + v%4 of column l%32 as element v.
+struct Mfma32In { unsigned char a[16], b[16]; v16f_emu c; };
+template <float (*VALUE)(const unsigned char *)>
+static void op_mfma_32(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
+  static float A[32][16], B[16][32];
+  for (int l = 0; l < 64; ++l) {
+    Mfma32In x;
+    memcpy(&x, in + l * SLOT, sizeof x);
+    for (int q = 0; q < 8; ++q) {
+      A[l % 32][8 * (l / 32) + q] = VALUE(x.a + 2 * q);
+      B[8 * (l / 32) + q][l % 32] = VALUE(x.b + 2 * q);
+    }
+  }
+  for (int l = 0; l < 64; ++l) {
+    Mfma32In x;
+    memcpy(&x, in + l * SLOT, sizeof x);
+    v16f_emu r;
+    for (int v = 0; v < 16; ++v) {
+      double acc = 0;
+      for (int k = 0; k < 16; ++k) acc += static_cast<double>(A[8 * (v / 4) + 4 * (l / 32) + v % 4][k]) * B[k][l % 32];
+      r[v] = static_cast<float>(acc + x.c[v]);
+    }
+    memcpy(out + l * SLOT, &r, 64);
+  }
+}
+
 // Of each 16 lanes' four 16-bit values: lane j gets value j % 4 of lanes j / 4, 4 + j / 4, 8 + j / 4 and 12 + j / 4.
 static void op_transpose(const unsigned char *in, unsigned char *out, size_t, size_t, const void *) {
   for (int l = 0; l < 64; ++l)
@@ -599,6 +626,18 @@ v4f_emu emu_amdgcn_mfma_f32_16x16x32_f16(v8h_emu a, v8h_emu b, v4f_emu c, int, i
   wave_op(&x, sizeof x, &r, 16, op_mfma_16bit<fp16_value>, nullptr);
   return r;
 }
+template <typename V>
+static v16f_emu mfma_32(const V &a, const V &b, const v16f_emu &c, void (*op)(const unsigned char *, unsigned char *, size_t, size_t, const void *)) {
+  Mfma32In x;
+  memcpy(x.a, &a, 16);
+  memcpy(x.b, &b, 16);
+  x.c = c;
+  v16f_emu r;
+  wave_op(&x, sizeof x, &r, 64, op, nullptr);
+  return r;
+}
+v16f_emu emu_amdgcn_mfma_f32_32x32x16_bf16(v8bf_emu a, v8bf_emu b, v16f_emu c, int, int, int) { return mfma_32(a, b, c, op_mfma_32<bf16_value>); }
+v16f_emu emu_amdgcn_mfma_f32_32x32x16_f16(v8h_emu a, v8h_emu b, v16f_emu c, int, int, int) { return mfma_32(a, b, c, op_mfma_32<fp16_value>); }
 v4s_emu emu_amdgcn_ds_read_tr16_b64_v4i16(const v4s_emu *p) {
   const v4s_emu mine = *p;                                // read here: under the sanitizers
   v4s_emu r;

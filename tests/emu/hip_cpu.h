@@ -147,6 +147,9 @@ v2bf_emu emu_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned src, float scale, bool hig
 v4f_emu emu_amdgcn_mfma_f32_16x16x32_bf16(v8bf_emu a, v8bf_emu b, v4f_emu c, int, int, int);
 typedef _Float16 v8h_emu __attribute__((ext_vector_type(8)));
 v4f_emu emu_amdgcn_mfma_f32_16x16x32_f16(v8h_emu a, v8h_emu b, v4f_emu c, int, int, int);
+typedef float v16f_emu __attribute__((ext_vector_type(16)));
+v16f_emu emu_amdgcn_mfma_f32_32x32x16_bf16(v8bf_emu a, v8bf_emu b, v16f_emu c, int, int, int);
+v16f_emu emu_amdgcn_mfma_f32_32x32x16_f16(v8h_emu a, v8h_emu b, v16f_emu c, int, int, int);
 // transposing LDS read: of 16 lanes' 8 bytes each, lane j gets element j % 4 of lanes j / 4, 4 + j / 4, ..
 typedef short v4s_emu __attribute__((ext_vector_type(4)));
 v4s_emu emu_amdgcn_ds_read_tr16_b64_v4i16(const v4s_emu *p);
