@@ -30,18 +30,22 @@ namespace echo {
 constexpr int WAVES = 4, TILE = 32, STAGES = 4;            // tokens of a tile, tiles in LDS
 constexpr int KSTEPS = LATENT / 32, COLS = VALUES / WAVES; // products of a score, columns of a wave
 constexpr int LOADS = TILE / WAVES + 1;                    // a wave's loads of a tile
+constexpr int BATCH = 1536;                                // tokens whose rows are looked up at once
 constexpr float SLACK = 8.f;
 
 // Tokens whose list entry, position or page leads nowhere read this row instead of the cache, so that
 // nothing of the cache's contents can get into a sum through a weight of 0.
 __device__ const uint32_t g_zero_row[LATENT / 2] = {};
 
-// A tile in LDS: the rows' first 512 values, 1024 bytes a row, then their last 64, 128 bytes a row.
-// Pieces of 16 bytes are exchanged within a row so that the reads of 16 rows at one piece (scores) and of
-// four rows at 64 bytes (sums) touch every bank once.
-constexpr int ROPE_AT = TILE * 1024, STAGE = TILE * LATENT * 2;
-ECHO_DEV constexpr int swap_v(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+// A tile in LDS: the rows' first 512 values, 1024 bytes a row and then 64 of weights, every four rows 16 bytes
+// more apart; then the rows' last 64 values, 128 bytes a row.  So the reads of 16 rows at one place (scores,
+// weights) and of four rows at 64 bytes (sums) touch every bank once, and every read of a lane is one address and
+// a constant.  In the last 64 values the pieces of 16 bytes are exchanged within a row instead.
+constexpr int ROW_STEP = 1024 + 64, ROPE_AT = TILE * ROW_STEP + TILE / 4 * 16, STAGE = ROPE_AT + TILE * 128;
+ECHO_DEV constexpr int row_at(int row) { return row * ROW_STEP + (row >> 2) * 16; }
 ECHO_DEV constexpr int swap_r(int row) { return (row >> 1) & 7; }
+// Weights of query `at` for tile t (by t % 2): behind row at % 32 of stage 2 (t % 2) + at / 32, 32 tokens.
+ECHO_DEV constexpr int weights_at(int t, int at) { return (2 * (t & 1) + (at >> 5)) * STAGE + row_at(at & 31) + 1024; }
 
 struct AttArgs {
   LatentArgs a;
@@ -64,29 +68,67 @@ struct Work {
 };
 
 struct Lds {
-  uint8_t stage[STAGES][STAGE];
-  uint8_t p[2][64 * TILE * 2];   // weights by query: 4 pieces of 8 tokens
+  uint8_t stage[STAGES * STAGE];
   float m[64], top[2][64];       // maxima; a tile's, or at the end the sums
   int32_t raise[2];              // t + 1: tile t (by t % 2) has a score far above its maximum
+  int32_t rows[BATCH];           // cache rows of a batch of tokens, -1: none
 };
 static_assert(sizeof(Lds) <= 160 * 1024, "a workgroup's LDS");
 
-// The wave's 8 rows of a tile to LDS; lane i holds the cache row of the tile's row i.
-ECHO_DEV void fetch(const AttArgs &x, int32_t row, uint8_t *__restrict__ stage, int wv) {
-  const int l = lane_id();
-  const uint8_t *kv = reinterpret_cast<const uint8_t *>(x.a.kv), *zero = reinterpret_cast<const uint8_t *>(g_zero_row);
-  const int64_t stride = x.a.kv_stride * 2;
+// Cache rows of the chunk's tokens from `first` on, up to a batch of them.  Entries and pages are loaded
+// for a batch at once: loaded tile by tile, their waits held up the rows on their way (the same counter).
+ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) {
+  const int32_t t0 = w.t0 + first, count = min(w.t1 - t0, BATCH);
+  constexpr int PER = BATCH / (WAVES * 64);
+  const int tid = threadIdx.x;
+  int32_t e[PER], page[PER];
+  int64_t pos[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) e[i] = 0;
+  if (w.src.list) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * WAVES * 64 < count) e[i] = w.src.list[(t0 + min(i * WAVES * 64 + tid, count - 1)) >> w.src.shift];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) pos[i] = i * WAVES * 64 + tid < count ? w.src.position(t0 + i * WAVES * 64 + tid, e[i]) : -1;
+  if (w.src.table && w.src.max_pages > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t p = pos[i] >> w.src.pshift;            // -1: none
+      page[i] = w.src.table[p < 0 || p >= w.src.max_pages ? 0 : p];
+      if (p >= w.src.max_pages) page[i] = -1;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) page[i] = -1;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (i * WAVES * 64 < count) rows[i * WAVES * 64 + tid] = w.src.row(pos[i], page[i]);
+}
+
+// The wave's 8 rows of a tile to LDS, the tile's cache rows at `rows`.  Returns which of its 32 tokens there are.
+ECHO_DEV uint32_t fetch(const AttArgs &x, const int32_t *__restrict__ rows, uint8_t *__restrict__ stage, int wv) {
+  const int l = lane_id(), r0 = wv * (TILE / WAVES);
+  const uint32_t stride = static_cast<uint32_t>(x.a.kv_stride * 2);
+  const auto address = [&](int32_t row) {
+    const uint64_t at = reinterpret_cast<uint64_t>(x.a.kv) + static_cast<uint64_t>(static_cast<uint32_t>(row)) * stride;
+    return row < 0 ? reinterpret_cast<uint64_t>(g_zero_row) : at;
+  };
+  const int32_t row = rows[l & 31], rope_row = rows[r0 + (l >> 3)];
+  const uint64_t at = address(row);
+  const int lo = static_cast<int>(at), hi = static_cast<int>(at >> 32);
+  uint8_t *to = stage + row_at(r0);                        // r0 is a multiple of 4
 #pragma unroll
   for (int i = 0; i < TILE / WAVES; ++i) {
-    const int at = wv * (TILE / WAVES) + i;
-    const int32_t r = __builtin_amdgcn_readlane(row, at);
-    const uint8_t *src = r < 0 ? zero : kv + r * stride;
-    __builtin_amdgcn_global_load_lds((glb_void *)(src + ((l ^ swap_v(at)) << 4)), (lds_void *)(stage + at * 1024), 16, 0, 0);
+    const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r0 + i)), b = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i));
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(static_cast<uint64_t>(b) << 32 | a);
+    __builtin_amdgcn_global_load_lds((glb_void *)(src + static_cast<uint32_t>(l * 16)), (lds_void *)(to + row_at(i)), 16, 0, 0);
   }
-  const int at = wv * (TILE / WAVES) + (l >> 3);
-  const int32_t r = __shfl(row, at, 64);
-  const uint8_t *src = r < 0 ? zero : kv + r * stride;
-  __builtin_amdgcn_global_load_lds((glb_void *)(src + 1024 + (((l & 7) ^ swap_r(at)) << 4)), (lds_void *)(stage + ROPE_AT + wv * 1024), 16, 0, 0);
+  const uint8_t *src = reinterpret_cast<const uint8_t *>(address(rope_row)) + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4);
+  __builtin_amdgcn_global_load_lds((glb_void *)src, (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
+  return static_cast<uint32_t>(__ballot(row >= 0));
 }
 
 template <typename T, int QT>
@@ -98,20 +140,19 @@ struct Waves {
   v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
   int wv, qb, th;                // qb: the wave's first query for scores
 
-  // Scores of a tile and their weights; `real`: the tile's tokens that there are.
-  ECHO_DEV void scores(const uint8_t *__restrict__ stage, float scale2, uint32_t real) {
+  // Scores of a tile's tokens: product k of the wave's 16 rows.
+  struct Rows {
+    const uint8_t *v, *r;
+    int g, swap;
+    ECHO_DEV x8 read(int k) const { return k < 16 ? read16<x8>(v + 16 * k) : read16<x8>(r + (((4 * (k - 16) + g) ^ swap) << 4)); }
+  };
+  ECHO_DEV Rows rows_of(const uint8_t *__restrict__ stage) const {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-    const uint8_t *vrow = stage + (th * 16 + j) * 1024, *rrow = stage + ROPE_AT + (th * 16 + j) * 128;
-#pragma unroll
-    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) {
-      const x8 row = k < 16 ? read16<x8>(vrow + (((k + 16 * g) ^ swap_v(j)) << 4))
-                            : read16<x8>(rrow + (((4 * (k - 16) + g) ^ swap_r(j)) << 4));
-#pragma unroll
-      for (int i = 0; i < QT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
-    }
-    const uint32_t mine = real >> (16 * th + 4 * g);
+    return Rows{stage + row_at(th * 16 + j) + 256 * g, stage + ROPE_AT + (th * 16 + j) * 128, g, swap_r(j)};
+  }
+  // Base 2, and -infinity where there is no token; `real`: the tile's tokens that there are.
+  ECHO_DEV void finish(float scale2, uint32_t real) {
+    const uint32_t mine = real >> (16 * th + 4 * (lane_id() >> 4));
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float none = mine >> v & 1 ? 0.f : -INFINITY;
@@ -119,25 +160,36 @@ struct Waves {
       for (int i = 0; i < QT; ++i) s[i][v] = fmaf(s[i][v], scale2, none);
     }
   }
-  ECHO_DEV void weigh(uint8_t *__restrict__ p) {
-    const int l = lane_id(), j = l & 15, g = l >> 4;
+  ECHO_DEV void scores(const uint8_t *__restrict__ stage, float scale2, uint32_t real) {
+    const Rows r = rows_of(stage);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k) {
+      const x8 row = r.read(k);
+#pragma unroll
+      for (int i = 0; i < QT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
+    }
+    finish(scale2, real);
+  }
+  ECHO_DEV void put(uint8_t *__restrict__ lds, int t, int i, const v4f &w) {
+    const int l = lane_id(), j = l & 15, g = l >> 4, at = qb + 16 * i + j;
+    tile_sum[i] = (w[0] + w[1]) + (w[2] + w[3]);
+    *reinterpret_cast<u32x2 *>(lds + weights_at(t, at) + 32 * th + 8 * g) = pack4<T>(w);
+  }
+  ECHO_DEV void weigh(uint8_t *__restrict__ lds, int t) {
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
       v4f w;
 #pragma unroll
       for (int v = 0; v < 4; ++v) w[v] = exp2_(s[i][v] - m[i]);
-      tile_sum[i] = (w[0] + w[1]) + (w[2] + w[3]);
-      const int at = qb + 16 * i + j;
-      *reinterpret_cast<u32x2 *>(p + at * 64 + (((2 * th + (g >> 1)) ^ ((at >> 2) & 3)) << 4) + 8 * (g & 1)) = pack4<T>(w);
+      put(lds, t, i, w);
     }
   }
-  // Keeps the sums where the matrix core adds them up: an empty statement that takes and gives accumulation registers.
-  ECHO_DEV void pin() {
-#pragma unroll
-    for (int i = 0; i < QT; ++i)
-#pragma unroll
-      for (int c = 0; c < COLS / 32; ++c) asm volatile("" : "+a"(o[i][c]));
-  }
+  // An empty statement that takes and gives accumulation registers: between two of them the compiler copies one
+  // group of sums to where it can be multiplied, and holds them all where the matrix core adds them up otherwise.
+  ECHO_DEV static void pin(v16f &v) { asm volatile("" : "+a"(v)); }
+  ECHO_DEV static void pin(v4f &v) { asm volatile("" : "+a"(v)); }
   ECHO_DEV static float top_of(const v4f &s) { return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])); }
   ECHO_DEV bool far_above() const {
     bool f = false;
@@ -146,7 +198,7 @@ struct Waves {
     return __ballot(f) != 0;
   }
   // Every wave: maxima up to those of the tile, sums and weights on the new scale.
-  ECHO_DEV void raise(Lds &lds, uint8_t *__restrict__ p) {
+  ECHO_DEV void raise(Lds &lds, int t) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
@@ -156,17 +208,18 @@ struct Waves {
       if (g == 0) lds.top[th][qb + 16 * i + j] = top;
     }
     meet();
-    pin();
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
       const int at = 32 * i + (l & 31);
       const float was = lds.m[at], less = exp2_(was - fmaxf(was, fmaxf(lds.top[0][at], lds.top[1][at])));
 #pragma unroll
-      for (int c = 0; c < COLS / 32; ++c)
+      for (int c = 0; c < COLS / 32; ++c) {
+        pin(o[i][c]);
 #pragma unroll
         for (int v = 0; v < 16; ++v) o[i][c][v] *= less;
+        pin(o[i][c]);
+      }
     }
-    pin();
     float to[QT];
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
@@ -179,31 +232,87 @@ struct Waves {
     if (th == 0 && g == 0)
 #pragma unroll
       for (int i = 0; i < QT; ++i) lds.m[qb + 16 * i + j] = to[i];
-    weigh(p);
+    weigh(lds.stage, t);
     meet();
   }
-  // Product k takes tokens 16 k + 8 h .. + 7.
-  ECHO_DEV void add(const uint8_t *__restrict__ stage, const uint8_t *__restrict__ p) {
+  // The sum's operands: weights of query 32 i + j and columns 32 c .. of the wave's, tokens 16 k + 8 h .. + 7.
+  struct Cols {
+    const uint8_t *p, *v;
+    ECHO_DEV x8 weights(int i, int k) const { return read16<x8>(p + i * STAGE + 32 * k); }
+    ECHO_DEV x8 read(int c, int k) const {
+      struct { v4s lo, hi; } e;
+      e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k) + 64 * c));
+      e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k + 4) + 64 * c));
+      return __builtin_bit_cast(x8, e);
+    }
+  };
+  ECHO_DEV Cols cols_of(const uint8_t *__restrict__ lds, int t) const {
     const int l = lane_id(), j = l & 31, h = l >> 5;
-    const int r = 8 * h + ((l & 15) >> 2);
+    return Cols{lds + weights_at(t, j) + 16 * h,
+                lds + t % STAGES * STAGE + row_at(8 * h) + ((l & 15) >> 2) * ROW_STEP + wv * (2 * COLS) + 32 * ((l >> 4) & 1) + 8 * (l & 3)};
+  }
+  ECHO_DEV void add(const uint8_t *__restrict__ lds, int t) {
+    const Cols x = cols_of(lds, t);
     x8 w[QT][2];
 #pragma unroll
     for (int i = 0; i < QT; ++i)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) w[i][k] = read16<x8>(p + (32 * i + j) * 64 + (((2 * k + h) ^ ((j >> 2) & 3)) << 4));
+      for (int k = 0; k < 2; ++k) w[i][k] = x.weights(i, k);
 #pragma unroll
     for (int c = 0; c < COLS / 32; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        struct { v4s lo, hi; } e;
-        const int piece = wv * (COLS / 8) + 4 * c + 2 * ((l >> 4) & 1) + ((l >> 1) & 1);
-        const uint8_t *at = stage + (16 * k + r) * 1024 + 8 * (l & 1);
-        e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + ((piece ^ swap_v(r)) << 4)));
-        e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(at + 4 * 1024 + ((piece ^ swap_v(r + 4)) << 4)));
-        const x8 col = __builtin_bit_cast(x8, e);
+        const x8 col = x.read(c, k);
 #pragma unroll
         for (int i = 0; i < QT; ++i) o[i][c] = Mma<T>::mul(col, w[i][k], o[i][c]);
       }
+  }
+  // Scores and weights of tile t + 1 and the sum over tile t.  The order of the reads and products is this one: left to
+  // itself the compiler reads each operand right before its product, and the matrix core waits for LDS.  An
+  // operand is read AHEAD products before its use, and the exponentials stand between the products of the sum.
+  ECHO_DEV void step(uint8_t *__restrict__ lds, int t, float scale2, uint32_t real) {
+    constexpr int AHEAD = 6, STEPS = COLS / 16, AHEAD_V = 3;
+    const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE);
+    const Cols x = cols_of(lds, t);
+    x8 row[AHEAD], col[AHEAD_V], w[QT][2];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        pin(s[i]);
+        s[i] = Mma<T>::mul(row[k % AHEAD], q[i][k], s[i]);
+      }
+      pin(s[0]);
+      if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
+      else if (k + AHEAD - KSTEPS < AHEAD_V) col[k + AHEAD - KSTEPS] = x.read((k + AHEAD - KSTEPS) >> 1, (k + AHEAD - KSTEPS) & 1);
+      else if (k == KSTEPS - 2 || k == KSTEPS - 1) {
+#pragma unroll
+        for (int i = 0; i < QT; ++i) w[i][k - (KSTEPS - 2)] = x.weights(i, k - (KSTEPS - 2));
+      }
+    }
+    float e[QT * 4];
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        pin(o[i][u >> 1]);
+        o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD_V], w[i][u & 1], o[i][u >> 1]);
+      }
+      pin(o[0][u >> 1]);
+      if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = x.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
+      if (u == 1) finish(scale2, real);
+      if (u >= 2) {
+#pragma unroll
+        for (int n = 0; n < 4 * QT; ++n)
+          if (n % (STEPS - 3) == u - 2) e[n] = exp2_(s[n >> 2][n & 3] - m[n >> 2]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < QT; ++i) put(lds, t + 1, i, v4f{e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]});
   }
 };
 
@@ -234,29 +343,17 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   }
   if (threadIdx.x < 64) lds.m[threadIdx.x] = NO_SCORE;
   if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
-  // Tile t's token of the lane; entries are loaded first, pages from them, rows from those.
   const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
-  const auto token = [&](int t) { return w.t0 + t * TILE + (l & 31); };
-  const auto entry = [&](int t) { return token(t) < w.t1 ? w.src.entry(token(t)) : -1; };
-  const auto position = [&](int t, int32_t e) -> int64_t { return token(t) < w.t1 ? w.src.position(token(t), e) : -1; };
-  const auto there = [&](int32_t row) { return static_cast<uint32_t>(__ballot(row >= 0)); };
+  constexpr int TILES = BATCH / TILE;
   uint32_t real[3];                                        // of tiles t + 1, t + 2, t + 3
-  int64_t pos[4];
-  int32_t page[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) pos[t] = position(t, entry(t));
-  int32_t e_next = entry(4);
-#pragma unroll
-  for (int t = 0; t < 4; ++t) page[t] = w.src.page(pos[t]);
-#pragma unroll
-  for (int t = 0; t < 3; ++t) {
-    const int32_t row = w.src.row(pos[t], page[t]);
-    real[t] = there(row);
-    if (t < n) fetch(x, row, lds.stage[t], wv);
+  if (n > 0) {
+    look_up(w, 0, lds.rows);
+    meet();
   }
-  int64_t pos1 = pos[3];
-  int32_t page1 = page[3];
-  // Tile t of this wave's loads is in LDS; `later` tiles have been asked for after it.
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    if (t < n) real[t] = fetch(x, lds.rows + t * TILE, lds.stage + t * STAGE, wv);
+  // The tiles but the `later` youngest of this wave's loads are in LDS.
   const auto arrived = [&](int later) {
     asm volatile("" ::: "memory");
     if (later >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * LOADS));
@@ -264,38 +361,41 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
     else __builtin_amdgcn_s_waitcnt(vmcnt(0));
     meet();
   };
-  // Scores and weights of tile t, which is there.
-  const auto score = [&](int t, uint32_t have) {
-    a.scores(lds.stage[t % STAGES], scale2, have);
-    a.weigh(lds.p[t & 1]);
+  const auto tell = [&](int t) {
     if (a.far_above() && l == 0) lds.raise[t & 1] = t + 1;
   };
   if (n > 0) {
     arrived(min(n - 1, 2));
-    score(0, real[0]);
-    for (int t = 0; t < n; ++t) {
-      // Tile t + 1 and the weights of tile t are there for all; every wave is done with tile t - 1.
+    a.scores(lds.stage, scale2, real[0]);
+    a.weigh(lds.stage, 0);
+    tell(0);
+    // Tile t + 1 and the weights of tile t are there for all; every wave is done with tile t - 1.
+    const auto begin = [&](int t) {
       arrived(t + 2 < n ? 1 : 0);
-      if (lds.raise[t & 1] == t + 1) a.raise(lds, lds.p[t & 1]);
+      const int32_t far = lds.raise[t & 1];
+      if (t + 3 < n) {
+        const int in = (t + 3) % TILES;
+        if (in == 0) {                                     // every wave has taken the last batch's rows
+          look_up(w, (t + 3) * TILE, lds.rows);
+          meet();
+        }
+        real[2] = fetch(x, lds.rows + in * TILE, lds.stage + (t + 3) % STAGES * STAGE, wv);
+      }
+      if (far == t + 1) a.raise(lds, t);
 #pragma unroll
       for (int i = 0; i < QT; ++i) a.sum[i] += a.tile_sum[i];
+    };
+    int t = 0;
+    for (; t + 1 < n; ++t) {
       const uint32_t have = real[1];
-      if (t + 3 < n) {
-        const int32_t row = w.src.row(pos1, page1);
-        real[1] = real[2];
-        real[2] = there(row);
-        pos1 = position(t + 4, e_next);
-        page1 = w.src.page(pos1);
-        e_next = entry(t + 5);
-        fetch(x, row, lds.stage[(t + 3) % STAGES], wv);
-      } else {
-        real[1] = real[2];
-      }
-      if (t + 1 < n) score(t + 1, have);
-      a.add(lds.stage[t % STAGES], lds.p[t & 1]);
+      real[1] = real[2];
+      begin(t);
+      a.step(lds.stage, t, scale2, have);
+      tell(t + 1);
     }
+    begin(t);
+    a.add(lds.stage, t);
   }
-  a.pin();
   // The sums of a query: four lane groups, two waves.
   meet();
 #pragma unroll
@@ -318,7 +418,8 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
       T *out = static_cast<T *>(x.out) + r * x.o_row + (min(qi, w.q1 - 1) - r * x.a.n_heads) * x.o_head + wv * COLS + 8 * h;
       // Halves of the wave exchange: a lane gets 8 consecutive columns, the lower half the first 8 of 16.
 #pragma unroll
-      for (int c = 0; c < COLS / 32; ++c)
+      for (int c = 0; c < COLS / 32; ++c) {
+        a.pin(a.o[i][c]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           u32x2 u[2];
@@ -331,15 +432,18 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
           const auto hi = __builtin_amdgcn_permlane32_swap(u[0][1], u[1][1], false, false);
           if (qi < w.q1) *reinterpret_cast<u32x4 *>(out + 32 * c + 16 * b) = u32x4{lo[0], hi[0], lo[1], hi[1]};
         }
+      }
       if (x.lse && wv == 0 && h == 0 && qi < w.q1) x.lse[qi] = sum == 0.f ? -INFINITY : (m + log2_(sum)) * LN2;
     } else if (qi < w.q1) {
       const int64_t p = qi * x.parts + w.part;
       float *out = x.part + p * VALUES + wv * COLS + 4 * h;
 #pragma unroll
-      for (int c = 0; c < COLS / 32; ++c)
+      for (int c = 0; c < COLS / 32; ++c) {
+        a.pin(a.o[i][c]);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
           *reinterpret_cast<v4f *>(out + 32 * c + 8 * b) = v4f{a.o[i][c][4 * b], a.o[i][c][4 * b + 1], a.o[i][c][4 * b + 2], a.o[i][c][4 * b + 3]};
+      }
       if (wv == 0 && h == 0) {
         x.part_ml[2 * p] = m;
         x.part_ml[2 * p + 1] = sum;
@@ -540,6 +644,7 @@ int check_cache(const char *fn, int32_t n_rows, int32_t n_heads, int32_t type, f
   if (n_rows == 0 || n_heads == 0) return ECHO_OK;
   if (!q || (n_kv && !kv)) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
   if (q_row < 0 || q_head < 0 || kv_stride < 0 || (n_kv > 1 && kv_stride < LATENT)) return fail(ECHO_EINVAL, "%s: a stride below 0 or below the row", fn);
+  if (kv_stride > 1 << 30) return fail(ECHO_EUNSUPPORTED, "%s: rows of kv more than 2^30 elements apart", fn);
   if (!aligned(q, 16) || !aligned(kv, 16) || q_row % 8 || q_head % 8 || (n_kv > 1 && kv_stride % 8))
     return fail(ECHO_EUNSUPPORTED, "%s: q, kv or their strides are not multiples of 16 bytes", fn);
   return ECHO_OK;
