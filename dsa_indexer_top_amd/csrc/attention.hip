@@ -33,10 +33,6 @@ constexpr int LOADS = TILE / WAVES + 1;                    // a wave's loads of 
 constexpr int BATCH = 1536;                                // tokens whose rows are looked up at once
 constexpr float SLACK = 8.f;
 
-// Tokens whose list entry, position or page leads nowhere read this row instead of the cache, so that
-// nothing of the cache's contents can get into a sum through a weight of 0.
-__device__ const uint32_t g_zero_row[LATENT / 2] = {};
-
 // A tile in LDS: the rows' first 512 values, 1024 bytes a row and then 64 of weights, every four rows 16 bytes
 // more apart; then the rows' last 64 values, 128 bytes a row.  So the reads of 16 rows at one place (scores,
 // weights) and of four rows at 64 bytes (sums) touch every bank once, and every read of a lane is one address and
@@ -108,34 +104,82 @@ ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) 
     if (i * WAVES * 64 < count) rows[i * WAVES * 64 + tid] = w.src.row(pos[i], page[i]);
 }
 
-// The wave's 8 rows of a tile to LDS, the tile's cache rows at `rows`.  Returns which of its 32 tokens there are.
-ECHO_DEV uint32_t fetch(const AttArgs &x, const int32_t *__restrict__ rows, uint8_t *__restrict__ stage, int wv) {
-  const int l = lane_id(), r0 = wv * (TILE / WAVES);
-  const uint32_t stride = static_cast<uint32_t>(x.a.kv_stride * 2);
-  const auto address = [&](int32_t row) {
-    const uint64_t at = reinterpret_cast<uint64_t>(x.a.kv) + static_cast<uint64_t>(static_cast<uint32_t>(row)) * stride;
-    return row < 0 ? reinterpret_cast<uint64_t>(g_zero_row) : at;
-  };
-  const int32_t row = rows[l & 31], rope_row = rows[r0 + (l >> 3)];
-  const uint64_t at = address(row);
-  const int lo = static_cast<int>(at), hi = static_cast<int>(at >> 32);
-  uint8_t *to = stage + row_at(r0);                        // r0 is a multiple of 4
+// 8 rows on their way to LDS, 1024 bytes and then the last 128 bytes of each; lane i (and every 8th after it) has the
+// address of row i.  For queries.
+ECHO_DEV void load_rows(uint64_t at, uint8_t *__restrict__ stage, int r0) {
+  const int l = lane_id(), lo = static_cast<int>(at), hi = static_cast<int>(at >> 32);
 #pragma unroll
   for (int i = 0; i < TILE / WAVES; ++i) {
-    const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r0 + i)), b = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i));
+    const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i)), b = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i));
     const uint8_t *src = reinterpret_cast<const uint8_t *>(static_cast<uint64_t>(b) << 32 | a);
-    __builtin_amdgcn_global_load_lds((glb_void *)(src + static_cast<uint32_t>(l * 16)), (lds_void *)(to + row_at(i)), 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((glb_void *)(src + l * 16), (lds_void *)(stage + row_at(r0) + row_at(i)), 16, 0, 0);
   }
-  const uint8_t *src = reinterpret_cast<const uint8_t *>(address(rope_row)) + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4);
-  __builtin_amdgcn_global_load_lds((glb_void *)src, (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
-  return static_cast<uint32_t>(__ballot(row >= 0));
+  const uint64_t rope = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, l >> 3, 64))) << 32 | static_cast<uint32_t>(__shfl(lo, l >> 3, 64));
+  __builtin_amdgcn_global_load_lds((glb_void *)(reinterpret_cast<const uint8_t *>(rope) + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4)),
+                                   (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
 }
 
-template <typename T, int QT>
+// The wave's 8 rows of a tile on their way to LDS, in LOADS parts; the tile's cache rows are at `rows`.  Through a
+// buffer descriptor: one lane's offset and the place in LDS are all that a row takes, and unlike a global
+// load it does not make the compiler wait for every LDS read under way.  A cache of 4 GB and more (WIDE) adds
+// the upper half of an offset to the descriptor's base.  Where there is no row it is the cache's first; zero() takes it out.
+template <bool WIDE>
+struct Fetch {
+  int32_t row, rope_row;
+  int lo, hi, r0;
+  uint32_t rope, rope_stride;
+  uint64_t base;
+  uint8_t *stage;
+  ECHO_DEV void look(const int32_t *__restrict__ rows, int wv) {
+    r0 = wv * (TILE / WAVES);
+    row = rows[lane_id() & 31];
+    rope_row = rows[r0 + (lane_id() >> 3)];
+  }
+  // Returns which of the tile's 32 tokens there are.
+  ECHO_DEV uint32_t prepare(const AttArgs &x, uint8_t *to) {
+    const uint32_t stride = static_cast<uint32_t>(x.a.kv_stride * 2);
+    base = reinterpret_cast<uint64_t>(x.a.kv);
+    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * stride;
+    lo = static_cast<int>(at);
+    hi = WIDE ? static_cast<int>(at >> 32) : 0;
+    rope = static_cast<uint32_t>(max(rope_row, 0)) * stride;
+    rope_stride = stride;
+    stage = to;
+    return static_cast<uint32_t>(__ballot(row >= 0));
+  }
+  ECHO_DEV void load(int i) const {
+    const int l = lane_id();
+    if (i < TILE / WAVES) {                                // r0 is a multiple of 4
+      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i))) << 32 : 0;
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base + above), 0, -1, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(r0) + row_at(i)), 16, l * 16,
+                                               __builtin_amdgcn_readlane(lo, r0 + i), 0, 0);
+    } else if (WIDE) {                                     // eight rows in one load: addresses by lane
+      const uint64_t at = base + static_cast<uint64_t>(static_cast<uint32_t>(max(rope_row, 0))) * (rope_stride) + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4);
+      __builtin_amdgcn_global_load_lds((glb_void *)reinterpret_cast<const uint8_t *>(at), (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
+    } else {
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base), 0, -1, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + ROPE_AT + r0 * 128), 16, rope + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4), 0, 0, 0);
+    }
+  }
+};
+// Rows of this wave's 8 that are no token's, once they are there: zeros, so that nothing of the cache gets into a sum
+// through a weight of 0.
+ECHO_DEV void zero(uint8_t *__restrict__ stage, uint32_t real, int wv) {
+  const int l = lane_id(), r0 = wv * (TILE / WAVES);
+  const uint32_t mine = real >> r0 & 0xFFu;
+  if (mine == 0xFFu) return;                               // the same for the whole wave
+#pragma unroll
+  for (int i = 0; i < TILE / WAVES; ++i)
+    if (!(mine >> i & 1)) *reinterpret_cast<u32x4 *>(stage + row_at(r0 + i) + 16 * l) = u32x4{0, 0, 0, 0};
+  if (!(mine >> (l >> 3) & 1)) *reinterpret_cast<u32x4 *>(stage + ROPE_AT + (r0 + (l >> 3)) * 128 + 16 * (l & 7)) = u32x4{0, 0, 0, 0};
+}
+
+template <typename T, int QT, bool WIDE>
 struct Waves {
   typedef typename Mma<T>::x8 x8;
   x8 q[QT][KSTEPS];              // 16 QT queries: lane (j, g) values of query 16 i + j
-  v4f s[QT];                     // a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
+  v4f acc[QT], s[QT];            // products, and a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
   float m[QT], sum[QT], tile_sum[QT];
   v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
   int wv, qb, th;                // qb: the wave's first query for scores
@@ -146,9 +190,9 @@ struct Waves {
     int g, swap;
     ECHO_DEV x8 read(int k) const { return k < 16 ? read16<x8>(v + 16 * k) : read16<x8>(r + (((4 * (k - 16) + g) ^ swap) << 4)); }
   };
-  ECHO_DEV Rows rows_of(const uint8_t *__restrict__ stage) const {
+  ECHO_DEV static Rows rows_of(const uint8_t *__restrict__ stage, int half) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-    return Rows{stage + row_at(th * 16 + j) + 256 * g, stage + ROPE_AT + (th * 16 + j) * 128, g, swap_r(j)};
+    return Rows{stage + row_at(half * 16 + j) + 256 * g, stage + ROPE_AT + (half * 16 + j) * 128, g, swap_r(j)};
   }
   // Base 2, and -infinity where there is no token; `real`: the tile's tokens that there are.
   ECHO_DEV void finish(float scale2, uint32_t real) {
@@ -157,18 +201,18 @@ struct Waves {
     for (int v = 0; v < 4; ++v) {
       const float none = mine >> v & 1 ? 0.f : -INFINITY;
 #pragma unroll
-      for (int i = 0; i < QT; ++i) s[i][v] = fmaf(s[i][v], scale2, none);
+      for (int i = 0; i < QT; ++i) s[i][v] = fmaf(acc[i][v], scale2, none);
     }
   }
   ECHO_DEV void scores(const uint8_t *__restrict__ stage, float scale2, uint32_t real) {
-    const Rows r = rows_of(stage);
+    const Rows r = rows_of(stage, th);
 #pragma unroll
-    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < QT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k) {
       const x8 row = r.read(k);
 #pragma unroll
-      for (int i = 0; i < QT; ++i) s[i] = Mma<T>::mul(row, q[i][k], s[i]);
+      for (int i = 0; i < QT; ++i) acc[i] = Mma<T>::mul(row, q[i][k], acc[i]);
     }
     finish(scale2, real);
   }
@@ -267,34 +311,51 @@ struct Waves {
         for (int i = 0; i < QT; ++i) o[i][c] = Mma<T>::mul(col, w[i][k], o[i][c]);
       }
   }
-  // Scores and weights of tile t + 1 and the sum over tile t.  The order of the reads and products is this one: left to
-  // itself the compiler reads each operand right before its product, and the matrix core waits for LDS.  An
-  // operand is read AHEAD products before its use, and the exponentials stand between the products of the sum.
-  ECHO_DEV void step(uint8_t *__restrict__ lds, int t, float scale2, uint32_t real) {
+  // Scores and weights of tile t + 1, the sum over tile t and, with FETCH, the loads of tile t + 3, whose tokens go to
+  // `real3`.  The order of the reads and products is this one: left to itself the compiler reads each operand right
+  // before its product, and the matrix core waits for LDS.  An operand is read six products before its use;
+  // the loads stand between the products of the scores, the exponentials between those of the sum.
+  template <bool FETCH>
+  ECHO_DEV void step(const AttArgs &x, Lds &l_, int t, float scale2, uint32_t real, const int32_t *__restrict__ rows, uint32_t &real3) {
     constexpr int AHEAD = 6, STEPS = COLS / 16, AHEAD_V = 3;
-    const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE);
-    const Cols x = cols_of(lds, t);
+    uint8_t *lds = l_.stage;
+    const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE, th);
+    const Cols cols = cols_of(lds, t);
     x8 row[AHEAD], col[AHEAD_V], w[QT][2];
+    Fetch<WIDE> f;
+    if (FETCH) f.look(rows, wv);
+    const int32_t far = l_.raise[t & 1];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
 #pragma unroll
-    for (int i = 0; i < QT; ++i) s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < QT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k) {
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
-        pin(s[i]);
-        s[i] = Mma<T>::mul(row[k % AHEAD], q[i][k], s[i]);
+        pin(acc[i]);
+        acc[i] = Mma<T>::mul(row[k % AHEAD], q[i][k], acc[i]);
       }
-      pin(s[0]);
+      pin(acc[0]);
       if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
-      else if (k + AHEAD - KSTEPS < AHEAD_V) col[k + AHEAD - KSTEPS] = x.read((k + AHEAD - KSTEPS) >> 1, (k + AHEAD - KSTEPS) & 1);
-      else if (k == KSTEPS - 2 || k == KSTEPS - 1) {
+      else if (k + AHEAD - KSTEPS < AHEAD_V) col[k + AHEAD - KSTEPS] = cols.read((k + AHEAD - KSTEPS) >> 1, (k + AHEAD - KSTEPS) & 1);
+      else if (k >= KSTEPS - 2) {
 #pragma unroll
-        for (int i = 0; i < QT; ++i) w[i][k - (KSTEPS - 2)] = x.weights(i, k - (KSTEPS - 2));
+        for (int i = 0; i < QT; ++i) w[i][k - (KSTEPS - 2)] = cols.weights(i, k - (KSTEPS - 2));
       }
+      if (FETCH && k == 1) real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
+      if (FETCH && k >= 2 && k < 2 + LOADS) f.load(k - 2);
     }
-    float e[QT * 4];
+    if (__builtin_amdgcn_readfirstlane(far) == t + 1) {
+      raise(l_, t);
+#pragma unroll
+      for (int i = 0; i < QT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) w[i][k] = cols.weights(i, k);
+    }
+#pragma unroll
+    for (int i = 0; i < QT; ++i) sum[i] += tile_sum[i];
+    float e[QT][4];
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
 #pragma unroll
@@ -303,37 +364,69 @@ struct Waves {
         o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD_V], w[i][u & 1], o[i][u >> 1]);
       }
       pin(o[0][u >> 1]);
-      if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = x.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
-      if (u == 1) finish(scale2, real);
-      if (u >= 2) {
+      if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = cols.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
+      if (u == 0) finish(scale2, real);
+      if (u >= 1 && u <= 4) {
 #pragma unroll
-        for (int n = 0; n < 4 * QT; ++n)
-          if (n % (STEPS - 3) == u - 2) e[n] = exp2_(s[n >> 2][n & 3] - m[n >> 2]);
+        for (int i = 0; i < QT; ++i) {
+          e[i][u - 1] = exp2_(s[i][u - 1] - m[i]);
+          asm volatile("" : "+v"(e[i][u - 1]));
+        }
+      }
+      if (u == 5) {
+#pragma unroll
+        for (int i = 0; i < QT; ++i) put(lds, t + 1, i, v4f{e[i][0], e[i][1], e[i][2], e[i][3]});
       }
     }
-#pragma unroll
-    for (int i = 0; i < QT; ++i) put(lds, t + 1, i, v4f{e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]});
+    if (far_above() && lane_id() == 0) l_.raise[(t + 1) & 1] = t + 2;
   }
 };
 
-template <typename T, int QT>
+template <typename T, int QT, bool WIDE>
 ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int l = lane_id(), j = l & 15, g = l >> 4;
-  Waves<T, QT> a;
+  Waves<T, QT, WIDE> a;
   a.wv = wv;
   a.qb = (wv >> 1) * 16 * QT;
   a.th = wv & 1;
+  // The queries' rows go to registers by way of LDS, to the stages that the first two tiles of tokens do not
+  // need: read by the waves themselves they were four pieces of a row a load, a line each.
+  constexpr int Q_STAGE = STAGES - QT;
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int64_t qi = min(w.q0 + 32 * i + wv * (TILE / WAVES) + (l & 7), w.q1 - 1), r = qi / x.a.n_heads;
+    load_rows(reinterpret_cast<uint64_t>(x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head), lds.stage + (Q_STAGE + i) * STAGE, wv * (TILE / WAVES));
+  }
+  if (threadIdx.x < 64) lds.m[threadIdx.x] = NO_SCORE;
+  if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
+  const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
+  constexpr int TILES = BATCH / TILE;
+  uint32_t real[3] = {};                                   // of tiles t + 1, t + 2, t + 3
+  if (n > 0) look_up(w, 0, lds.rows);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vmcnt(0));
+  meet();
+  const auto first = [&](int t) {
+    if (t >= n) return;
+    Fetch<WIDE> f;
+    f.look(lds.rows + t * TILE, wv);
+    real[t] = f.prepare(x, lds.stage + t * STAGE);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) f.load(i);
+  };
+  first(0);
+  first(1);
   // A negative scale goes into the queries' signs, no scale makes them 0: a masked product then stays at -infinity.
   const uint32_t flip = x.a.scale2 < 0.f ? 0x80008000u : 0u, keep = x.a.scale2 == 0.f ? 0u : ~0u;
   const float scale2 = x.a.scale2 == 0.f ? 1.f : fabsf(x.a.scale2);
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
-    const int64_t qi = min(w.q0 + a.qb + 16 * i + j, w.q1 - 1), r = qi / x.a.n_heads;
-    const uint16_t *q = x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head;
+    const int at = a.qb + 16 * i;
+    const auto rows = a.rows_of(lds.stage + (Q_STAGE + (at >> 5)) * STAGE, (at >> 4) & 1);
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k) {
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(q + 8 * (k < 16 ? k + 16 * g : 64 + 4 * (k - 16) + g));
+      const u32x4 v = __builtin_bit_cast(u32x4, rows.read(k));
       a.q[i][k] = __builtin_bit_cast(typename Mma<T>::x8, (v & keep) ^ flip);
     }
     a.m[i] = NO_SCORE;
@@ -341,59 +434,47 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
 #pragma unroll
     for (int c = 0; c < COLS / 32; ++c) a.o[i][c] = v16f{};
   }
-  if (threadIdx.x < 64) lds.m[threadIdx.x] = NO_SCORE;
-  if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
-  const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
-  constexpr int TILES = BATCH / TILE;
-  uint32_t real[3];                                        // of tiles t + 1, t + 2, t + 3
-  if (n > 0) {
-    look_up(w, 0, lds.rows);
-    meet();
-  }
-#pragma unroll
-  for (int t = 0; t < 3; ++t)
-    if (t < n) real[t] = fetch(x, lds.rows + t * TILE, lds.stage + t * STAGE, wv);
-  // The tiles but the `later` youngest of this wave's loads are in LDS.
-  const auto arrived = [&](int later) {
+  meet();
+  first(2);
+  // The tiles but the `later` youngest of this wave's loads are in LDS, rows that are no token's made zeros, and so are
+  // the other waves'; the tile that is needed next is `t`, its tokens `have`.
+  const auto arrived = [&](int later, int t, uint32_t have) {
     asm volatile("" ::: "memory");
     if (later >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * LOADS));
     else if (later == 1) __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));
     else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    asm volatile("" ::: "memory");
+    zero(lds.stage + t % STAGES * STAGE, have, wv);
     meet();
   };
-  const auto tell = [&](int t) {
-    if (a.far_above() && l == 0) lds.raise[t & 1] = t + 1;
-  };
   if (n > 0) {
-    arrived(min(n - 1, 2));
+    arrived(min(n - 1, 2), 0, real[0]);
     a.scores(lds.stage, scale2, real[0]);
     a.weigh(lds.stage, 0);
-    tell(0);
-    // Tile t + 1 and the weights of tile t are there for all; every wave is done with tile t - 1.
-    const auto begin = [&](int t) {
-      arrived(t + 2 < n ? 1 : 0);
-      const int32_t far = lds.raise[t & 1];
-      if (t + 3 < n) {
-        const int in = (t + 3) % TILES;
-        if (in == 0) {                                     // every wave has taken the last batch's rows
-          look_up(w, (t + 3) * TILE, lds.rows);
-          meet();
-        }
-        real[2] = fetch(x, lds.rows + in * TILE, lds.stage + (t + 3) % STAGES * STAGE, wv);
-      }
-      if (far == t + 1) a.raise(lds, t);
-#pragma unroll
-      for (int i = 0; i < QT; ++i) a.sum[i] += a.tile_sum[i];
-    };
+    if (a.far_above() && l == 0) lds.raise[0] = 1;
+    // A step begins when tile t + 1 and the weights of tile t are there for all, and every wave is done with tile t - 1.
     int t = 0;
-    for (; t + 1 < n; ++t) {
+    for (; t + 3 < n; ++t) {
+      arrived(1, t + 1, real[1]);
+      const int in = (t + 3) % TILES;
+      if (in == 0) {                                       // every wave has taken the last batch's rows
+        look_up(w, (t + 3) * TILE, lds.rows);
+        meet();
+      }
       const uint32_t have = real[1];
       real[1] = real[2];
-      begin(t);
-      a.step(lds.stage, t, scale2, have);
-      tell(t + 1);
+      a.template step<true>(x, lds, t, scale2, have, lds.rows + in * TILE, real[2]);
     }
-    begin(t);
+    for (; t + 1 < n; ++t) {
+      arrived(t + 2 < n ? 1 : 0, t + 1, real[1]);
+      const uint32_t have = real[1];
+      real[1] = real[2];
+      a.template step<false>(x, lds, t, scale2, have, nullptr, real[2]);
+    }
+    meet();
+    if (lds.raise[t & 1] == t + 1) a.raise(lds, t);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) a.sum[i] += a.tile_sum[i];
     a.add(lds.stage, t);
   }
   // The sums of a query: four lane groups, two waves.
@@ -406,83 +487,90 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
     if (g == 0) lds.top[a.th][a.qb + 16 * i + j] = s;
   }
   meet();
+  // Results by way of LDS, a query's row after the other, so that a store writes whole lines.
+  const bool whole = w.part < 0;
   const int h = l >> 5;
+  constexpr int OUT_ROW = VALUES * static_cast<int>(sizeof(T)) + 16, PART_ROW = VALUES * 4 + 16;
+  static_assert(64 * PART_ROW <= STAGES * STAGE, "results fit the stages");
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     const int at = 32 * i + (l & 31);
-    const int64_t qi = w.q0 + at;
+    const float sum = lds.top[0][at] + lds.top[1][at];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c) {
+      a.pin(a.o[i][c]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const v4f v = {a.o[i][c][4 * b], a.o[i][c][4 * b + 1], a.o[i][c][4 * b + 2], a.o[i][c][4 * b + 3]};
+        const int col = wv * COLS + 32 * c + 8 * b + 4 * h;
+        if (whole) *reinterpret_cast<u32x2 *>(lds.stage + at * OUT_ROW + col * sizeof(T)) = pack4<T>(v * inv);
+        else *reinterpret_cast<v4f *>(lds.stage + at * PART_ROW + col * 4) = v;
+      }
+    }
+  }
+  meet();
+  constexpr int PER = 32 * QT / WAVES;                     // queries that a wave stores
+  const int64_t mine = min(w.q0 + wv * PER + (l % PER), w.q1 - 1), r = mine / x.a.n_heads;
+  const uint64_t to = whole ? reinterpret_cast<uint64_t>(static_cast<T *>(x.out) + r * x.o_row + (mine - r * x.a.n_heads) * x.o_head)
+                            : reinterpret_cast<uint64_t>(x.part + (mine * x.parts + w.part) * VALUES);
+  const int lo = static_cast<int>(to), hi = static_cast<int>(to >> 32);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int at = wv * PER + i;
+    const uint32_t u = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i)), v = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i));
+    uint8_t *p = reinterpret_cast<uint8_t *>(static_cast<uint64_t>(v) << 32 | u) + 16 * l;
+    if (w.q0 + at >= w.q1) break;
+    if (whole) {
+      *reinterpret_cast<u32x4 *>(p) = *reinterpret_cast<const u32x4 *>(lds.stage + at * OUT_ROW + 16 * l);
+    } else {
+      *reinterpret_cast<u32x4 *>(p) = *reinterpret_cast<const u32x4 *>(lds.stage + at * PART_ROW + 16 * l);
+      *reinterpret_cast<u32x4 *>(p + 1024) = *reinterpret_cast<const u32x4 *>(lds.stage + at * PART_ROW + 1024 + 16 * l);
+    }
+  }
+  const int at = threadIdx.x;
+  if (at < 32 * QT && w.q0 + at < w.q1) {
     const float sum = lds.top[0][at] + lds.top[1][at], m = lds.m[at];
-    if (w.part < 0) {
-      const int64_t r = min(qi, w.q1 - 1) / x.a.n_heads;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      T *out = static_cast<T *>(x.out) + r * x.o_row + (min(qi, w.q1 - 1) - r * x.a.n_heads) * x.o_head + wv * COLS + 8 * h;
-      // Halves of the wave exchange: a lane gets 8 consecutive columns, the lower half the first 8 of 16.
-#pragma unroll
-      for (int c = 0; c < COLS / 32; ++c) {
-        a.pin(a.o[i][c]);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          u32x2 u[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int v = 8 * b + 4 * e;
-            u[e] = pack4<T>(v4f{a.o[i][c][v], a.o[i][c][v + 1], a.o[i][c][v + 2], a.o[i][c][v + 3]} * inv);
-          }
-          const auto lo = __builtin_amdgcn_permlane32_swap(u[0][0], u[1][0], false, false);
-          const auto hi = __builtin_amdgcn_permlane32_swap(u[0][1], u[1][1], false, false);
-          if (qi < w.q1) *reinterpret_cast<u32x4 *>(out + 32 * c + 16 * b) = u32x4{lo[0], hi[0], lo[1], hi[1]};
-        }
-      }
-      if (x.lse && wv == 0 && h == 0 && qi < w.q1) x.lse[qi] = sum == 0.f ? -INFINITY : (m + log2_(sum)) * LN2;
-    } else if (qi < w.q1) {
-      const int64_t p = qi * x.parts + w.part;
-      float *out = x.part + p * VALUES + wv * COLS + 4 * h;
-#pragma unroll
-      for (int c = 0; c < COLS / 32; ++c) {
-        a.pin(a.o[i][c]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          *reinterpret_cast<v4f *>(out + 32 * c + 8 * b) = v4f{a.o[i][c][4 * b], a.o[i][c][4 * b + 1], a.o[i][c][4 * b + 2], a.o[i][c][4 * b + 3]};
-      }
-      if (wv == 0 && h == 0) {
-        x.part_ml[2 * p] = m;
-        x.part_ml[2 * p + 1] = sum;
-      }
+    if (!whole) {
+      const int64_t p = (w.q0 + at) * x.parts + w.part;
+      x.part_ml[2 * p] = m;
+      x.part_ml[2 * p + 1] = sum;
+    } else if (x.lse) {
+      x.lse[w.q0 + at] = sum == 0.f ? -INFINITY : (m + log2_(sum)) * LN2;
     }
   }
 }
 
+ECHO_DEV int32_t clamp_row(int32_t r, int32_t n) { return r < 0 ? 0 : r > n ? n : r; }
+
 // The tokens that a query row lists (or, without a list, its own).  Workgroups go to the 8 XCDs in turn, each
 // with an L2 of its own: the head tiles of a chunk follow each other by 8, so that they share the one that the
 // chunk's rows are in.
-template <typename T, int QT>
-__global__ __launch_bounds__(WAVES * 64, 1) void rows_kernel(AttArgs x, uint32_t units, uint32_t head_tiles) {
-  __shared__ __attribute__((aligned(16))) Lds lds;
+template <int QT>
+ECHO_DEV bool rows_work(const AttArgs &x, Work &w) {
+  const uint32_t head_tiles = (x.a.n_heads + 32 * QT - 1) / (32 * QT), units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(x.n_chunks);
   const uint32_t eight = blockIdx.x / (8 * head_tiles), in = blockIdx.x - eight * 8 * head_tiles;
   const uint32_t u = eight * 8 + (in & 7), ht = in >> 3;
-  if (u >= units) return;
+  if (u >= units) return false;
   const int32_t r = static_cast<int32_t>(u / x.n_chunks), c = static_cast<int32_t>(u - static_cast<uint32_t>(r) * x.n_chunks);
-  Work w;
   w.src = x.a.tokens(r);
   w.t0 = c * x.chunk;
   w.t1 = min(w.t0 + x.chunk, x.a.n_tok);
   if (!x.a.idx) {
     w.src.list = nullptr;
     w.t1 = static_cast<int32_t>(min<int64_t>(w.t1, max<int64_t>(w.src.limit, 0)));
-    if (w.t0 >= w.t1 && x.parts > 0) return;               // join_kernel goes by the length too
+    if (w.t0 >= w.t1 && x.parts > 0) return false;         // join_kernel goes by the length too
   }
+  if (x.a.n_kv < 1) w.t1 = w.t0;                           // no rows: no tokens
   w.q0 = static_cast<int64_t>(r) * x.a.n_heads + ht * (32 * QT);
   w.q1 = static_cast<int64_t>(r + 1) * x.a.n_heads;
   w.part = x.parts > 0 ? x.first_part + c : -1;
-  attend<T, QT>(x, w, lds);
+  return true;
 }
 
-ECHO_DEV int32_t clamp_row(int32_t r, int32_t n) { return r < 0 ? 0 : r > n ? n : r; }
-
-// The prefixes: tile `tile` of the groups' query tiles in order, chunk `c`.
-template <typename T, int QT>
-__global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32_t tiles) {
-  __shared__ __attribute__((aligned(16))) Lds lds;
+// The prefixes: a tile of the groups' queries in order, a chunk.
+template <int QT>
+ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
   const int32_t c = blockIdx.x % x.n_chunks;
   uint32_t tile = blockIdx.x / x.n_chunks;
   int32_t gi = 0, r0 = 0, r1 = 0;
@@ -494,16 +582,24 @@ __global__ __launch_bounds__(WAVES * 64, 1) void prefix_kernel(AttArgs x, uint32
     if (tile < has) break;
     tile -= has;
   }
-  if (gi == x.n_groups) return;
-  Work w;
+  if (gi == x.n_groups) return false;
   w.src = Tokens{nullptr, x.prefix_table + static_cast<int64_t>(gi) * x.prefix_pages, x.prefix_len[gi], 0, x.a.pshift, x.prefix_pages, x.a.n_kv};
   w.t0 = c * x.chunk;
   w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.chunk, x.a.n_tok), w.src.limit));
-  if (w.t0 >= w.t1) return;
+  if (w.t0 >= w.t1) return false;
+  if (x.a.n_kv < 1) w.t1 = w.t0;                           // no rows: no tokens
   w.q0 = static_cast<int64_t>(r0) * x.a.n_heads + static_cast<int64_t>(tile) * (32 * QT);
   w.q1 = static_cast<int64_t>(r1) * x.a.n_heads;
   w.part = c;
-  attend<T, QT>(x, w, lds);
+  return true;
+}
+
+template <typename T, int QT, bool WIDE>
+__global__ __launch_bounds__(WAVES * 64, 1) void attention_kernel(AttArgs x) {
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  Work w;
+  const bool any = x.n_groups > 0 ? prefix_work<QT>(x, w) : rows_work<QT>(x, w);
+  if (any) attend<T, QT, WIDE>(x, w, lds);
 }
 
 // ---------------------------------------------------------------- joining chunks
@@ -606,24 +702,23 @@ PrefixPlan prefix_plan(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_
   return p;
 }
 
-template <typename T>
-int launch_rows(const AttArgs &x, const RowsPlan &p, hipStream_t st) {
-  const uint32_t units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(p.n_chunks), ht = static_cast<uint32_t>(p.head_tiles);
-  const uint32_t grid = (units + 7) / 8 * 8 * ht;
-  switch (p.mt) {
-    case 1: rows_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
-    default: rows_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, units, ht); break;
-  }
+template <typename T, bool WIDE>
+int launch_attention(const AttArgs &x, int mt, uint32_t grid, hipStream_t st) {
+  if (mt == 1) attention_kernel<T, 1, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
+  else attention_kernel<T, 2, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
   return check_launch("attention");
 }
-template <typename T>
-int launch_prefix(const AttArgs &x, const PrefixPlan &p, hipStream_t st) {
-  const uint32_t tiles = static_cast<uint32_t>(p.tiles), grid = tiles * static_cast<uint32_t>(p.prefix_parts);
-  switch (p.mt) {
-    case 1: prefix_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
-    default: prefix_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x, tiles); break;
-  }
-  return check_launch("prefix attention");
+int launch_attention(const AttArgs &x, int type, int mt, uint32_t grid, hipStream_t st) {
+  const bool wide = static_cast<int64_t>(x.a.n_kv) * x.a.kv_stride * 2 >= (1ll << 32) - 4096;
+  if (type == ECHO_BF16) return wide ? launch_attention<bf16_t, true>(x, mt, grid, st) : launch_attention<bf16_t, false>(x, mt, grid, st);
+  return wide ? launch_attention<fp16_t, true>(x, mt, grid, st) : launch_attention<fp16_t, false>(x, mt, grid, st);
+}
+int launch_rows(const AttArgs &x, int type, const RowsPlan &p, hipStream_t st) {
+  const uint32_t units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(p.n_chunks), ht = static_cast<uint32_t>(p.head_tiles);
+  return launch_attention(x, type, p.mt, (units + 7) / 8 * 8 * ht, st);
+}
+int launch_prefix(const AttArgs &x, int type, const PrefixPlan &p, hipStream_t st) {
+  return launch_attention(x, type, p.mt, static_cast<uint32_t>(p.tiles) * static_cast<uint32_t>(p.prefix_parts), st);
 }
 template <typename T>
 int launch_join(const JoinArgs &j, hipStream_t st) {
@@ -730,7 +825,7 @@ extern "C" int echo_sparse_attention(const echo_latent_args *a, void *out, int64
     x.part = static_cast<float *>(ws);
     x.part_ml = x.part + queries * p.n_chunks * VALUES;
   }
-  rc = a->type == ECHO_BF16 ? launch_rows<bf16_t>(x, p, S(stream)) : launch_rows<fp16_t>(x, p, S(stream));
+  rc = launch_rows(x, a->type, p, S(stream));
   if (rc != ECHO_OK || p.n_chunks == 1) return rc;
   JoinArgs j = {};
   j.part = x.part; j.ml = x.part_ml; j.out = out; j.o_row = out_row_stride; j.o_head = out_head_stride; j.lse = lse;
@@ -786,12 +881,12 @@ extern "C" int echo_prefix_attention(const echo_prefix_args *a, void *out, int64
     y.chunk = p.chunk; y.n_chunks = p.prefix_parts;
     y.group_begin = a->group_begin; y.prefix_len = a->prefix_len; y.prefix_table = a->prefix_table;
     y.n_groups = a->n_groups; y.prefix_pages = a->prefix_pages;
-    rc = bf ? launch_prefix<bf16_t>(y, p, S(stream)) : launch_prefix<fp16_t>(y, p, S(stream));
+    rc = launch_prefix(y, a->type, p, S(stream));
     if (rc != ECHO_OK) return rc;
   }
   if (p.own_parts) {
     x.chunk = p.own.chunk; x.n_chunks = p.own_parts; x.first_part = p.prefix_parts;
-    rc = bf ? launch_rows<bf16_t>(x, p.own, S(stream)) : launch_rows<fp16_t>(x, p.own, S(stream));
+    rc = launch_rows(x, a->type, p.own, S(stream));
     if (rc != ECHO_OK) return rc;
   }
   const JoinArgs j = {x.part, x.part_ml, out, out_row_stride, out_head_stride, lse, a->n_rows, a->n_heads, parts, a->own_len, a->group_begin,

@@ -160,6 +160,15 @@ inline float emu_amdgcn_logf(float x) { return std::log2(x); }
 inline void emu_amdgcn_global_load_lds(const void *g, void *lds, unsigned size, int, unsigned) {
   memcpy(static_cast<char *>(lds) + emu::ctx()->lane * size, g, size);
 }
+// the same through a buffer descriptor of `bytes` bytes: what lies behind them reads as 0
+struct emu_rsrc { const char *base; unsigned bytes; };
+inline emu_rsrc emu_amdgcn_make_buffer_rsrc(void *base, short, int bytes, int) { return emu_rsrc{static_cast<const char *>(base), static_cast<unsigned>(bytes)}; }
+inline void emu_amdgcn_raw_ptr_buffer_load_lds(emu_rsrc r, void *lds, unsigned size, unsigned voffset, unsigned soffset, unsigned offset, unsigned) {
+  char *to = static_cast<char *>(lds) + emu::ctx()->lane * size;
+  const unsigned at = voffset + soffset + offset;
+  if (at + size <= r.bytes) memcpy(to, r.base + at, size);
+  else memset(to, 0, size);
+}
 inline void emu_amdgcn_s_waitcnt(int) {}
 inline void emu_amdgcn_s_setprio(int) {}
 #define emu_amdgcn_s_barrier() emu::barrier()
