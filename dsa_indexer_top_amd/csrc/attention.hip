@@ -27,9 +27,10 @@
 
 namespace echo {
 
-constexpr int WAVES = 4, TILE = 32, STAGES = 4;            // tokens of a tile, tiles in LDS
+constexpr int WAVES = 8, TILE = 32, STAGES = 4;            // tokens of a tile, tiles in LDS
 constexpr int KSTEPS = LATENT / 32, COLS = VALUES / WAVES; // products of a score, columns of a wave
-constexpr int LOADS = TILE / WAVES + 1;                    // a wave's loads of a tile
+constexpr int OWN = TILE / WAVES;                          // a wave's rows of a tile; the first four waves also load
+                                                           // the last 64 values of 8 rows each
 constexpr int BATCH = 1536;                                // tokens whose rows are looked up at once
 constexpr float SLACK = 8.f;
 
@@ -109,7 +110,7 @@ ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) 
 ECHO_DEV void load_rows(uint64_t at, uint8_t *__restrict__ stage, int r0) {
   const int l = lane_id(), lo = static_cast<int>(at), hi = static_cast<int>(at >> 32);
 #pragma unroll
-  for (int i = 0; i < TILE / WAVES; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i)), b = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i));
     const uint8_t *src = reinterpret_cast<const uint8_t *>(static_cast<uint64_t>(b) << 32 | a);
     __builtin_amdgcn_global_load_lds((glb_void *)(src + l * 16), (lds_void *)(stage + row_at(r0) + row_at(i)), 16, 0, 0);
@@ -119,70 +120,72 @@ ECHO_DEV void load_rows(uint64_t at, uint8_t *__restrict__ stage, int r0) {
                                    (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
 }
 
-// The wave's 8 rows of a tile on their way to LDS, in LOADS parts; the tile's cache rows are at `rows`.  Through a
+// The wave's rows of a tile on their way to LDS, a part at a time; the tile's cache rows are at `rows`.  Through a
 // buffer descriptor: one lane's offset and the place in LDS are all that a row takes, and unlike a global
 // load it does not make the compiler wait for every LDS read under way.  A cache of 4 GB and more (WIDE) adds
 // the upper half of an offset to the descriptor's base.  Where there is no row it is the cache's first; zero() takes it out.
 template <bool WIDE>
 struct Fetch {
   int32_t row, rope_row;
-  int lo, hi, r0;
-  uint32_t rope, rope_stride;
-  uint64_t base;
+  int lo, hi, wv;
+  uint64_t rope;
+  const void *kv;
   uint8_t *stage;
-  ECHO_DEV void look(const int32_t *__restrict__ rows, int wv) {
-    r0 = wv * (TILE / WAVES);
+  ECHO_DEV void look(const int32_t *__restrict__ rows, int wave) {
+    wv = wave;
     row = rows[lane_id() & 31];
-    rope_row = rows[r0 + (lane_id() >> 3)];
+    rope_row = rows[8 * (wv & 3) + (lane_id() >> 3)];
   }
   // Returns which of the tile's 32 tokens there are.
   ECHO_DEV uint32_t prepare(const AttArgs &x, uint8_t *to) {
+    const int l = lane_id();
     const uint32_t stride = static_cast<uint32_t>(x.a.kv_stride * 2);
-    base = reinterpret_cast<uint64_t>(x.a.kv);
+    kv = x.a.kv;
     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * stride;
     lo = static_cast<int>(at);
-    hi = WIDE ? static_cast<int>(at >> 32) : 0;
-    rope = static_cast<uint32_t>(max(rope_row, 0)) * stride;
-    rope_stride = stride;
+    hi = static_cast<int>(at >> 32);
+    rope = static_cast<uint64_t>(static_cast<uint32_t>(max(rope_row, 0))) * stride + 1024 + (((l & 7) ^ swap_r(8 * (wv & 3) + (l >> 3))) << 4);
     stage = to;
     return static_cast<uint32_t>(__ballot(row >= 0));
   }
   ECHO_DEV void load(int i) const {
-    const int l = lane_id();
-    if (i < TILE / WAVES) {                                // r0 is a multiple of 4
-      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i))) << 32 : 0;
-      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base + above), 0, -1, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(r0) + row_at(i)), 16, l * 16,
-                                               __builtin_amdgcn_readlane(lo, r0 + i), 0, 0);
-    } else if (WIDE) {                                     // eight rows in one load: addresses by lane
-      const uint64_t at = base + static_cast<uint64_t>(static_cast<uint32_t>(max(rope_row, 0))) * (rope_stride) + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4);
-      __builtin_amdgcn_global_load_lds((glb_void *)reinterpret_cast<const uint8_t *>(at), (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
-    } else {
-      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base), 0, -1, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + ROPE_AT + r0 * 128), 16, rope + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4), 0, 0, 0);
+    if (i < OWN) {
+      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, OWN * wv + i))) << 32 : 0;
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(reinterpret_cast<uint64_t>(kv) + above), 0, -1, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(OWN * wv) + row_at(i)), 16, lane_id() * 16,
+                                               __builtin_amdgcn_readlane(lo, OWN * wv + i), 0, 0);
+    } else if (wv < 4) {
+      uint8_t *to = stage + ROPE_AT + wv * 1024;
+      if (WIDE) {                                          // eight rows in one load: addresses by lane
+        __builtin_amdgcn_global_load_lds((glb_void *)(static_cast<const uint8_t *>(kv) + rope), (lds_void *)to, 16, 0, 0);
+      } else {
+        const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(kv), 0, -1, 0x00027000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)to, 16, static_cast<uint32_t>(rope), 0, 0, 0);
+      }
     }
   }
 };
-// Rows of this wave's 8 that are no token's, once they are there: zeros, so that nothing of the cache gets into a sum
-// through a weight of 0.
+// Rows that this wave has loaded and that are no token's, once they are there: zeros, so that nothing of the cache gets
+// into a sum through a weight of 0.
 ECHO_DEV void zero(uint8_t *__restrict__ stage, uint32_t real, int wv) {
-  const int l = lane_id(), r0 = wv * (TILE / WAVES);
-  const uint32_t mine = real >> r0 & 0xFFu;
-  if (mine == 0xFFu) return;                               // the same for the whole wave
+  if (real == ~0u) return;                                 // the same for the whole wave
+  const int l = lane_id();
 #pragma unroll
-  for (int i = 0; i < TILE / WAVES; ++i)
-    if (!(mine >> i & 1)) *reinterpret_cast<u32x4 *>(stage + row_at(r0 + i) + 16 * l) = u32x4{0, 0, 0, 0};
-  if (!(mine >> (l >> 3) & 1)) *reinterpret_cast<u32x4 *>(stage + ROPE_AT + (r0 + (l >> 3)) * 128 + 16 * (l & 7)) = u32x4{0, 0, 0, 0};
+  for (int i = 0; i < OWN; ++i)
+    if (!(real >> (OWN * wv + i) & 1)) *reinterpret_cast<u32x4 *>(stage + row_at(OWN * wv) + row_at(i) + 16 * l) = u32x4{0, 0, 0, 0};
+  if (wv < 4 && !(real >> (8 * wv + (l >> 3)) & 1)) *reinterpret_cast<u32x4 *>(stage + ROPE_AT + wv * 1024 + 16 * l) = u32x4{0, 0, 0, 0};
 }
 
 template <typename T, int QT, bool WIDE>
 struct Waves {
   typedef typename Mma<T>::x8 x8;
-  x8 q[QT][KSTEPS];              // 16 QT queries: lane (j, g) values of query 16 i + j
-  v4f acc[QT], s[QT];            // products, and a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
-  float m[QT], sum[QT], tile_sum[QT];
+  x8 q[KSTEPS];                  // 16 queries: lane (j, g) values of query qb + j
+  v4f acc, s;                    // products, and a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
+  float m, sum, tile_sum;
   v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
   int wv, qb, th;                // qb: the wave's first query for scores
+
+  ECHO_DEV bool scores_here() const { return QT == 2 || wv < 4; }
 
   // Scores of a tile's tokens: product k of the wave's 16 rows.
   struct Rows {
@@ -198,58 +201,32 @@ struct Waves {
   ECHO_DEV void finish(float scale2, uint32_t real) {
     const uint32_t mine = real >> (16 * th + 4 * (lane_id() >> 4));
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float none = mine >> v & 1 ? 0.f : -INFINITY;
-#pragma unroll
-      for (int i = 0; i < QT; ++i) s[i][v] = fmaf(acc[i][v], scale2, none);
-    }
+    for (int v = 0; v < 4; ++v) s[v] = fmaf(acc[v], scale2, mine >> v & 1 ? 0.f : -INFINITY);
   }
-  ECHO_DEV void scores(const uint8_t *__restrict__ stage, float scale2, uint32_t real) {
-    const Rows r = rows_of(stage, th);
-#pragma unroll
-    for (int i = 0; i < QT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) {
-      const x8 row = r.read(k);
-#pragma unroll
-      for (int i = 0; i < QT; ++i) acc[i] = Mma<T>::mul(row, q[i][k], acc[i]);
-    }
-    finish(scale2, real);
-  }
-  ECHO_DEV void put(uint8_t *__restrict__ lds, int t, int i, const v4f &w) {
-    const int l = lane_id(), j = l & 15, g = l >> 4, at = qb + 16 * i + j;
-    tile_sum[i] = (w[0] + w[1]) + (w[2] + w[3]);
-    *reinterpret_cast<u32x2 *>(lds + weights_at(t, at) + 32 * th + 8 * g) = pack4<T>(w);
+  ECHO_DEV void put(uint8_t *__restrict__ lds, int t, const v4f &w) {
+    const int l = lane_id(), j = l & 15, g = l >> 4;
+    tile_sum = (w[0] + w[1]) + (w[2] + w[3]);
+    *reinterpret_cast<u32x2 *>(lds + weights_at(t, qb + j) + 32 * th + 8 * g) = pack4<T>(w);
   }
   ECHO_DEV void weigh(uint8_t *__restrict__ lds, int t) {
+    v4f w;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      v4f w;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) w[v] = exp2_(s[i][v] - m[i]);
-      put(lds, t, i, w);
-    }
+    for (int v = 0; v < 4; ++v) w[v] = exp2_(s[v] - m);
+    put(lds, t, w);
   }
   // An empty statement that takes and gives accumulation registers: between two of them the compiler copies one
   // group of sums to where it can be multiplied, and holds them all where the matrix core adds them up otherwise.
   ECHO_DEV static void pin(v16f &v) { asm volatile("" : "+a"(v)); }
   ECHO_DEV static void pin(v4f &v) { asm volatile("" : "+a"(v)); }
-  ECHO_DEV static float top_of(const v4f &s) { return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])); }
-  ECHO_DEV bool far_above() const {
-    bool f = false;
-#pragma unroll
-    for (int i = 0; i < QT; ++i) f |= top_of(s[i]) > m[i] + SLACK;
-    return __ballot(f) != 0;
-  }
+  ECHO_DEV float top() const { return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])); }
   // Every wave: maxima up to those of the tile, sums and weights on the new scale.
   ECHO_DEV void raise(Lds &lds, int t) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-#pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      float top = top_of(s[i]);
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      if (g == 0) lds.top[th][qb + 16 * i + j] = top;
+    if (scores_here()) {
+      float a = top();
+      a = fmaxf(a, __shfl_xor(a, 16, 64));
+      a = fmaxf(a, __shfl_xor(a, 32, 64));
+      if (g == 0) lds.top[th][qb + j] = a;
     }
     meet();
 #pragma unroll
@@ -264,19 +241,17 @@ struct Waves {
         pin(o[i][c]);
       }
     }
-    float to[QT];
-#pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      const int at = qb + 16 * i + j;
-      to[i] = fmaxf(m[i], fmaxf(lds.top[0][at], lds.top[1][at]));
-      sum[i] *= exp2_(m[i] - to[i]);
-      m[i] = to[i];
+    float to = m;
+    if (scores_here()) {
+      to = fmaxf(m, fmaxf(lds.top[0][qb + j], lds.top[1][qb + j]));
+      sum *= exp2_(m - to);
+      m = to;
     }
     meet();
-    if (th == 0 && g == 0)
-#pragma unroll
-      for (int i = 0; i < QT; ++i) lds.m[qb + 16 * i + j] = to[i];
-    weigh(lds.stage, t);
+    if (scores_here()) {
+      if (th == 0 && g == 0) lds.m[qb + j] = to;
+      weigh(lds.stage, t);
+    }
     meet();
   }
   // The sum's operands: weights of query 32 i + j and columns 32 c .. of the wave's, tokens 16 k + 8 h .. + 7.
@@ -295,92 +270,72 @@ struct Waves {
     return Cols{lds + weights_at(t, j) + 16 * h,
                 lds + t % STAGES * STAGE + row_at(8 * h) + ((l & 15) >> 2) * ROW_STEP + wv * (2 * COLS) + 32 * ((l >> 4) & 1) + 8 * (l & 3)};
   }
-  ECHO_DEV void add(const uint8_t *__restrict__ lds, int t) {
-    const Cols x = cols_of(lds, t);
-    x8 w[QT][2];
-#pragma unroll
-    for (int i = 0; i < QT; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) w[i][k] = x.weights(i, k);
-#pragma unroll
-    for (int c = 0; c < COLS / 32; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const x8 col = x.read(c, k);
-#pragma unroll
-        for (int i = 0; i < QT; ++i) o[i][c] = Mma<T>::mul(col, w[i][k], o[i][c]);
-      }
-  }
-  // Scores and weights of tile t + 1, the sum over tile t and, with FETCH, the loads of tile t + 3, whose tokens go to
-  // `real3`.  The order of the reads and products is this one: left to itself the compiler reads each operand right
-  // before its product, and the matrix core waits for LDS.  An operand is read six products before its use;
-  // the loads stand between the products of the scores, the exponentials between those of the sum.
-  template <bool FETCH>
+  // Scores and weights of tile t + 1 (SCORE), the sum over tile t (SUM) and, with FETCH, the loads of tile t + 3, whose
+  // tokens go to `real3`.  The order of the reads and products is this one: left to itself the compiler reads each
+  // operand right before its product, and the matrix core waits for LDS.
+  template <bool SCORE, bool SUM, bool FETCH>
   ECHO_DEV void step(const AttArgs &x, Lds &l_, int t, float scale2, uint32_t real, const int32_t *__restrict__ rows, uint32_t &real3) {
-    constexpr int AHEAD = 6, STEPS = COLS / 16, AHEAD_V = 3;
+    constexpr int AHEAD = 4, STEPS = COLS / 16, AHEAD_V = 2;
     uint8_t *lds = l_.stage;
-    const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE, th);
     const Cols cols = cols_of(lds, t);
-    x8 row[AHEAD], col[AHEAD_V], w[QT][2];
     Fetch<WIDE> f;
     if (FETCH) f.look(rows, wv);
-    const int32_t far = l_.raise[t & 1];
+    int32_t far = 0;
+    if (SUM) far = l_.raise[t & 1];
+    const bool scoring = SCORE && scores_here();
+    x8 col[AHEAD_V], w[QT][2];
+    if (scoring) {
+      const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE, th);
+      x8 row[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
+      for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
+      acc = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < QT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        pin(acc[i]);
-        acc[i] = Mma<T>::mul(row[k % AHEAD], q[i][k], acc[i]);
+      for (int k = 0; k < KSTEPS; ++k) {
+        pin(acc);
+        acc = Mma<T>::mul(row[k % AHEAD], q[k], acc);
+        pin(acc);
+        if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
+        if (FETCH && k == 1) real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
+        if (FETCH && k >= 2 && k <= 2 + 2 * OWN && k % 2 == 0) f.load((k - 2) / 2);
       }
-      pin(acc[0]);
-      if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
-      else if (k + AHEAD - KSTEPS < AHEAD_V) col[k + AHEAD - KSTEPS] = cols.read((k + AHEAD - KSTEPS) >> 1, (k + AHEAD - KSTEPS) & 1);
-      else if (k >= KSTEPS - 2) {
+    } else if (FETCH) {
+      real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
 #pragma unroll
-        for (int i = 0; i < QT; ++i) w[i][k - (KSTEPS - 2)] = cols.weights(i, k - (KSTEPS - 2));
-      }
-      if (FETCH && k == 1) real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
-      if (FETCH && k >= 2 && k < 2 + LOADS) f.load(k - 2);
+      for (int i = 0; i <= OWN; ++i) f.load(i);
     }
-    if (__builtin_amdgcn_readfirstlane(far) == t + 1) {
-      raise(l_, t);
+    if (SUM) {
+      if (__builtin_amdgcn_readfirstlane(far) == t + 1) raise(l_, t);
+      sum += tile_sum;
 #pragma unroll
       for (int i = 0; i < QT; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) w[i][k] = cols.weights(i, k);
-    }
 #pragma unroll
-    for (int i = 0; i < QT; ++i) sum[i] += tile_sum[i];
-    float e[QT][4];
+      for (int u = 0; u < AHEAD_V; ++u) col[u] = cols.read(u >> 1, u & 1);
+    }
+    if (scoring) finish(scale2, real);
+    float e[4];
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        pin(o[i][u >> 1]);
-        o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD_V], w[i][u & 1], o[i][u >> 1]);
-      }
-      pin(o[0][u >> 1]);
-      if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = cols.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
-      if (u == 0) finish(scale2, real);
-      if (u >= 1 && u <= 4) {
+      if (SUM) {
 #pragma unroll
         for (int i = 0; i < QT; ++i) {
-          e[i][u - 1] = exp2_(s[i][u - 1] - m[i]);
-          asm volatile("" : "+v"(e[i][u - 1]));
+          pin(o[i][u >> 1]);
+          o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD_V], w[i][u & 1], o[i][u >> 1]);
         }
+        pin(o[0][u >> 1]);
+        if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = cols.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
       }
-      if (u == 5) {
-#pragma unroll
-        for (int i = 0; i < QT; ++i) put(lds, t + 1, i, v4f{e[i][0], e[i][1], e[i][2], e[i][3]});
-      }
+      if (scoring) e[u] = exp2_(s[u] - m);
     }
-    if (far_above() && lane_id() == 0) l_.raise[(t + 1) & 1] = t + 2;
+    if (scoring) {
+      put(lds, t + 1, v4f{e[0], e[1], e[2], e[3]});
+      if (__ballot(top() > m + SLACK) && lane_id() == 0) l_.raise[(t + 1) & 1] = t + 2;
+    }
   }
 };
+static_assert(COLS / 16 == 4, "an exponential for each product of the sum");
 
 template <typename T, int QT, bool WIDE>
 ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
@@ -388,15 +343,14 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   const int l = lane_id(), j = l & 15, g = l >> 4;
   Waves<T, QT, WIDE> a;
   a.wv = wv;
-  a.qb = (wv >> 1) * 16 * QT;
+  a.qb = (wv >> 1) * 16;
   a.th = wv & 1;
   // The queries' rows go to registers by way of LDS, to the stages that the first two tiles of tokens do not
   // need: read by the waves themselves they were four pieces of a row a load, a line each.
   constexpr int Q_STAGE = STAGES - QT;
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    const int64_t qi = min(w.q0 + 32 * i + wv * (TILE / WAVES) + (l & 7), w.q1 - 1), r = qi / x.a.n_heads;
-    load_rows(reinterpret_cast<uint64_t>(x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head), lds.stage + (Q_STAGE + i) * STAGE, wv * (TILE / WAVES));
+  if (wv < 4 * QT) {
+    const int64_t qi = min(w.q0 + 8 * wv + (l & 7), w.q1 - 1), r = qi / x.a.n_heads;
+    load_rows(reinterpret_cast<uint64_t>(x.a.q + r * x.a.q_row + (qi - r * x.a.n_heads) * x.a.q_head), lds.stage + (Q_STAGE + (wv >> 2)) * STAGE, 8 * (wv & 3));
   }
   if (threadIdx.x < 64) lds.m[threadIdx.x] = NO_SCORE;
   if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
@@ -413,45 +367,44 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
     f.look(lds.rows + t * TILE, wv);
     real[t] = f.prepare(x, lds.stage + t * STAGE);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) f.load(i);
+    for (int i = 0; i <= OWN; ++i) f.load(i);
   };
   first(0);
   first(1);
   // A negative scale goes into the queries' signs, no scale makes them 0: a masked product then stays at -infinity.
   const uint32_t flip = x.a.scale2 < 0.f ? 0x80008000u : 0u, keep = x.a.scale2 == 0.f ? 0u : ~0u;
   const float scale2 = x.a.scale2 == 0.f ? 1.f : fabsf(x.a.scale2);
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    const int at = a.qb + 16 * i;
-    const auto rows = a.rows_of(lds.stage + (Q_STAGE + (at >> 5)) * STAGE, (at >> 4) & 1);
+  if (a.scores_here()) {
+    const auto rows = a.rows_of(lds.stage + (Q_STAGE + (a.qb >> 5)) * STAGE, (a.qb >> 4) & 1);
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k) {
       const u32x4 v = __builtin_bit_cast(u32x4, rows.read(k));
-      a.q[i][k] = __builtin_bit_cast(typename Mma<T>::x8, (v & keep) ^ flip);
+      a.q[k] = __builtin_bit_cast(typename Mma<T>::x8, (v & keep) ^ flip);
     }
-    a.m[i] = NO_SCORE;
-    a.sum[i] = 0.f;
+  }
+  a.m = NO_SCORE;
+  a.sum = a.tile_sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
 #pragma unroll
     for (int c = 0; c < COLS / 32; ++c) a.o[i][c] = v16f{};
-  }
   meet();
   first(2);
   // The tiles but the `later` youngest of this wave's loads are in LDS, rows that are no token's made zeros, and so are
   // the other waves'; the tile that is needed next is `t`, its tokens `have`.
   const auto arrived = [&](int later, int t, uint32_t have) {
     asm volatile("" ::: "memory");
-    if (later >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * LOADS));
-    else if (later == 1) __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));
-    else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    if (later == 0) __builtin_amdgcn_s_waitcnt(vmcnt(0));
+    else if (wv < 4) later > 1 ? __builtin_amdgcn_s_waitcnt(vmcnt(2 * OWN + 2)) : __builtin_amdgcn_s_waitcnt(vmcnt(OWN + 1));
+    else later > 1 ? __builtin_amdgcn_s_waitcnt(vmcnt(2 * OWN)) : __builtin_amdgcn_s_waitcnt(vmcnt(OWN));
     asm volatile("" ::: "memory");
     zero(lds.stage + t % STAGES * STAGE, have, wv);
     meet();
   };
   if (n > 0) {
     arrived(min(n - 1, 2), 0, real[0]);
-    a.scores(lds.stage, scale2, real[0]);
-    a.weigh(lds.stage, 0);
-    if (a.far_above() && l == 0) lds.raise[0] = 1;
+    uint32_t none;
+    a.template step<true, false, false>(x, lds, -1, scale2, real[0], nullptr, none);
     // A step begins when tile t + 1 and the weights of tile t are there for all, and every wave is done with tile t - 1.
     int t = 0;
     for (; t + 3 < n; ++t) {
@@ -463,28 +416,24 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
       }
       const uint32_t have = real[1];
       real[1] = real[2];
-      a.template step<true>(x, lds, t, scale2, have, lds.rows + in * TILE, real[2]);
+      a.template step<true, true, true>(x, lds, t, scale2, have, lds.rows + in * TILE, real[2]);
     }
     for (; t + 1 < n; ++t) {
       arrived(t + 2 < n ? 1 : 0, t + 1, real[1]);
       const uint32_t have = real[1];
       real[1] = real[2];
-      a.template step<false>(x, lds, t, scale2, have, nullptr, real[2]);
+      a.template step<true, true, false>(x, lds, t, scale2, have, nullptr, none);
     }
     meet();
-    if (lds.raise[t & 1] == t + 1) a.raise(lds, t);
-#pragma unroll
-    for (int i = 0; i < QT; ++i) a.sum[i] += a.tile_sum[i];
-    a.add(lds.stage, t);
+    a.template step<false, true, false>(x, lds, t, scale2, 0, nullptr, none);
   }
   // The sums of a query: four lane groups, two waves.
   meet();
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    float s = a.sum[i];
+  if (a.scores_here()) {
+    float s = a.sum;
     s += __shfl_xor(s, 16, 64);
     s += __shfl_xor(s, 32, 64);
-    if (g == 0) lds.top[a.th][a.qb + 16 * i + j] = s;
+    if (g == 0) lds.top[a.th][a.qb + j] = s;
   }
   meet();
   // Results by way of LDS, a query's row after the other, so that a store writes whole lines.
@@ -595,7 +544,7 @@ ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
 }
 
 template <typename T, int QT, bool WIDE>
-__global__ __launch_bounds__(WAVES * 64, 1) void attention_kernel(AttArgs x) {
+__global__ __launch_bounds__(WAVES * 64) void attention_kernel(AttArgs x) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   Work w;
   const bool any = x.n_groups > 0 ? prefix_work<QT>(x, w) : rows_work<QT>(x, w);
