@@ -522,16 +522,24 @@ template <int QT>
 ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
   const int32_t c = blockIdx.x % x.n_chunks;
   uint32_t tile = blockIdx.x / x.n_chunks;
-  int32_t gi = 0, r0 = 0, r1 = 0;
-  for (; gi < x.n_groups; ++gi) {
-    r0 = clamp_row(x.group_begin[gi], x.a.n_rows);
-    r1 = clamp_row(x.group_begin[gi + 1], x.a.n_rows);
-    if (r1 < r0) r1 = r0;
-    const uint32_t has = static_cast<uint32_t>((static_cast<int64_t>(r1 - r0) * x.a.n_heads + 32 * QT - 1) / (32 * QT));
-    if (tile < has) break;
-    tile -= has;
+  int32_t gi = -1, r0 = 0, r1 = 0;
+  for (int32_t g0 = 0; g0 < x.n_groups; g0 += 64) {        // 64 groups at a time
+    const int32_t g = min(g0 + lane_id(), x.n_groups - 1);
+    const int32_t a = clamp_row(x.group_begin[g], x.a.n_rows), b = max(a, clamp_row(x.group_begin[g + 1], x.a.n_rows));
+    const uint32_t has = g0 + lane_id() < x.n_groups ? static_cast<uint32_t>((static_cast<int64_t>(b - a) * x.a.n_heads + 32 * QT - 1) / (32 * QT)) : 0u;
+    const uint32_t upto = wave_incl_scan(has);
+    const uint64_t in = __ballot(tile < upto);
+    if (in) {
+      const int at = __ffsll(static_cast<unsigned long long>(in)) - 1;
+      gi = g0 + at;
+      r0 = __builtin_amdgcn_readlane(a, at);
+      r1 = __builtin_amdgcn_readlane(b, at);
+      tile -= static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto - has), at));
+      break;
+    }
+    tile -= static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), 63));
   }
-  if (gi == x.n_groups) return false;
+  if (gi < 0) return false;
   w.src = Tokens{nullptr, x.prefix_table + static_cast<int64_t>(gi) * x.prefix_pages, x.prefix_len[gi], 0, x.a.pshift, x.prefix_pages, x.a.n_kv};
   w.t0 = c * x.chunk;
   w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.chunk, x.a.n_tok), w.src.limit));
@@ -563,40 +571,98 @@ struct JoinArgs {
   int32_t n_groups, prefix_chunk, max_prefix, prefix_parts, own_chunk, max_own;
 };
 
-// One wave per query, 8 columns a lane.
-template <typename T>
+// Group of row r: the first g with group_begin[g] <= r < group_begin[g + 1], 64 groups at a time; -1: none.
+ECHO_DEV int32_t group_of(const int32_t *__restrict__ begin, int32_t n_groups, int32_t r) {
+  for (int32_t g0 = 0; g0 < n_groups; g0 += 64) {
+    const int32_t g = min(g0 + lane_id(), n_groups - 1);
+    const uint64_t in = __ballot(begin[g] <= r && r < begin[g + 1]);
+    if (in) return min(g0 + __ffsll(static_cast<unsigned long long>(in)) - 1, n_groups - 1);
+  }
+  return -1;
+}
+
+// out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the largest m_p.  W waves take a query's parts in turn, 8
+// columns a lane: as many as a workgroup has where there are few queries.  Eight parts are on their way at
+// once, the first ones while the parts' maxima are.
+template <typename T, int W>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs x) {
-  const int64_t qi = blockIdx.x * 4ll + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  __shared__ float lds[W > 1 ? W : 1][W > 1 ? VALUES + 4 : 1];
+  const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), l = lane_id();
+  const int64_t qi = W > 1 ? static_cast<int64_t>(blockIdx.x) : blockIdx.x * 4ll + wv;
   if (qi >= static_cast<int64_t>(x.n_rows) * x.n_heads) return;
-  const int32_t r = static_cast<int32_t>(qi / x.n_heads), l = lane_id();
+  const int32_t r = static_cast<int32_t>(qi / x.n_heads);
   int32_t n0 = x.parts, skip = 0, n1 = 0;                  // parts [0, n0) and [skip, skip + n1)
   if (x.own_chunk) {
-    n0 = 0;
-    for (int32_t gi = 0; gi < x.n_groups; ++gi) {
-      const int32_t b = clamp_row(x.group_begin[gi], x.n_rows), e = clamp_row(x.group_begin[gi + 1], x.n_rows);
-      if (r >= b && r < e) {
-        n0 = (max(0, min(x.prefix_len[gi], x.max_prefix)) + x.prefix_chunk - 1) / x.prefix_chunk;
-        break;
-      }
-    }
+    const int32_t gi = group_of(x.group_begin, x.n_groups, r);
+    n0 = gi < 0 ? 0 : (max(0, min(x.prefix_len[gi], x.max_prefix)) + x.prefix_chunk - 1) / x.prefix_chunk;
     skip = x.prefix_parts;
     n1 = (max(0, min(x.len[r], x.max_own)) + x.own_chunk - 1) / x.own_chunk;
   }
   const int64_t p0 = qi * x.parts;
+  const int32_t first = W > 1 ? wv : 0, n = (n0 + n1 - first + W - 1) / W;       // this wave's parts: first, first + W, ..
+  const auto part = [&](int32_t i) { const int32_t at = first + i * W; return p0 + (at < n0 ? at : skip + at - n0); };
   float m = NO_SCORE, sum = 0.f, o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int32_t i = 0; i < n0 + n1; ++i) {
-    const int64_t p = p0 + (i < n0 ? i : skip + i - n0);
-    const float pm = x.ml[2 * p], ps = x.ml[2 * p + 1];
-    const float top = fmaxf(m, pm), was = exp2_(m - top), is = exp2_(pm - top);
-    const v4f a = *reinterpret_cast<const v4f *>(x.part + p * VALUES + 8 * l), b = *reinterpret_cast<const v4f *>(x.part + p * VALUES + 8 * l + 4);
-    sum = sum * was + ps * is;
+  for (int32_t i0 = 0; i0 < n; i0 += 64) {
+    const int32_t some = min(n - i0, 64);
+    const int64_t mine = part(i0 + min(l, some - 1));
+    const float pm = x.ml[2 * mine], ps = x.ml[2 * mine + 1];
+    v4f v[8][2];
+    const auto load = [&](int32_t i) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float *at = x.part + part(i0 + min(i + u, some - 1)) * VALUES + 8 * l;
+        v[u][0] = *reinterpret_cast<const v4f *>(at);
+        v[u][1] = *reinterpret_cast<const v4f *>(at + 4);
+      }
+    };
+    load(0);
+    float top = fmaxf(m, pm);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const float was = exp2_(m - top), scale = l < some ? exp2_(pm - top) : 0.f;
+    float add = scale == 0.f ? 0.f : ps * scale;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) add += __shfl_xor(add, d, 64);
+    sum = sum * was + add;
     m = top;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      o[v] = o[v] * was + a[v] * is;
-      o[4 + v] = o[4 + v] * was + b[v] * is;
+    for (int c = 0; c < 8; ++c) o[c] *= was;
+    for (int32_t i = 0; i < some; i += 8) {
+      if (i) load(i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (i + u >= some) break;                          // the same for the whole wave
+        const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), i + u));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] = fmaf(v[u][c >> 2][c & 3], f, o[c]);
+      }
+    }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int c = 0; c < 8; c += 4) *reinterpret_cast<v4f *>(&lds[wv][8 * l + c]) = v4f{o[c], o[c + 1], o[c + 2], o[c + 3]};
+    if (l == 0) {
+      lds[wv][VALUES] = m;
+      lds[wv][VALUES + 1] = sum;
+    }
+    __syncthreads();
+    if (wv) return;
+    float top = m;
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, lds[w][VALUES]);
+    const float mine = exp2_(m - top);
+    sum *= mine;
+    m = top;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] *= mine;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float f = exp2_(lds[w][VALUES] - top);
+      sum = fmaf(lds[w][VALUES + 1], f, sum);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] = fmaf(lds[w][8 * l + c], f, o[c]);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -672,7 +738,8 @@ int launch_prefix(const AttArgs &x, int type, const PrefixPlan &p, hipStream_t s
 template <typename T>
 int launch_join(const JoinArgs &j, hipStream_t st) {
   const int64_t q = static_cast<int64_t>(j.n_rows) * j.n_heads;
-  join_kernel<T><<<static_cast<uint32_t>((q + 3) / 4), 256, 0, st>>>(j);
+  if (q <= 1024 && j.parts > 8) join_kernel<T, 4><<<static_cast<uint32_t>(q), 256, 0, st>>>(j);
+  else join_kernel<T, 1><<<static_cast<uint32_t>((q + 3) / 4), 256, 0, st>>>(j);
   return check_launch("attention join");
 }
 
