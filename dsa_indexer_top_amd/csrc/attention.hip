@@ -3,17 +3,17 @@
 //   s_t = scale * q . row_t,   out = sum_t softmax(s)_t row_t[0 .. 512),   lse = log sum_t exp s_t.
 //
 // A workgroup takes 32 QT queries that share their tokens (heads of one row, or of the rows behind one
-// prefix) and a chunk of those tokens, in tiles of 32.  Its four waves:
+// prefix) and a chunk of those tokens, in tiles of 32.  Four of its eight waves score, four add up, one of each on a SIMD:
 //   scores   wave w multiplies 16 of the tile's tokens (w % 2) with 16 QT of the queries (w / 2), whose 576 values
 //            stay in registers; the rows come from LDS.
 //   softmax  base 2, relative to a maximum per query that all waves know.  It is raised only when a score exceeds
 //            it by 2^8: weights up to 2^8 are as exact as those up to 1, and neither the waves' maxima have to be
 //            exchanged nor the sums multiplied but then.  The weights go to LDS.
-//   sum      wave w adds up columns 128 w .. 128 w + 127 of all queries over all 32 tokens: the weights from
+//   sum      wave 4 + w adds up columns 128 w .. 128 w + 127 of all queries over all 32 tokens: the weights from
 //            LDS, the rows' columns from LDS through transposing reads.
-// A wave multiplies the scores of tile t + 1 while the weights of tile t are summed, so one barrier a tile
-// is enough and the vector unit's exponentials run beside the matrix core.  Rows go from the cache straight to
-// LDS, two to three tiles (74 to 110 KB) ahead.
+// Tile t + 1 is scored while tile t is added up, so one barrier a tile is enough, and where one wave of a SIMD computes
+// exponentials or waits for LDS the other has products.  Rows go from the cache straight to LDS, two to
+// three tiles (74 to 110 KB) ahead, loaded by the adding waves, which have less to do.
 //
 // Weights are rounded to the cache's type for the product, as the matrix core takes them (off by half a
 // step of the type each, which in a sum of many is what the result's own rounding is); scores, sums,
@@ -27,10 +27,9 @@
 
 namespace echo {
 
-constexpr int WAVES = 8, TILE = 32, STAGES = 4;            // tokens of a tile, tiles in LDS
-constexpr int KSTEPS = LATENT / 32, COLS = VALUES / WAVES; // products of a score, columns of a wave
-constexpr int OWN = TILE / WAVES;                          // a wave's rows of a tile; the first four waves also load
-                                                           // the last 64 values of 8 rows each
+constexpr int WAVES = 8, ADD = 4, TILE = 32, STAGES = 4;   // waves, those that add up; tokens of a tile, tiles in LDS
+constexpr int KSTEPS = LATENT / 32, COLS = VALUES / ADD;   // products of a score, columns of a wave
+constexpr int OWN = TILE / ADD, LOADS = OWN + 1;           // rows of a tile that an adding wave loads, its loads
 constexpr int BATCH = 1536;                                // tokens whose rows are looked up at once
 constexpr float SLACK = 8.f;
 
@@ -52,9 +51,10 @@ struct AttArgs {
   float *lse;
   float *part, *part_ml;         // [query, parts, 512], [query, parts, 2]
   int32_t chunk, n_chunks, parts, first_part;
-  // groups of rows that share a prefix (echo_prefix_attention)
+  // groups of rows that share a prefix (echo_prefix_attention): the first workgroups
   const int32_t *group_begin, *prefix_len, *prefix_table;
-  int32_t n_groups, prefix_pages;
+  int32_t n_groups, prefix_pages, max_prefix, prefix_chunk, prefix_chunks;
+  uint32_t prefix_blocks;
 };
 
 // Queries [q0, q1) (row * n_heads + head) over tokens [t0, t1) of `src`; part < 0: the only chunk.
@@ -68,16 +68,17 @@ struct Lds {
   uint8_t stage[STAGES * STAGE];
   float m[64], top[2][64];       // maxima; a tile's, or at the end the sums
   int32_t raise[2];              // t + 1: tile t (by t % 2) has a score far above its maximum
+  uint32_t real[STAGES];         // which tokens of a tile there are
   int32_t rows[BATCH];           // cache rows of a batch of tokens, -1: none
 };
 static_assert(sizeof(Lds) <= 160 * 1024, "a workgroup's LDS");
 
-// Cache rows of the chunk's tokens from `first` on, up to a batch of them.  Entries and pages are loaded
+// Cache rows of the chunk's tokens from `first` on, up to a batch of them, by the adding waves.  Entries and pages are loaded
 // for a batch at once: loaded tile by tile, their waits held up the rows on their way (the same counter).
 ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) {
   const int32_t t0 = w.t0 + first, count = min(w.t1 - t0, BATCH);
-  constexpr int PER = BATCH / (WAVES * 64);
-  const int tid = threadIdx.x;
+  constexpr int N = ADD * 64, PER = BATCH / N;
+  const int tid = threadIdx.x & (N - 1);
   int32_t e[PER], page[PER];
   int64_t pos[PER];
 #pragma unroll
@@ -85,10 +86,10 @@ ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) 
   if (w.src.list) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * WAVES * 64 < count) e[i] = w.src.list[(t0 + min(i * WAVES * 64 + tid, count - 1)) >> w.src.shift];
+      if (i * N < count) e[i] = w.src.list[(t0 + min(i * N + tid, count - 1)) >> w.src.shift];
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) pos[i] = i * WAVES * 64 + tid < count ? w.src.position(t0 + i * WAVES * 64 + tid, e[i]) : -1;
+  for (int i = 0; i < PER; ++i) pos[i] = i * N + tid < count ? w.src.position(t0 + i * N + tid, e[i]) : -1;
   if (w.src.table && w.src.max_pages > 0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -102,7 +103,7 @@ ECHO_DEV void look_up(const Work &w, int32_t first, int32_t *__restrict__ rows) 
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (i * WAVES * 64 < count) rows[i * WAVES * 64 + tid] = w.src.row(pos[i], page[i]);
+    if (i * N < count) rows[i * N + tid] = w.src.row(pos[i], page[i]);
 }
 
 // 8 rows on their way to LDS, 1024 bytes and then the last 128 bytes of each; lane i (and every 8th after it) has the
@@ -120,75 +121,74 @@ ECHO_DEV void load_rows(uint64_t at, uint8_t *__restrict__ stage, int r0) {
                                    (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
 }
 
-// The wave's rows of a tile on their way to LDS, a part at a time; the tile's cache rows are at `rows`.  Through a
+// An adding wave's 8 rows of a tile on their way to LDS, a part at a time; the tile's cache rows are at `rows`.  Through a
 // buffer descriptor: one lane's offset and the place in LDS are all that a row takes, and unlike a global
 // load it does not make the compiler wait for every LDS read under way.  A cache of 4 GB and more (WIDE) adds
 // the upper half of an offset to the descriptor's base.  Where there is no row it is the cache's first; zero() takes it out.
 template <bool WIDE>
 struct Fetch {
   int32_t row, rope_row;
-  int lo, hi, wv;
+  int lo, hi, r0;
   uint64_t rope;
   const void *kv;
-  uint8_t *stage;
-  ECHO_DEV void look(const int32_t *__restrict__ rows, int wave) {
-    wv = wave;
+  ECHO_DEV void look(const int32_t *__restrict__ rows, int wa) {
+    r0 = wa * OWN;
     row = rows[lane_id() & 31];
-    rope_row = rows[8 * (wv & 3) + (lane_id() >> 3)];
+    rope_row = rows[r0 + (lane_id() >> 3)];
   }
   // Returns which of the tile's 32 tokens there are.
-  ECHO_DEV uint32_t prepare(const AttArgs &x, uint8_t *to) {
+  ECHO_DEV uint32_t prepare(const AttArgs &x) {
     const int l = lane_id();
     const uint32_t stride = static_cast<uint32_t>(x.a.kv_stride * 2);
     kv = x.a.kv;
     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * stride;
     lo = static_cast<int>(at);
     hi = static_cast<int>(at >> 32);
-    rope = static_cast<uint64_t>(static_cast<uint32_t>(max(rope_row, 0))) * stride + 1024 + (((l & 7) ^ swap_r(8 * (wv & 3) + (l >> 3))) << 4);
-    stage = to;
+    rope = static_cast<uint64_t>(static_cast<uint32_t>(max(rope_row, 0))) * stride + 1024 + (((l & 7) ^ swap_r(r0 + (l >> 3))) << 4);
     return static_cast<uint32_t>(__ballot(row >= 0));
   }
-  ECHO_DEV void load(int i) const {
-    if (i < OWN) {
-      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, OWN * wv + i))) << 32 : 0;
+  ECHO_DEV void load(uint8_t *__restrict__ stage, int i) const {
+    if (i < OWN) {                                         // r0 is a multiple of 4
+      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i))) << 32 : 0;
       const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(reinterpret_cast<uint64_t>(kv) + above), 0, -1, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(OWN * wv) + row_at(i)), 16, lane_id() * 16,
-                                               __builtin_amdgcn_readlane(lo, OWN * wv + i), 0, 0);
-    } else if (wv < 4) {
-      uint8_t *to = stage + ROPE_AT + wv * 1024;
-      if (WIDE) {                                          // eight rows in one load: addresses by lane
-        __builtin_amdgcn_global_load_lds((glb_void *)(static_cast<const uint8_t *>(kv) + rope), (lds_void *)to, 16, 0, 0);
-      } else {
-        const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(kv), 0, -1, 0x00027000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)to, 16, static_cast<uint32_t>(rope), 0, 0, 0);
-      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(r0) + row_at(i)), 16, lane_id() * 16, __builtin_amdgcn_readlane(lo, r0 + i), 0, 0);
+    } else if (WIDE) {                                     // eight rows in one load: addresses by lane
+      __builtin_amdgcn_global_load_lds((glb_void *)(static_cast<const uint8_t *>(kv) + rope), (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
+    } else {
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(kv), 0, -1, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + ROPE_AT + r0 * 128), 16, static_cast<uint32_t>(rope), 0, 0, 0);
     }
   }
 };
 // Rows that this wave has loaded and that are no token's, once they are there: zeros, so that nothing of the cache gets
 // into a sum through a weight of 0.
-ECHO_DEV void zero(uint8_t *__restrict__ stage, uint32_t real, int wv) {
+ECHO_DEV void zero(uint8_t *__restrict__ stage, uint32_t real, int wa) {
   if (real == ~0u) return;                                 // the same for the whole wave
-  const int l = lane_id();
+  const int l = lane_id(), r0 = wa * OWN;
 #pragma unroll
   for (int i = 0; i < OWN; ++i)
-    if (!(real >> (OWN * wv + i) & 1)) *reinterpret_cast<u32x4 *>(stage + row_at(OWN * wv) + row_at(i) + 16 * l) = u32x4{0, 0, 0, 0};
-  if (wv < 4 && !(real >> (8 * wv + (l >> 3)) & 1)) *reinterpret_cast<u32x4 *>(stage + ROPE_AT + wv * 1024 + 16 * l) = u32x4{0, 0, 0, 0};
+    if (!(real >> (r0 + i) & 1)) *reinterpret_cast<u32x4 *>(stage + row_at(r0) + row_at(i) + 16 * l) = u32x4{0, 0, 0, 0};
+  if (!(real >> (r0 + (l >> 3)) & 1)) *reinterpret_cast<u32x4 *>(stage + ROPE_AT + r0 * 128 + 16 * l) = u32x4{0, 0, 0, 0};
 }
 
-template <typename T, int QT, bool WIDE>
-struct Waves {
+// An empty statement that takes and gives accumulation registers: between two of them the compiler copies one
+// group of sums to where it can be multiplied, and holds them all where the matrix core adds them up otherwise.
+// It also keeps its place among the reads of LDS, so that an operand is read as far ahead of its product as is written
+// here; left to itself the compiler reads it right before, and the matrix core waits for LDS.
+ECHO_DEV void pin(v16f &v) { asm volatile("" : "+a"(v)); }
+ECHO_DEV void pin(v4f &v) { asm volatile("" : "+a"(v)); }
+template <typename X8> ECHO_DEV void pin_operand(X8 &v) { asm volatile("" : "+a"(v)); }
+
+template <typename T, int QT>
+struct Scorer {
   typedef typename Mma<T>::x8 x8;
-  x8 q[KSTEPS];                  // 16 queries: lane (j, g) values of query qb + j
-  v4f acc, s;                    // products, and a tile's scores (base 2): tokens 4 g .. 4 g + 3 of the wave's 16
-  float m, sum, tile_sum;
-  v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
-  int wv, qb, th;                // qb: the wave's first query for scores
+  x8 q[QT][KSTEPS];              // 16 QT queries: lane (j, g) values of query qb + 16 i + j
+  v4f acc[QT], s[QT];            // products; those of the tile whose weights were given last: tokens 4 g .. 4 g + 3 of the wave's 16
+  float m[QT], far[QT], sum[QT], tile_sum[QT];             // maxima (base 2), the product from which on they are raised; sums of weights
+  float scale2;
+  int qb, th;
 
-  ECHO_DEV bool scores_here() const { return QT == 2 || wv < 4; }
-
-  // Scores of a tile's tokens: product k of the wave's 16 rows.
-  struct Rows {
+  struct Rows {                  // product k of the wave's 16 rows
     const uint8_t *v, *r;
     int g, swap;
     ECHO_DEV x8 read(int k) const { return k < 16 ? read16<x8>(v + 16 * k) : read16<x8>(r + (((4 * (k - 16) + g) ^ swap) << 4)); }
@@ -197,37 +197,126 @@ struct Waves {
     const int l = lane_id(), j = l & 15, g = l >> 4;
     return Rows{stage + row_at(half * 16 + j) + 256 * g, stage + ROPE_AT + (half * 16 + j) * 128, g, swap_r(j)};
   }
-  // Base 2, and -infinity where there is no token; `real`: the tile's tokens that there are.
-  ECHO_DEV void finish(float scale2, uint32_t real) {
-    const uint32_t mine = real >> (16 * th + 4 * (lane_id() >> 4));
-#pragma unroll
-    for (int v = 0; v < 4; ++v) s[v] = fmaf(acc[v], scale2, mine >> v & 1 ? 0.f : -INFINITY);
+  ECHO_DEV void set(int i, float to) {
+    m[i] = to;
+    far[i] = (to + SLACK) / scale2;
   }
-  ECHO_DEV void put(uint8_t *__restrict__ lds, int t, const v4f &w) {
+  ECHO_DEV void init(const Lds &lds, int q_stage, int wv, float scale) {
+    qb = (wv >> 1) * 16 * QT;
+    th = wv & 1;
+    // A negative scale goes into the queries' signs, no scale makes them 0: a masked product then stays at -infinity.
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u, keep = scale == 0.f ? 0u : ~0u;
+    scale2 = scale == 0.f ? 1.f : fabsf(scale);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      const int at = qb + 16 * i;
+      const Rows r = rows_of(lds.stage + (q_stage + (at >> 5)) * STAGE, (at >> 4) & 1);
+#pragma unroll
+      for (int k = 0; k < KSTEPS; ++k) {
+        q[i][k] = __builtin_bit_cast(x8, (__builtin_bit_cast(u32x4, r.read(k)) & keep) ^ flip);
+        pin_operand(q[i][k]);                              // in accumulation registers, from where products take them as well
+      }
+      set(i, NO_SCORE);
+      sum[i] = tile_sum[i] = 0.f;
+    }
+  }
+  ECHO_DEV void products(const uint8_t *__restrict__ stage) {
+    constexpr int AHEAD = 6;
+    const Rows r = rows_of(stage, th);
+    x8 row[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
+#pragma unroll
+    for (int i = 0; i < QT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        pin(acc[i]);
+        acc[i] = Mma<T>::mul(row[k % AHEAD], q[i][k], acc[i]);
+      }
+      pin(acc[0]);
+      if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
+    }
+  }
+  // Weights of tile t from its products; `real`: its tokens.
+  ECHO_DEV void weigh(Lds &lds, int t) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-    tile_sum = (w[0] + w[1]) + (w[2] + w[3]);
-    *reinterpret_cast<u32x2 *>(lds + weights_at(t, qb + j) + 32 * th + 8 * g) = pack4<T>(w);
-  }
-  ECHO_DEV void weigh(uint8_t *__restrict__ lds, int t) {
-    v4f w;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) w[v] = exp2_(s[v] - m);
-    put(lds, t, w);
+    for (int i = 0; i < QT; ++i) {
+      v4f w;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) w[v] = exp2_(fmaf(s[i][v], scale2, -m[i]));
+      tile_sum[i] = (w[0] + w[1]) + (w[2] + w[3]);
+      *reinterpret_cast<u32x2 *>(lds.stage + weights_at(t, qb + 16 * i + j) + 32 * th + 8 * g) = pack4<T>(w);
+    }
   }
-  // An empty statement that takes and gives accumulation registers: between two of them the compiler copies one
-  // group of sums to where it can be multiplied, and holds them all where the matrix core adds them up otherwise.
-  ECHO_DEV static void pin(v16f &v) { asm volatile("" : "+a"(v)); }
-  ECHO_DEV static void pin(v4f &v) { asm volatile("" : "+a"(v)); }
-  ECHO_DEV float top() const { return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])); }
-  // Every wave: maxima up to those of the tile, sums and weights on the new scale.
+  ECHO_DEV float top(int i) const { return fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3])); }
+  ECHO_DEV void weights(Lds &lds, int t, uint32_t real) {
+#pragma unroll
+    for (int i = 0; i < QT; ++i) s[i] = acc[i];
+    if (real != ~0u) {                                     // the same for the whole wave
+      const uint32_t mine = real >> (16 * th + 4 * (lane_id() >> 4));
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int i = 0; i < QT; ++i) s[i][v] = mine >> v & 1 ? s[i][v] : -INFINITY;
+    }
+    weigh(lds, t);
+    bool above = false;
+#pragma unroll
+    for (int i = 0; i < QT; ++i) above |= top(i) > far[i];
+    if (__ballot(above)) lds.raise[t & 1] = t + 1;         // every lane the same
+  }
+  // Maxima up to those of tile t, whose weights are given anew; with Adder::raise.
   ECHO_DEV void raise(Lds &lds, int t) {
     const int l = lane_id(), j = l & 15, g = l >> 4;
-    if (scores_here()) {
-      float a = top();
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      float a = top(i) * scale2;
       a = fmaxf(a, __shfl_xor(a, 16, 64));
       a = fmaxf(a, __shfl_xor(a, 32, 64));
-      if (g == 0) lds.top[th][qb + j] = a;
+      if (g == 0) lds.top[th][qb + 16 * i + j] = a;
     }
+    meet();
+    float to[QT];
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      const int at = qb + 16 * i + j;
+      to[i] = fmaxf(m[i], fmaxf(lds.top[0][at], lds.top[1][at]));
+      sum[i] *= exp2_(m[i] - to[i]);
+      set(i, to[i]);
+    }
+    meet();
+    if (th == 0 && g == 0)
+#pragma unroll
+      for (int i = 0; i < QT; ++i) lds.m[qb + 16 * i + j] = to[i];
+    weigh(lds, t);
+    meet();
+  }
+  ECHO_DEV void count() {
+#pragma unroll
+    for (int i = 0; i < QT; ++i) sum[i] += tile_sum[i];
+  }
+};
+
+template <typename T, int QT>
+struct Adder {
+  typedef typename Mma<T>::x8 x8;
+  v16f o[QT][COLS / 32];         // lane (j, h): columns 32 c + 8 (v / 4) + 4 h + v % 4 of query 32 i + j
+  int wa;
+
+  // The operands: weights of query 32 i + j and columns 32 c .. of the wave's, tokens 16 k + 8 h .. + 7.
+  const uint8_t *p, *v;
+  ECHO_DEV x8 weights(int i, int k) const { return read16<x8>(p + i * STAGE + 32 * k); }
+  ECHO_DEV x8 cols(int c, int k) const {
+    struct { v4s lo, hi; } e;
+    e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k) + 64 * c));
+    e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k + 4) + 64 * c));
+    return __builtin_bit_cast(x8, e);
+  }
+  ECHO_DEV void raise(const Lds &lds) {
+    const int l = lane_id();
     meet();
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
@@ -237,114 +326,56 @@ struct Waves {
       for (int c = 0; c < COLS / 32; ++c) {
         pin(o[i][c]);
 #pragma unroll
-        for (int v = 0; v < 16; ++v) o[i][c][v] *= less;
+        for (int u = 0; u < 16; ++u) o[i][c][u] *= less;
         pin(o[i][c]);
       }
     }
-    float to = m;
-    if (scores_here()) {
-      to = fmaxf(m, fmaxf(lds.top[0][qb + j], lds.top[1][qb + j]));
-      sum *= exp2_(m - to);
-      m = to;
-    }
     meet();
-    if (scores_here()) {
-      if (th == 0 && g == 0) lds.m[qb + j] = to;
-      weigh(lds.stage, t);
-    }
     meet();
   }
-  // The sum's operands: weights of query 32 i + j and columns 32 c .. of the wave's, tokens 16 k + 8 h .. + 7.
-  struct Cols {
-    const uint8_t *p, *v;
-    ECHO_DEV x8 weights(int i, int k) const { return read16<x8>(p + i * STAGE + 32 * k); }
-    ECHO_DEV x8 read(int c, int k) const {
-      struct { v4s lo, hi; } e;
-      e.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k) + 64 * c));
-      e.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(v + row_at(16 * k + 4) + 64 * c));
-      return __builtin_bit_cast(x8, e);
-    }
-  };
-  ECHO_DEV Cols cols_of(const uint8_t *__restrict__ lds, int t) const {
-    const int l = lane_id(), j = l & 31, h = l >> 5;
-    return Cols{lds + weights_at(t, j) + 16 * h,
-                lds + t % STAGES * STAGE + row_at(8 * h) + ((l & 15) >> 2) * ROW_STEP + wv * (2 * COLS) + 32 * ((l >> 4) & 1) + 8 * (l & 3)};
-  }
-  // Scores and weights of tile t + 1 (SCORE), the sum over tile t (SUM) and, with FETCH, the loads of tile t + 3, whose
-  // tokens go to `real3`.  The order of the reads and products is this one: left to itself the compiler reads each
-  // operand right before its product, and the matrix core waits for LDS.
-  template <bool SCORE, bool SUM, bool FETCH>
-  ECHO_DEV void step(const AttArgs &x, Lds &l_, int t, float scale2, uint32_t real, const int32_t *__restrict__ rows, uint32_t &real3) {
-    constexpr int AHEAD = 4, STEPS = COLS / 16, AHEAD_V = 2;
-    uint8_t *lds = l_.stage;
-    const Cols cols = cols_of(lds, t);
-    Fetch<WIDE> f;
-    if (FETCH) f.look(rows, wv);
-    int32_t far = 0;
-    if (SUM) far = l_.raise[t & 1];
-    const bool scoring = SCORE && scores_here();
-    x8 col[AHEAD_V], w[QT][2];
-    if (scoring) {
-      const Rows r = rows_of(lds + (t + 1) % STAGES * STAGE, th);
-      x8 row[AHEAD];
+  // Adds up the tile in `cur`.  With a fetch the loads of a later tile, to `next`, stand between the products.  (Three
+  // pointers that the compiler may take for different memory: it waits for loads to LDS before reads of the same.)
+  template <bool FETCH, typename F>
+  ECHO_DEV void add(const uint8_t *__restrict__ cur, const uint8_t *__restrict__ weights_of_tile, uint8_t *__restrict__ next, const Lds &lds, int t, const F &f) {
+    constexpr int STEPS = COLS / 16, AHEAD = 4;
+    const int l = lane_id(), h = l >> 5;
+    p = weights_of_tile + 16 * h;
+    v = cur + row_at(8 * h) + ((l & 15) >> 2) * ROW_STEP + wa * (2 * COLS) + 32 * ((l >> 4) & 1) + 8 * (l & 3);
+    const int32_t far = lds.raise[t & 1];
+    x8 col[AHEAD], w[QT][2];
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) row[k] = r.read(k);
-      acc = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < AHEAD; ++u) col[u] = cols(u >> 1, u & 1);
 #pragma unroll
-      for (int k = 0; k < KSTEPS; ++k) {
-        pin(acc);
-        acc = Mma<T>::mul(row[k % AHEAD], q[k], acc);
-        pin(acc);
-        if (k + AHEAD < KSTEPS) row[k % AHEAD] = r.read(k + AHEAD);
-        if (FETCH && k == 1) real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
-        if (FETCH && k >= 2 && k <= 2 + 2 * OWN && k % 2 == 0) f.load((k - 2) / 2);
-      }
-    } else if (FETCH) {
-      real3 = f.prepare(x, lds + (t + 3) % STAGES * STAGE);
+    for (int i = 0; i < QT; ++i)
 #pragma unroll
-      for (int i = 0; i <= OWN; ++i) f.load(i);
-    }
-    if (SUM) {
-      if (__builtin_amdgcn_readfirstlane(far) == t + 1) raise(l_, t);
-      sum += tile_sum;
+      for (int k = 0; k < 2; ++k) w[i][k] = weights(i, k);
+    if (__builtin_amdgcn_readfirstlane(far) == t + 1) {
+      raise(lds);
 #pragma unroll
       for (int i = 0; i < QT; ++i)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) w[i][k] = cols.weights(i, k);
-#pragma unroll
-      for (int u = 0; u < AHEAD_V; ++u) col[u] = cols.read(u >> 1, u & 1);
+        for (int k = 0; k < 2; ++k) w[i][k] = weights(i, k);
     }
-    if (scoring) finish(scale2, real);
-    float e[4];
+    if (FETCH) f.load(next, 0);
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-      if (SUM) {
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          pin(o[i][u >> 1]);
-          o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD_V], w[i][u & 1], o[i][u >> 1]);
-        }
-        pin(o[0][u >> 1]);
-        if (u + AHEAD_V < STEPS) col[u % AHEAD_V] = cols.read((u + AHEAD_V) >> 1, (u + AHEAD_V) & 1);
+      for (int i = 0; i < QT; ++i) {
+        pin(o[i][u >> 1]);
+        o[i][u >> 1] = Mma<T>::mul(col[u % AHEAD], w[i][u & 1], o[i][u >> 1]);
       }
-      if (scoring) e[u] = exp2_(s[u] - m);
-    }
-    if (scoring) {
-      put(lds, t + 1, v4f{e[0], e[1], e[2], e[3]});
-      if (__ballot(top() > m + SLACK) && lane_id() == 0) l_.raise[(t + 1) & 1] = t + 2;
+      pin(o[0][u >> 1]);
+      if (u + AHEAD < STEPS) col[u % AHEAD] = cols((u + AHEAD) >> 1, (u + AHEAD) & 1);
+      if (FETCH) f.load(next, 1 + u);
     }
   }
 };
-static_assert(COLS / 16 == 4, "an exponential for each product of the sum");
+static_assert(COLS / 16 == LOADS - 1, "a load for each product of the sum, one before");
 
 template <typename T, int QT, bool WIDE>
 ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int l = lane_id(), j = l & 15, g = l >> 4;
-  Waves<T, QT, WIDE> a;
-  a.wv = wv;
-  a.qb = (wv >> 1) * 16;
-  a.th = wv & 1;
+  const int l = lane_id();
   // The queries' rows go to registers by way of LDS, to the stages that the first two tiles of tokens do not
   // need: read by the waves themselves they were four pieces of a row a load, a line each.
   constexpr int Q_STAGE = STAGES - QT;
@@ -356,84 +387,102 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   if (threadIdx.x < 2) lds.raise[threadIdx.x] = 0;
   const int n = (w.t1 - w.t0 + TILE - 1) / TILE;
   constexpr int TILES = BATCH / TILE;
-  uint32_t real[3] = {};                                   // of tiles t + 1, t + 2, t + 3
-  if (n > 0) look_up(w, 0, lds.rows);
+  const bool adding = wv >= ADD;
+  if (adding && n > 0) look_up(w, 0, lds.rows);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(vmcnt(0));
   meet();
-  const auto first = [&](int t) {
-    if (t >= n) return;
-    Fetch<WIDE> f;
-    f.look(lds.rows + t * TILE, wv);
-    real[t] = f.prepare(x, lds.stage + t * STAGE);
-#pragma unroll
-    for (int i = 0; i <= OWN; ++i) f.load(i);
-  };
-  first(0);
-  first(1);
-  // A negative scale goes into the queries' signs, no scale makes them 0: a masked product then stays at -infinity.
-  const uint32_t flip = x.a.scale2 < 0.f ? 0x80008000u : 0u, keep = x.a.scale2 == 0.f ? 0u : ~0u;
-  const float scale2 = x.a.scale2 == 0.f ? 1.f : fabsf(x.a.scale2);
-  if (a.scores_here()) {
-    const auto rows = a.rows_of(lds.stage + (Q_STAGE + (a.qb >> 5)) * STAGE, (a.qb >> 4) & 1);
-#pragma unroll
-    for (int k = 0; k < KSTEPS; ++k) {
-      const u32x4 v = __builtin_bit_cast(u32x4, rows.read(k));
-      a.q[k] = __builtin_bit_cast(typename Mma<T>::x8, (v & keep) ^ flip);
-    }
-  }
-  a.m = NO_SCORE;
-  a.sum = a.tile_sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < QT; ++i)
-#pragma unroll
-    for (int c = 0; c < COLS / 32; ++c) a.o[i][c] = v16f{};
-  meet();
-  first(2);
-  // The tiles but the `later` youngest of this wave's loads are in LDS, rows that are no token's made zeros, and so are
-  // the other waves'; the tile that is needed next is `t`, its tokens `have`.
-  const auto arrived = [&](int later, int t, uint32_t have) {
-    asm volatile("" ::: "memory");
-    if (later == 0) __builtin_amdgcn_s_waitcnt(vmcnt(0));
-    else if (wv < 4) later > 1 ? __builtin_amdgcn_s_waitcnt(vmcnt(2 * OWN + 2)) : __builtin_amdgcn_s_waitcnt(vmcnt(OWN + 1));
-    else later > 1 ? __builtin_amdgcn_s_waitcnt(vmcnt(2 * OWN)) : __builtin_amdgcn_s_waitcnt(vmcnt(OWN));
-    asm volatile("" ::: "memory");
-    zero(lds.stage + t % STAGES * STAGE, have, wv);
+  // Both sides go through the same barriers: [queries taken] [tile 0] and, for every tile t, [tile t + 1 and the weights of
+  // tile t are there, and tile t - 1 is done with], where a score is far above its maximum three more, and one more where a
+  // batch of rows is looked up.
+  v16f o[QT][COLS / 32];
+  if (!adding) {
+    Scorer<T, QT> a;
+    a.init(lds, Q_STAGE, wv, x.a.scale2);
     meet();
-  };
-  if (n > 0) {
-    arrived(min(n - 1, 2), 0, real[0]);
-    uint32_t none;
-    a.template step<true, false, false>(x, lds, -1, scale2, real[0], nullptr, none);
-    // A step begins when tile t + 1 and the weights of tile t are there for all, and every wave is done with tile t - 1.
-    int t = 0;
-    for (; t + 3 < n; ++t) {
-      arrived(1, t + 1, real[1]);
-      const int in = (t + 3) % TILES;
-      if (in == 0) {                                       // every wave has taken the last batch's rows
-        look_up(w, (t + 3) * TILE, lds.rows);
+    if (n > 0) {
+      meet();
+      a.products(lds.stage);
+      a.weights(lds, 0, lds.real[0]);
+      for (int t = 0; t < n; ++t) {
         meet();
+        if (t + 3 < n && (t + 3) % TILES == 0) meet();
+        const int32_t far = lds.raise[t & 1];
+        const uint32_t have = lds.real[(t + 1) % STAGES];
+        if (t + 1 < n) a.products(lds.stage + (t + 1) % STAGES * STAGE);
+        if (__builtin_amdgcn_readfirstlane(far) == t + 1) a.raise(lds, t);
+        a.count();
+        if (t + 1 < n) a.weights(lds, t + 1, static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(have))));
       }
-      const uint32_t have = real[1];
-      real[1] = real[2];
-      a.template step<true, true, true>(x, lds, t, scale2, have, lds.rows + in * TILE, real[2]);
-    }
-    for (; t + 1 < n; ++t) {
-      arrived(t + 2 < n ? 1 : 0, t + 1, real[1]);
-      const uint32_t have = real[1];
-      real[1] = real[2];
-      a.template step<true, true, false>(x, lds, t, scale2, have, nullptr, none);
     }
     meet();
-    a.template step<false, true, false>(x, lds, t, scale2, 0, nullptr, none);
-  }
-  // The sums of a query: four lane groups, two waves.
-  meet();
-  if (a.scores_here()) {
-    float s = a.sum;
-    s += __shfl_xor(s, 16, 64);
-    s += __shfl_xor(s, 32, 64);
-    if (g == 0) lds.top[a.th][a.qb + j] = s;
+    // The sums of a query: four lane groups, two waves.
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      float s = a.sum[i];
+      s += __shfl_xor(s, 16, 64);
+      s += __shfl_xor(s, 32, 64);
+      if (l < 16) lds.top[a.th][a.qb + 16 * i + l] = s;
+    }
+  } else {
+    Adder<T, QT> a;
+    a.wa = wv - ADD;
+#pragma unroll
+    for (int i = 0; i < QT; ++i)
+#pragma unroll
+      for (int c = 0; c < COLS / 32; ++c) a.o[i][c] = v16f{};
+    uint32_t real[3] = {};                                 // of tiles t + 1, t + 2, t + 3
+    Fetch<WIDE> f;
+    const auto tell = [&](int t, uint32_t have) { if (a.wa == 0) lds.real[t % STAGES] = have; };
+    const auto first = [&](int t) {
+      if (t >= n) return;
+      f.look(lds.rows + t * TILE, a.wa);
+      real[t] = f.prepare(x);
+      tell(t, real[t]);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) f.load(lds.stage + t * STAGE, i);
+    };
+    first(0);
+    first(1);
+    meet();
+    first(2);
+    // The tiles but the `later` youngest of this wave's loads are in LDS, of tile t rows that are no token's made zeros.
+    const auto arrived = [&](int later, int t, uint32_t have) {
+      asm volatile("" ::: "memory");
+      if (later > 1) __builtin_amdgcn_s_waitcnt(vmcnt(2 * LOADS));
+      else if (later == 1) __builtin_amdgcn_s_waitcnt(vmcnt(LOADS));
+      else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+      asm volatile("" ::: "memory");
+      zero(lds.stage + t % STAGES * STAGE, have, a.wa);
+      meet();
+    };
+    if (n > 0) {
+      arrived(min(n - 1, 2), 0, real[0]);
+      int t = 0;
+      for (; t + 3 < n; ++t) {
+        arrived(1, t + 1, real[1]);
+        const int in = (t + 3) % TILES;
+        if (in == 0) {                                     // every wave has taken the last batch's rows
+          look_up(w, (t + 3) * TILE, lds.rows);
+          meet();
+        }
+        f.look(lds.rows + in * TILE, a.wa);
+        real[1] = real[2];
+        real[2] = f.prepare(x);
+        tell(t + 3, real[2]);
+        a.template add<true>(lds.stage + t % STAGES * STAGE, lds.stage + weights_at(t, l & 31), lds.stage + (t + 3) % STAGES * STAGE, lds, t, f);
+      }
+      for (; t < n; ++t) {
+        arrived(t + 2 < n ? 1 : 0, t + 1, t + 1 < n ? real[1] : ~0u);
+        real[1] = real[2];
+        a.template add<false>(lds.stage + t % STAGES * STAGE, lds.stage + weights_at(t, l & 31), nullptr, lds, t, f);
+      }
+    }
+    meet();
+#pragma unroll
+    for (int i = 0; i < QT; ++i)
+#pragma unroll
+      for (int c = 0; c < COLS / 32; ++c) o[i][c] = a.o[i][c];
   }
   meet();
   // Results by way of LDS, a query's row after the other, so that a store writes whole lines.
@@ -441,20 +490,22 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
   const int h = l >> 5;
   constexpr int OUT_ROW = VALUES * static_cast<int>(sizeof(T)) + 16, PART_ROW = VALUES * 4 + 16;
   static_assert(64 * PART_ROW <= STAGES * STAGE, "results fit the stages");
+  if (adding) {
 #pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    const int at = 32 * i + (l & 31);
-    const float sum = lds.top[0][at] + lds.top[1][at];
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int i = 0; i < QT; ++i) {
+      const int at = 32 * i + (l & 31);
+      const float sum = lds.top[0][at] + lds.top[1][at];
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int c = 0; c < COLS / 32; ++c) {
-      a.pin(a.o[i][c]);
+      for (int c = 0; c < COLS / 32; ++c) {
+        pin(o[i][c]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const v4f v = {a.o[i][c][4 * b], a.o[i][c][4 * b + 1], a.o[i][c][4 * b + 2], a.o[i][c][4 * b + 3]};
-        const int col = wv * COLS + 32 * c + 8 * b + 4 * h;
-        if (whole) *reinterpret_cast<u32x2 *>(lds.stage + at * OUT_ROW + col * sizeof(T)) = pack4<T>(v * inv);
-        else *reinterpret_cast<v4f *>(lds.stage + at * PART_ROW + col * 4) = v;
+        for (int b = 0; b < 4; ++b) {
+          const v4f v = {o[i][c][4 * b], o[i][c][4 * b + 1], o[i][c][4 * b + 2], o[i][c][4 * b + 3]};
+          const int col = (wv - ADD) * COLS + 32 * c + 8 * b + 4 * h;
+          if (whole) *reinterpret_cast<u32x2 *>(lds.stage + at * OUT_ROW + col * sizeof(T)) = pack4<T>(v * inv);
+          else *reinterpret_cast<v4f *>(lds.stage + at * PART_ROW + col * 4) = v;
+        }
       }
     }
   }
@@ -498,7 +549,7 @@ ECHO_DEV int32_t clamp_row(int32_t r, int32_t n) { return r < 0 ? 0 : r > n ? n 
 template <int QT>
 ECHO_DEV bool rows_work(const AttArgs &x, Work &w) {
   const uint32_t head_tiles = (x.a.n_heads + 32 * QT - 1) / (32 * QT), units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(x.n_chunks);
-  const uint32_t eight = blockIdx.x / (8 * head_tiles), in = blockIdx.x - eight * 8 * head_tiles;
+  const uint32_t id = blockIdx.x - x.prefix_blocks, eight = id / (8 * head_tiles), in = id - eight * 8 * head_tiles;
   const uint32_t u = eight * 8 + (in & 7), ht = in >> 3;
   if (u >= units) return false;
   const int32_t r = static_cast<int32_t>(u / x.n_chunks), c = static_cast<int32_t>(u - static_cast<uint32_t>(r) * x.n_chunks);
@@ -517,11 +568,14 @@ ECHO_DEV bool rows_work(const AttArgs &x, Work &w) {
   return true;
 }
 
-// The prefixes: a tile of the groups' queries in order, a chunk.
+// The prefixes: a tile of the groups' queries in order, a chunk.  With eight chunks and more a chunk's workgroups are
+// a multiple of 8 apart, on one XCD, so that its L2 has the chunk's rows for all of them.
+__host__ __device__ constexpr int32_t chunk_step(int32_t chunks) { return chunks < 8 ? chunks : (chunks + 7) & ~7; }
 template <int QT>
 ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
-  const int32_t c = blockIdx.x % x.n_chunks;
-  uint32_t tile = blockIdx.x / x.n_chunks;
+  const int32_t step = chunk_step(x.prefix_chunks), c = blockIdx.x % step;
+  if (c >= x.prefix_chunks) return false;
+  uint32_t tile = blockIdx.x / step;
   int32_t gi = -1, r0 = 0, r1 = 0;
   for (int32_t g0 = 0; g0 < x.n_groups; g0 += 64) {        // 64 groups at a time
     const int32_t g = min(g0 + lane_id(), x.n_groups - 1);
@@ -541,8 +595,8 @@ ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
   }
   if (gi < 0) return false;
   w.src = Tokens{nullptr, x.prefix_table + static_cast<int64_t>(gi) * x.prefix_pages, x.prefix_len[gi], 0, x.a.pshift, x.prefix_pages, x.a.n_kv};
-  w.t0 = c * x.chunk;
-  w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.chunk, x.a.n_tok), w.src.limit));
+  w.t0 = c * x.prefix_chunk;
+  w.t1 = static_cast<int32_t>(min<int64_t>(min<int64_t>(w.t0 + x.prefix_chunk, x.max_prefix), w.src.limit));
   if (w.t0 >= w.t1) return false;
   if (x.a.n_kv < 1) w.t1 = w.t0;                           // no rows: no tokens
   w.q0 = static_cast<int64_t>(r0) * x.a.n_heads + static_cast<int64_t>(tile) * (32 * QT);
@@ -551,12 +605,19 @@ ECHO_DEV bool prefix_work(const AttArgs &x, Work &w) {
   return true;
 }
 
-template <typename T, int QT, bool WIDE>
+// QP: of a prefix's workgroups, QR of the rows'.
+template <typename T, int QP, int QR, bool WIDE>
 __global__ __launch_bounds__(WAVES * 64) void attention_kernel(AttArgs x) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   Work w;
-  const bool any = x.n_groups > 0 ? prefix_work<QT>(x, w) : rows_work<QT>(x, w);
-  if (any) attend<T, QT, WIDE>(x, w, lds);
+  if (QP == QR) {
+    const bool any = blockIdx.x < x.prefix_blocks ? prefix_work<QP>(x, w) : rows_work<QR>(x, w);
+    if (any) attend<T, QR, WIDE>(x, w, lds);
+  } else if (blockIdx.x < x.prefix_blocks) {
+    if (prefix_work<QP>(x, w)) attend<T, QP, WIDE>(x, w, lds);
+  } else {
+    if (rows_work<QR>(x, w)) attend<T, QR, WIDE>(x, w, lds);
+  }
 }
 
 // ---------------------------------------------------------------- joining chunks
@@ -674,66 +735,63 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs x) {
 }
 
 // ---------------------------------------------------------------- host
-// Groups of 32 queries in a workgroup.
-int head_tile(int64_t queries) { return queries <= 32 ? 1 : 2; }
-
-// Chunks of n_tok tokens for `tiles` query tiles, and their tokens: as many as give each CU one workgroup.
+// Groups of 32 queries in a workgroup (QT), chunks of the tokens and their size.  Measured on MI355X over lists of
+// 2048 tokens (us; one group and two, chunks for 256 workgroups):
+//   128 heads of 1 row 15.3 and 18.5, 8 rows 22.8 and 26.0, 32 rows 43.2 and 40.6, 64 rows 62.8 and 61.8, 128 rows 122 and 92
+// so with one group the CUs have less to write and to join as long as each of them gets one workgroup, and beyond that
+// two groups have half the rows to load.  More chunks than CUs, or less than two tiles in one, cost more than
+// they give (8 rows: 16 chunks instead of 8 30.7; 1 row: 64 instead of 32 18.3).
 constexpr int CUS = 256;
-int32_t chunk_of(int64_t tiles, int64_t n_tok) {
+struct Plan { int qt; int64_t tiles; int32_t chunk, n_chunks; };
+Plan plan_of(int64_t rows, int64_t queries, int64_t n_tok) {           // `rows` times `queries` that share n_tok tokens
+  Plan p;
+  const int64_t one = rows * ((queries + 31) / 32), two = rows * ((queries + 63) / 64);
+  p.qt = queries <= 32 || one <= CUS ? 1 : 2;
+  p.tiles = p.qt == 1 ? one : two;
   const int64_t n = (n_tok + TILE - 1) / TILE;
-  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>(n, CUS / std::max<int64_t>(tiles, 1)));
-  return static_cast<int32_t>((n + chunks - 1) / std::max<int64_t>(chunks, 1)) * TILE;
-}
-int32_t chunks_of(int64_t n_tok, int32_t chunk) { return chunk ? static_cast<int32_t>((n_tok + chunk - 1) / chunk) : 0; }
-constexpr int64_t PART_BYTES = (VALUES + 2) * 4;
-constexpr int64_t MAX_GROUPS = 1 << 24;                    // workgroups of 256 threads in a launch
-constexpr int32_t MAX_HEADS = 1024, MAX_TOKENS = 1 << 28;
-
-struct RowsPlan { int mt; int64_t head_tiles; int32_t chunk, n_chunks; };
-RowsPlan rows_plan(int32_t n_rows, int32_t n_heads, int64_t n_tok) {
-  RowsPlan p;
-  p.mt = head_tile(n_heads);
-  p.head_tiles = (n_heads + 32 * p.mt - 1) / (32 * p.mt);
-  p.chunk = chunk_of(n_rows * p.head_tiles, n_tok);
-  p.n_chunks = std::max(1, chunks_of(n_tok, p.chunk));
+  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((n + 1) / 2, CUS / std::max<int64_t>(p.tiles, 1)));
+  p.chunk = std::max<int32_t>(1, static_cast<int32_t>((n + chunks - 1) / chunks)) * TILE;
+  p.n_chunks = std::max<int32_t>(1, static_cast<int32_t>((n_tok + p.chunk - 1) / p.chunk));
   return p;
 }
+constexpr int64_t PART_BYTES = (VALUES + 2) * 4;
+constexpr int64_t MAX_GROUPS = 1 << 23;                    // workgroups of 512 threads in a launch
+constexpr int32_t MAX_HEADS = 1024, MAX_TOKENS = 1 << 28;
+
 int64_t sparse_ws(int32_t n_rows, int32_t n_heads, int64_t n_tok) {
-  const int32_t c = rows_plan(n_rows, n_heads, n_tok).n_chunks;
+  const int32_t c = plan_of(n_rows, n_heads, n_tok).n_chunks;
   return c > 1 ? static_cast<int64_t>(n_rows) * n_heads * c * PART_BYTES : 0;
 }
 
-struct PrefixPlan { RowsPlan own; int mt; int64_t tiles; int32_t chunk, prefix_parts, own_parts; };
+struct PrefixPlan { Plan own, prefix; int64_t tiles; int32_t prefix_parts, own_parts; };
 PrefixPlan prefix_plan(int32_t n_rows, int32_t n_heads, int32_t n_groups, int32_t max_prefix, int32_t max_own) {
   PrefixPlan p;
-  p.own = rows_plan(n_rows, n_heads, max_own);
+  p.own = plan_of(n_rows, n_heads, max_own);
   p.own_parts = max_own > 0 ? p.own.n_chunks : 0;
-  const int64_t queries = static_cast<int64_t>(n_rows) * n_heads;
-  const int64_t groups = std::min(n_groups, n_rows);
-  p.mt = head_tile(groups ? queries / groups : queries);
-  p.tiles = groups ? queries / (32 * p.mt) + groups : 0;   // at least what the groups' last, partly filled tiles take
-  p.chunk = chunk_of(std::max<int64_t>(1, queries / (32 * p.mt)), max_prefix);
-  p.prefix_parts = groups && max_prefix > 0 ? chunks_of(max_prefix, p.chunk) : 0;
+  const int64_t queries = static_cast<int64_t>(n_rows) * n_heads, groups = std::min(n_groups, n_rows);
+  p.prefix = plan_of(std::max<int64_t>(groups, 1), groups ? (queries + groups - 1) / groups : queries, max_prefix);
+  if (p.own.qt == 2) p.prefix.qt = 2;                      // kernels are built for 1 and 1, 2 and 1, 2 and 2
+  p.tiles = groups ? queries / (32 * p.prefix.qt) + groups : 0;        // at least what the groups' last, partly filled tiles take
+  p.prefix_parts = groups && max_prefix > 0 ? p.prefix.n_chunks : 0;
   return p;
 }
 
 template <typename T, bool WIDE>
-int launch_attention(const AttArgs &x, int mt, uint32_t grid, hipStream_t st) {
-  if (mt == 1) attention_kernel<T, 1, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
-  else attention_kernel<T, 2, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
+int launch_attention(const AttArgs &x, int qp, int qr, uint32_t grid, hipStream_t st) {
+  if (qr == 2) attention_kernel<T, 2, 2, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
+  else if (qp == 2) attention_kernel<T, 2, 1, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
+  else attention_kernel<T, 1, 1, WIDE><<<grid, WAVES * 64, 0, st>>>(x);
   return check_launch("attention");
 }
-int launch_attention(const AttArgs &x, int type, int mt, uint32_t grid, hipStream_t st) {
+int launch_attention(const AttArgs &x, int type, int qp, int qr, int64_t row_blocks, hipStream_t st) {
   const bool wide = static_cast<int64_t>(x.a.n_kv) * x.a.kv_stride * 2 >= (1ll << 32) - 4096;
-  if (type == ECHO_BF16) return wide ? launch_attention<bf16_t, true>(x, mt, grid, st) : launch_attention<bf16_t, false>(x, mt, grid, st);
-  return wide ? launch_attention<fp16_t, true>(x, mt, grid, st) : launch_attention<fp16_t, false>(x, mt, grid, st);
+  const uint32_t grid = x.prefix_blocks + static_cast<uint32_t>(row_blocks);
+  if (type == ECHO_BF16) return wide ? launch_attention<bf16_t, true>(x, qp, qr, grid, st) : launch_attention<bf16_t, false>(x, qp, qr, grid, st);
+  return wide ? launch_attention<fp16_t, true>(x, qp, qr, grid, st) : launch_attention<fp16_t, false>(x, qp, qr, grid, st);
 }
-int launch_rows(const AttArgs &x, int type, const RowsPlan &p, hipStream_t st) {
-  const uint32_t units = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(p.n_chunks), ht = static_cast<uint32_t>(p.head_tiles);
-  return launch_attention(x, type, p.mt, (units + 7) / 8 * 8 * ht, st);
-}
-int launch_prefix(const AttArgs &x, int type, const PrefixPlan &p, hipStream_t st) {
-  return launch_attention(x, type, p.mt, static_cast<uint32_t>(p.tiles) * static_cast<uint32_t>(p.prefix_parts), st);
+// Workgroups of the rows: rows_work's numbering goes by eights of (row, chunk).
+int64_t row_blocks(int32_t n_rows, int32_t n_heads, const Plan &p) {
+  return (static_cast<int64_t>(n_rows) * p.n_chunks + 7) / 8 * 8 * ((n_heads + 32 * p.qt - 1) / (32 * p.qt));
 }
 template <typename T>
 int launch_join(const JoinArgs &j, hipStream_t st) {
@@ -827,8 +885,9 @@ extern "C" int echo_sparse_attention(const echo_latent_args *a, void *out, int64
   if (rc != ECHO_OK || a->n_rows == 0 || a->n_heads == 0) return rc;
   rc = check_out(fn, a->n_rows, a->n_heads, out, out_row_stride, out_head_stride, lse);
   if (rc != ECHO_OK) return rc;
-  const RowsPlan p = rows_plan(a->n_rows, a->n_heads, x.a.n_tok);
-  if ((static_cast<int64_t>(a->n_rows) * p.n_chunks + 8) * p.head_tiles >= MAX_GROUPS)
+  const Plan p = plan_of(a->n_rows, a->n_heads, x.a.n_tok);
+  const int64_t blocks = row_blocks(a->n_rows, a->n_heads, p);
+  if (blocks >= MAX_GROUPS)
     return fail(ECHO_EUNSUPPORTED, "%s: more rows, heads and tokens than a launch holds", fn);
   const int64_t need = sparse_ws(a->n_rows, a->n_heads, x.a.n_tok);
   rc = check_ws(fn, ws, ws_bytes, need);
@@ -841,7 +900,7 @@ extern "C" int echo_sparse_attention(const echo_latent_args *a, void *out, int64
     x.part = static_cast<float *>(ws);
     x.part_ml = x.part + queries * p.n_chunks * VALUES;
   }
-  rc = launch_rows(x, a->type, p, S(stream));
+  rc = launch_attention(x, a->type, 1, p.qt, blocks, S(stream));
   if (rc != ECHO_OK || p.n_chunks == 1) return rc;
   JoinArgs j = {};
   j.part = x.part; j.ml = x.part_ml; j.out = out; j.o_row = out_row_stride; j.o_head = out_head_stride; j.lse = lse;
@@ -874,8 +933,9 @@ extern "C" int echo_prefix_attention(const echo_prefix_args *a, void *out, int64
   if (rc != ECHO_OK) return rc;
   const PrefixPlan p = prefix_plan(a->n_rows, a->n_heads, a->n_groups, a->max_prefix, a->max_own);
   const int64_t queries = static_cast<int64_t>(a->n_rows) * a->n_heads;
-  if (p.tiles * std::max(1, p.prefix_parts) >= MAX_GROUPS || (static_cast<int64_t>(a->n_rows) * p.own.n_chunks + 8) * p.own.head_tiles >= MAX_GROUPS ||
-      queries / 4 >= MAX_GROUPS)
+  const int64_t blocks = p.own_parts ? row_blocks(a->n_rows, a->n_heads, p.own) : 0;
+  const int64_t prefix_blocks = p.prefix_parts ? p.tiles * chunk_step(p.prefix_parts) : 0;
+  if (blocks + prefix_blocks >= MAX_GROUPS || queries / 4 >= MAX_GROUPS)
     return fail(ECHO_EUNSUPPORTED, "%s: more rows, heads and tokens than a launch holds", fn);
   const int32_t parts = p.prefix_parts + p.own_parts;
   rc = check_ws(fn, ws, ws_bytes, queries * parts * PART_BYTES);
@@ -890,23 +950,18 @@ extern "C" int echo_prefix_attention(const echo_prefix_args *a, void *out, int64
   x.parts = parts;
   x.part = static_cast<float *>(ws);
   x.part_ml = x.part + queries * parts * VALUES;
-  const bool bf = a->type == ECHO_BF16;
+  x.chunk = p.own.chunk; x.n_chunks = p.own.n_chunks; x.first_part = p.prefix_parts;
   if (p.prefix_parts) {
-    AttArgs y = x;
-    y.a.n_tok = a->max_prefix;
-    y.chunk = p.chunk; y.n_chunks = p.prefix_parts;
-    y.group_begin = a->group_begin; y.prefix_len = a->prefix_len; y.prefix_table = a->prefix_table;
-    y.n_groups = a->n_groups; y.prefix_pages = a->prefix_pages;
-    rc = launch_prefix(y, a->type, p, S(stream));
-    if (rc != ECHO_OK) return rc;
+    x.group_begin = a->group_begin; x.prefix_len = a->prefix_len; x.prefix_table = a->prefix_table;
+    x.n_groups = a->n_groups; x.prefix_pages = a->prefix_pages;
+    x.max_prefix = a->max_prefix; x.prefix_chunk = p.prefix.chunk; x.prefix_chunks = p.prefix_parts;
+    x.prefix_blocks = static_cast<uint32_t>(prefix_blocks);
   }
-  if (p.own_parts) {
-    x.chunk = p.own.chunk; x.n_chunks = p.own_parts; x.first_part = p.prefix_parts;
-    rc = launch_rows(x, a->type, p.own, S(stream));
+  if (blocks + prefix_blocks > 0) {
+    rc = launch_attention(x, a->type, p.prefix.qt, p.own.qt, blocks, S(stream));
     if (rc != ECHO_OK) return rc;
   }
   const JoinArgs j = {x.part, x.part_ml, out, out_row_stride, out_head_stride, lse, a->n_rows, a->n_heads, parts, a->own_len, a->group_begin,
-                      a->prefix_len, p.prefix_parts ? a->n_groups : 0, std::max(p.chunk, TILE), a->max_prefix, p.prefix_parts,
-                      std::max(p.own.chunk, TILE), a->max_own};
-  return bf ? launch_join<bf16_t>(j, S(stream)) : launch_join<fp16_t>(j, S(stream));
+                      a->prefix_len, p.prefix_parts ? a->n_groups : 0, p.prefix.chunk, a->max_prefix, p.prefix_parts, p.own.chunk, a->max_own};
+  return a->type == ECHO_BF16 ? launch_join<bf16_t>(j, S(stream)) : launch_join<fp16_t>(j, S(stream));
 }
