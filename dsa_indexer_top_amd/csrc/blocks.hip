@@ -1,9 +1,12 @@
 // Blocks of a row's tokens that its scores select (echo_block_topk): a block's score is the largest of
 // its tokens' scores; the row's first and last blocks may be kept whatever they score.
 //
-// Reading the scores is all there is to it: a wave takes 256 of them at a time, 4 a lane, and the
-// lanes of a block are joined with moves between lanes.  The blocks' scores, a 16th of the row or less, go through
-// the exact top-k of topk.hip.
+// Reading the scores is all there is to it: a wave takes 1024 of them at a time in four loads, and the
+// lanes of a block are joined with moves between lanes.  On MI355X 4096 rows of 65536 scores (up to 1.07 GB, by their
+// lengths 0.8) with blocks of 128 take 148 us with the selection, 4 rows of 8192 6.8 us, most of that two launches.
+// One load a wave, as at first, took 242 us where four take about 100.
+// The blocks' scores, a 16th of the row or less, are selected from by a wave a row, or, above 512, by the
+// exact top-k of topk.hip.
 #include <algorithm>
 
 #include "float_types.cuh"
@@ -18,7 +21,8 @@ struct OpMaxF {
   }
 };
 
-// One wave per 256 tokens of a row, or per block where blocks are larger.
+// One wave per 1024 tokens of a row, or per block where blocks are larger; four loads on their way.
+constexpr int SPAN = 1024;
 template <int G>                                           // lanes of a block, 64 for blocks of 256 and more
 __global__ __launch_bounds__(256) void block_max_kernel(const float *__restrict__ scores, int64_t ld, const int32_t *__restrict__ len,
                                                         int64_t waves, int32_t per_row, int32_t max_len, int32_t block, int32_t n_blocks,
@@ -29,24 +33,88 @@ __global__ __launch_bounds__(256) void block_max_kernel(const float *__restrict_
   const int32_t n = max(0, min(len[r], max_len)), l = lane_id();
   const int32_t nb = static_cast<int32_t>((static_cast<int64_t>(n) + block - 1) / block);
   if (u == 0 && l == 0) count[r] = nb;
-  const int32_t span = max(block, 256);
+  const int32_t span = max(block, SPAN);
   const int64_t t0 = static_cast<int64_t>(u) * span;
   if (t0 >= n) return;
   const float *row = scores + r * ld;
-  float m = -INFINITY;
-  for (int32_t i = 4 * l; i < span; i += 256) {
-    const int64_t t = t0 + i;
-    if (t + 4 <= n) {
-      const f32x4 v = *reinterpret_cast<const f32x4_any *>(row + t);
-      m = fmaxf(m, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};             // of the four 256ths
+  for (int64_t t = t0 + 4 * l; t < t0 + span; t += SPAN) {
+    if (t - 4 * l + SPAN <= n) {
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const f32x4_any *>(row + t + 256 * i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], fmaxf(fmaxf(v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3])));
     } else {
-      for (int64_t e = t; e < n; ++e) m = fmaxf(m, row[e]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        for (int64_t e = t + 256 * i; e < min<int64_t>(n, t + 256 * i + 4); ++e) m[i] = fmaxf(m[i], row[e]);
     }
   }
-  m = __uint_as_float(group_reduce<G < 32 ? G : 32>(__float_as_uint(m), OpMaxF{}));
-  if (G == 64) m = fmaxf(m, __shfl_xor(m, 32, 64));
-  const int32_t b = G == 64 ? u : u * (64 / G) + l / G;
-  if (l % G == 0 && b < nb) pooled[static_cast<int64_t>(r) * n_blocks + b] = b < n_first || b >= nb - n_last ? INFINITY : m;
+  float *out = pooled + static_cast<int64_t>(r) * n_blocks;
+  const auto store = [&](int32_t b, float v) { if (b < nb) out[b] = b < n_first || b >= nb - n_last ? INFINITY : v; };
+  if (G < 64) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = __uint_as_float(group_reduce<G < 32 ? G : 32>(__float_as_uint(m[i]), OpMaxF{}));
+      if (l % G == 0) store((4 * u + i) * (64 / G) + l / G, v);
+    }
+  } else {                                                 // 4, 2 or 1 blocks
+    if (block > 256) { m[0] = fmaxf(m[0], m[1]); m[2] = fmaxf(m[2], m[3]); }
+    if (block > 512) m[0] = fmaxf(m[0], m[2]);
+    const int32_t step = min(block, SPAN) / 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v = __uint_as_float(group_reduce<32>(__float_as_uint(m[i]), OpMaxF{}));
+      v = fmaxf(v, __shfl_xor(v, 32, 64));
+      if (l == 0 && i % step == 0) store((4 * u + i) / step, v);
+    }
+  }
+}
+
+// The k highest of up to 64 V blocks' scores, a wave a row: the k-th highest key bit by bit, each bit a count of the
+// keys that are not below (a ballot for 64 of them, no waits), then the blocks above it and the first of those that equal it, in order.
+template <int V>
+__global__ __launch_bounds__(256) void block_select_kernel(const float *__restrict__ pooled, int32_t n_blocks, const int32_t *__restrict__ count,
+                                                           int32_t n_rows, int32_t k, int32_t *__restrict__ idx) {
+  const int32_t r = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), l = lane_id();
+  if (r >= n_rows) return;
+  const int32_t n = count[r];
+  const float *row = pooled + static_cast<int64_t>(r) * n_blocks;
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = 64 * v + l < n ? f32_key(row[64 * v + l]) : 0u;       // a score's key is above 0
+  const auto at_least = [&](uint32_t x) {
+    int32_t c = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) c += static_cast<int32_t>(__popcll(__ballot(key[v] >= x)));
+    return c;
+  };
+  uint32_t least = 1;                                      // of the keys taken
+  int32_t ties = n;                                        // how many that equal it are
+  if (n > k) {
+    least = 0;
+    int32_t have = n;
+    for (uint32_t bit = 1u << 31; bit && have != k; bit >>= 1) {
+      const int32_t c = at_least(least | bit);
+      if (c >= k) { least |= bit; have = c; }
+    }
+    if (have != k) ties = k - (least == ~0u ? 0 : at_least(least + 1));
+  }
+  const uint64_t below = (1ull << l) - 1;
+  const auto number = [](uint64_t m) { return static_cast<int32_t>(__popcll(m)); };
+  int32_t *out = idx + static_cast<int64_t>(r) * k;
+  int32_t pos = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint64_t eq = __ballot(key[v] == least);
+    const bool take = key[v] > least || (key[v] == least && number(eq & below) < ties);
+    const uint64_t all = __ballot(take);
+    if (take) out[pos + number(all & below)] = 64 * v + l;
+    ties -= number(eq);
+    pos += number(all);
+  }
+  for (int32_t j = pos + l; j < k; j += 64) out[j] = -1;
 }
 
 }  // namespace echo
@@ -72,7 +140,7 @@ extern "C" int echo_block_topk(const float *scores, int64_t ld, const int32_t *l
   if ((max_len && !scores) || !len || !idx) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
   if ((reinterpret_cast<uintptr_t>(scores) | reinterpret_cast<uintptr_t>(len) | reinterpret_cast<uintptr_t>(idx)) % 4)
     return fail(ECHO_EINVAL, "%s: an array is not aligned to its type", fn);
-  const int32_t n_blocks = static_cast<int32_t>(blocks_in(max_len, block)), span = std::max(block, 256);
+  const int32_t n_blocks = static_cast<int32_t>(blocks_in(max_len, block)), span = std::max(block, SPAN);
   const int32_t per_row = std::max<int32_t>(1, static_cast<int32_t>(blocks_in(max_len, span)));
   const int64_t waves = static_cast<int64_t>(n_rows) * per_row;
   if (waves >= 1 << 26 || n_rows >= 1 << 22) return fail(ECHO_EUNSUPPORTED, "%s: more rows and tokens than a launch holds", fn);
@@ -94,5 +162,12 @@ extern "C" int echo_block_topk(const float *scores, int64_t ld, const int32_t *l
 #undef RUN
   const int rc = check_launch("block maxima");
   if (rc != ECHO_OK) return rc;
-  return launch_topk_rows(pooled, n_blocks, count, n_rows, n_blocks, k, nullptr, idx, st);
+#define RUN(V) block_select_kernel<V><<<(n_rows + 3) / 4, 256, 0, st>>>(pooled, n_blocks, count, n_rows, k, idx)
+  // Measured on MI355X, both launches (us, and with topk.hip's): 128 blocks of 1 row 6.7 and 13.8; 512 blocks of 1 row 9.0 and 14.4, of
+  // 4096 rows 148 and 195; 1024 blocks of 1 row 16.4 and 15.0, 2048 of 64 rows 29 and 22.5.
+  if (n_blocks <= 128) RUN(2);
+  else if (n_blocks <= 512) RUN(8);
+  else return launch_topk_rows(pooled, n_blocks, count, n_rows, n_blocks, k, nullptr, idx, st);
+#undef RUN
+  return check_launch("block selection");
 }

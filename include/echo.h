@@ -748,7 +748,7 @@ int echo_newest_queries(const uint8_t *q8, const float *w, const int32_t *row_be
  * 1 <= k <= ECHO_MAX_TOPK, ld >= max_len.  Workspace: echo_block_topk_workspace_bytes; calls that may run
  * at the same time need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, ld < max_len, NULL
  * pointers and arrays not aligned to their types; ECHO_EUNSUPPORTED for other blocks or k and for more than
- * a launch holds (2^22 rows, 2^26 waves of 256 tokens or, where larger, a block); ECHO_EWORKSPACE.
+ * a launch holds (2^22 rows, 2^26 waves of 1024 tokens or, where larger, a block); ECHO_EWORKSPACE.
  */
 size_t echo_block_topk_workspace_bytes(int32_t n_rows, int32_t max_len, int32_t block);
 int echo_block_topk(const float *scores, int64_t ld, const int32_t *len, int32_t n_rows, int32_t max_len, int32_t block,

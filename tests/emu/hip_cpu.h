@@ -72,7 +72,7 @@ inline int __float_as_int(float f) { int x; memcpy(&x, &f, 4); return x; }
 inline unsigned __float_as_uint(float f) { unsigned x; memcpy(&x, &f, 4); return x; }
 inline int __ffsll(unsigned long long x) { return x ? __builtin_ctzll(x) + 1 : 0; }
 inline int __ffsll(long long x) { return __ffsll(static_cast<unsigned long long>(x)); }
-inline int __popcll(unsigned long long x) { return __builtin_popcountll(x); }
+inline unsigned int __popcll(unsigned long long x) { return __builtin_popcountll(x); }
 inline int __popc(unsigned x) { return __builtin_popcount(x); }
 inline int __ffs(unsigned x) { return x ? __builtin_ctz(x) + 1 : 0; }
 inline int __ffs(int x) { return __ffs(static_cast<unsigned>(x)); }
