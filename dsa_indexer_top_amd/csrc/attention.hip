@@ -739,16 +739,17 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs x) {
 // 2048 tokens (us; one group and two, chunks for 256 workgroups):
 //   128 heads of 1 row 15.3 and 18.5, 8 rows 22.8 and 26.0, 32 rows 43.2 and 40.6, 64 rows 62.8 and 61.8, 128 rows 122 and 92
 // so with one group the CUs have less to write and to join as long as each of them gets one workgroup, and beyond that
-// two groups have half the rows to load.  More chunks than CUs, or less than two tiles in one, cost more than
+// two groups have half the rows to load; so they have where a workgroup has many tiles to go through (prefixes, 64
+// tiles with two groups: 16 heads of 64 requests behind 32768 tokens 127 and 112; 32 tiles, 32 requests: 62 and 66).  More chunks than CUs, or less than two tiles in one, cost more than
 // they give (8 rows: 16 chunks instead of 8 30.7; 1 row: 64 instead of 32 18.3).
 constexpr int CUS = 256;
 struct Plan { int qt; int64_t tiles; int32_t chunk, n_chunks; };
 Plan plan_of(int64_t rows, int64_t queries, int64_t n_tok) {           // `rows` times `queries` that share n_tok tokens
   Plan p;
   const int64_t one = rows * ((queries + 31) / 32), two = rows * ((queries + 63) / 64);
-  p.qt = queries <= 32 || one <= CUS ? 1 : 2;
-  p.tiles = p.qt == 1 ? one : two;
   const int64_t n = (n_tok + TILE - 1) / TILE;
+  p.qt = queries <= 32 || (one <= CUS && n * two <= 32 * CUS) ? 1 : 2;
+  p.tiles = p.qt == 1 ? one : two;
   const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((n + 1) / 2, CUS / std::max<int64_t>(p.tiles, 1)));
   p.chunk = std::max<int32_t>(1, static_cast<int32_t>((n + chunks - 1) / chunks)) * TILE;
   p.n_chunks = std::max<int32_t>(1, static_cast<int32_t>((n_tok + p.chunk - 1) / p.chunk));
