@@ -136,6 +136,18 @@ class DecodeRunner:
         if self._own_buf:
             self.host_buf.close()
 
+class Heads:
+    """What a runner needs for attention over latent rows by n_heads heads: their queries q [n_rows, n_heads, 576]
+    and results out [n_rows, n_heads, 512] of `dtype`, log sums, and a workspace of ws_bytes."""
+
+    def __init__(self, n_rows, n_heads, scale, dtype, ws_bytes):
+        import torch
+        self.scale = scale
+        self.q = torch.zeros((n_rows, n_heads, 576), dtype=dtype, device="cuda")
+        self.out = torch.empty((n_rows, n_heads, 512), dtype=dtype, device="cuda")
+        self.lse = torch.empty((n_rows, n_heads), dtype=torch.float32, device="cuda")
+        self.ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device="cuda")
+
 
 class LoopRunner:
     """Device buffers of several decode steps in a row (inputs.MultiStepInputs): the K cache with
@@ -144,11 +156,13 @@ class LoopRunner:
     query and new tokens, then enqueues echo_decode_append and echo_decode_select.  With
     device_step=True the step stamp lives on the device; capture() then records
     echo_step_advance + echo_decode_append + echo_decode_select as one graph, and
-    replay_step(st) uploads step st's inputs and replays it.  No arithmetic of the method lives
-    here."""
+    replay_step(st) uploads step st's inputs and replays it.  With heads = dict(n_heads, scale, dtype
+    (bf16), decay (1)) every step goes on to attention over the selected pool rows, of the queries in
+    heads.q into heads.out, and to the pool's eviction order by the weight that each slot's token has got so far
+    (mass) in place of the step stamps.  No arithmetic of the method lives here."""
 
     def __init__(self, m, host_kv, topk, prefetch=False, pf=None, alpha=0.5, ema=True,
-                 device_step=False, reserve=0):
+                 device_step=False, reserve=0, heads=None):
         import torch
         self.torch = torch
         self.m = m
@@ -183,10 +197,10 @@ class LoopRunner:
         self.topk_idx = torch.empty((B_, topk), dtype=i32, device=dev)
         self.topk_slot = torch.empty((B_, topk), dtype=i32, device=dev)
         self.miss_host = torch.empty(B_ * topk, dtype=i32, device=dev)
-        self.miss_slot = torch.empty(B_ * topk, dtype=i32, device=dev)
+        self.fresh = torch.full((B_ * topk + B_,), -1, dtype=i32, device=dev)    # the step's slots with another token
+        self.miss_slot, self.new_slot = self.fresh[:B_ * topk], self.fresh[B_ * topk:]
         self.counters = torch.zeros(8, dtype=i32, device=dev)
         self.kth = torch.empty(B_, dtype=f32, device=dev)
-        self.new_slot = torch.empty(B_, dtype=i32, device=dev)
         self.theta = torch.full((B_,), float("nan"), dtype=f32, device=dev)
         self.out = B.DecodeOut(self.scores.data_ptr(), self.topk_idx.data_ptr(),
                                self.topk_slot.data_ptr(), self.miss_host.data_ptr(),
@@ -222,12 +236,28 @@ class LoopRunner:
             first = int(m.steps[0]["step_id"]) if m.steps else int(m.pool.step_id)
             self.step_dev = torch.full((1,), first - 1, dtype=i32, device=dev)
             self.args.step_dev = self.app.step_dev = self.step_dev.data_ptr()
+        self.heads = None
+        if heads is not None:
+            dtype = heads.get("dtype", torch.bfloat16)
+            self.heads = Heads(B_, heads["n_heads"], heads["scale"], dtype,
+                               B.sparse_attention_workspace_bytes(B_, heads["n_heads"], topk))
+            self.kv = self.live["gpu_kv"].view(dtype)
+            self.decay = heads.get("decay", 1.0)
+            self.weights = torch.empty((B_, topk), dtype=f32, device=dev)
+            self.mass = torch.zeros(self.n_gpu, dtype=f32, device=dev)
+            self.ws_weigh = torch.empty(max(B.pool_weigh_workspace_bytes(self.n_gpu), 256), dtype=torch.uint8, device=dev)
 
     def _enqueue_step(self, stream):
         if self.step_dev is not None:
             B.step_advance(self.step_dev, stream)
         B.decode_append(self.app, self.pool, self.new_slot, self.ws_app, stream)
         B.decode_select(self.args, self.pool, self.out, self.ws, stream)
+        if self.heads is not None:
+            h = self.heads
+            B.sparse_attention(h.q, self.kv, self.topk_slot, h.out, h.scale, h.ws, lse=h.lse, stream=stream)
+            B.attention_weights(h.q, self.kv, self.topk_slot, h.lse, self.weights, h.scale, stream=stream)
+            B.pool_weigh(self.live["free"], self.live["priority"], self.mass, self.topk_slot, self.weights,
+                         self.ws_weigh, decay=self.decay, fresh=self.fresh, stream=stream)
 
     def capture(self):
         assert self.step_dev is not None, "a replayable step needs the stamp on the device"
@@ -386,11 +416,18 @@ class PagedIndexerRunner:
     every request's newest query against its pages and selects its top-k; a request that got no token
     in the step (padding, a finished one, every one of a step that was refused) has no query and
     selects nothing.  A step costs what max_new tokens cost, however many it has.  Weights are (codes,
-    scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden], ww [64, hidden].  No arithmetic of the
-    method lives here."""
+    scales) pairs: wq [64 * 128, q_hidden], wk [128, hidden], ww [64, hidden].
+
+    With heads = dict(n_heads, scale, dtype (bf16), block (0: tokens), kept (1, 2)) there is a latent cache kv next to
+    the keys, in the same pages (the caller puts the new tokens' rows at `slot`), and score() goes on to attend(): the
+    newest queries' latents heads.q over the selected tokens, or, with block, over the `topk` best blocks of that many
+    tokens, the first kept[0] and last kept[1] of them always.  attend_all() is the same over every token, where a
+    context is no longer than the selection.  With heads["prefixes"] = (groups, pages) it goes over prefixes that
+    groups of requests share first: rows group_begin[g] .. group_begin[g + 1] of the batch the first prefix_len[g]
+    tokens of kv's pages prefix_table[g] (all 0: none).  No arithmetic of the method lives here."""
 
     def __init__(self, n_rows, page_size, max_pages, n_pages, max_new, topk, wq, wk, ww, cos_sin,
-                 k_weight, k_bias, w_mul, eps=1e-6, interleaved=False):
+                 k_weight, k_bias, w_mul, eps=1e-6, interleaved=False, heads=None):
         import torch
         dev, i32, u8, f32, bf16 = "cuda", torch.int32, torch.uint8, torch.float32, torch.bfloat16
         self.wq, self.wk, self.ww = wq, wk, ww
@@ -432,6 +469,22 @@ class PagedIndexerRunner:
         self.scores = torch.empty((n_rows, self.max_len), dtype=f32, device=dev)
         self.idx = torch.empty((n_rows, topk), dtype=i32, device=dev)
         self.ws_topk = torch.empty(max(B.topk_workspace_bytes(n_rows, self.max_len), 256), dtype=u8, device=dev)
+        self.heads, self.block = None, 0
+        if heads is not None:
+            self.block, self.kept = heads.get("block", 0), heads.get("kept", (1, 2))
+            dtype, n_heads = heads.get("dtype", bf16), heads["n_heads"]
+            groups, pages = heads.get("prefixes", (0, 0))
+            self.group_begin = torch.zeros(groups + 1, dtype=i32, device=dev)
+            self.prefix_len = torch.zeros(groups, dtype=i32, device=dev)
+            self.prefix_table = torch.zeros((groups, pages), dtype=i32, device=dev)
+            self.max_prefix = pages * page_size
+            self.heads = Heads(n_rows, n_heads, heads["scale"], dtype, max(
+                B.sparse_attention_workspace_bytes(n_rows, n_heads, topk * max(self.block, 1)),
+                B.prefix_attention_workspace_bytes(n_rows, n_heads, groups, self.max_prefix, self.max_len)))
+            self.kv = torch.zeros((n_pages * page_size, 576), dtype=dtype, device=dev)
+            if self.block:
+                self.ws_topk = torch.empty(max(B.block_topk_workspace_bytes(n_rows, self.max_len, self.block), 256),
+                                           dtype=u8, device=dev)
 
     def step(self, stream=None):
         """One step of the requests' new_len tokens (x and xq hold their states in request order),
@@ -457,4 +510,23 @@ class PagedIndexerRunner:
                          stream=stream)
         B.index_scores_paged(self.q_last, self.w_last, self.k, self.k_scale, self.table, self.page_size,
                              self.score_len, self.max_len, self.scores, stream=stream)
-        B.topk(self.scores, self.score_len, self.max_len, self.topk, self.idx, self.ws_topk, stream=stream)
+        if self.block:
+            B.block_topk(self.scores, self.score_len, self.max_len, self.block, self.topk, self.idx, self.ws_topk,
+                         n_first=self.kept[0], n_last=self.kept[1], stream=stream)
+        else:
+            B.topk(self.scores, self.score_len, self.max_len, self.topk, self.idx, self.ws_topk, stream=stream)
+        if self.heads is not None:
+            self.attend(stream)
+
+    def attend(self, stream=None):
+        """Attention of every request's newest query over what score() selected; zeros for a request without one."""
+        h = self.heads
+        B.sparse_attention(h.q, self.kv, self.idx, h.out, h.scale, h.ws, lse=h.lse, block=max(self.block, 1),
+                           length=self.score_len, page_table=self.table, page_size=self.page_size, stream=stream)
+
+    def attend_all(self, stream=None):
+        """Attention of every request's newest query over its group's prefix and all its own tokens."""
+        h = self.heads
+        B.prefix_attention(h.q, self.kv, h.out, h.scale, self.group_begin, self.prefix_len, self.prefix_table,
+                           self.score_len, self.table, self.page_size, self.max_prefix, self.max_len, h.ws, lse=h.lse,
+                           stream=stream)

@@ -22,7 +22,8 @@ def pytest_configure(config):
 BOTTOM_UP = ("test_gpu_pages.py", "test_gpu_blockfp8.py", "test_gpu_products.py", "test_gpu_heads.py",
              "test_gpu_blocks.py", "test_gpu_attention.py",
              "test_gpu_scores.py", "test_gpu_topk.py", "test_gpu_pool.py", "test_gpu_decode.py",
-             "test_gpu_inputs.py", "test_gpu_prefill.py", "test_gpu_multistep.py", "test_gpu_interquery.py",
+             "test_gpu_inputs.py", "test_gpu_prefill.py", "test_gpu_multistep.py", "test_gpu_attend.py",
+             "test_gpu_interquery.py",
              "test_gpu_layers.py", "test_gpu_fused.py", "test_gpu_stress.py")
 
 
