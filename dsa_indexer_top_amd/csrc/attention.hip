@@ -149,9 +149,11 @@ struct Fetch {
   }
   ECHO_DEV void load(uint8_t *__restrict__ stage, int i) const {
     if (i < OWN) {                                         // r0 is a multiple of 4
-      const uint64_t above = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i))) << 32 : 0;
-      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(reinterpret_cast<uint64_t>(kv) + above), 0, -1, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(r0) + row_at(i)), 16, lane_id() * 16, __builtin_amdgcn_readlane(lo, r0 + i), 0, 0);
+      const uint32_t at = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r0 + i));
+      // A descriptor's offsets are added up in 32 bits, so rows of a wide cache get a descriptor each.
+      const uint64_t from = WIDE ? static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0 + i))) << 32 | at : 0;
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(reinterpret_cast<uint64_t>(kv) + from), 0, -1, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void *)(stage + row_at(r0) + row_at(i)), 16, lane_id() * 16, WIDE ? 0 : at, 0, 0);
     } else if (WIDE) {                                     // eight rows in one load: addresses by lane
       __builtin_amdgcn_global_load_lds((glb_void *)(static_cast<const uint8_t *>(kv) + rope), (lds_void *)(stage + ROPE_AT + r0 * 128), 16, 0, 0);
     } else {
@@ -266,7 +268,7 @@ struct Scorer {
     bool above = false;
 #pragma unroll
     for (int i = 0; i < QT; ++i) above |= top(i) > far[i];
-    if (__ballot(above)) lds.raise[t & 1] = t + 1;         // every lane the same
+    if (__ballot(above) && lane_id() == 0) atomicMax(&lds.raise[t & 1], t + 1);     // by any of the waves
   }
   // Maxima up to those of tile t, whose weights are given anew; with Adder::raise.
   ECHO_DEV void raise(Lds &lds, int t) {

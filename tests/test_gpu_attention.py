@@ -315,3 +315,133 @@ def test_other_stream_and_two_calls_at_once():
     torch.cuda.synchronize()
     for (q, kv, idx, _), (out, lse) in zip(sets, got):
         check(out, lse, q, kv, [r for _, r in oa.listed_rows(idx, 1, 900)])
+
+
+# ---------------------------------------------------------------- sizes where something else runs
+@pytest.mark.parametrize("R,H,k", [(130, 5, 1700), (131, 64, 1600)])
+def test_long_chunks_full(R, H, k):
+    """Rows that are not cut, of more tokens than a workgroup looks up at once."""
+    rng = np.random.default_rng(R)
+    n = 4000
+    announce("long chunks", R, H, k)
+    assert B.sparse_attention_workspace_bytes(R, H, k) == 0
+    q, kv, idx = rand(rng, (R, H, 576), "bf16").cuda(), rand(rng, (n, 576), "bf16").cuda(), lists(rng, R, k, n)
+    idx[1, 1536:] = -1
+    idx[2, :1540] = -1
+    out, lse = sparse(q, kv, idx)
+    check(out, lse, q, kv, [r for _, r in oa.listed_rows(idx, 1, n)])
+
+
+@pytest.mark.parametrize("R,H,groups,prefix,own", [
+    (64, 16, [0, 33, 64], [17500, 16001], 70),             # two groups of 32 queries for the prefixes alone
+    (70, 128, [0, 64, 70], [900, 33], 50)])                # for prefixes and own tokens
+def test_shared_prefixes_of_many_queries_full(R, H, groups, prefix, own):
+    rng = np.random.default_rng(R + H)
+    c = prefix_case(rng, R, H, groups, prefix, list(rng.integers(0, own, R)), 64, "bf16")
+    announce("prefix, many queries", R, H)
+    out, lse = run_prefix(c)
+    check(out, lse, c["q"], c["kv"], prefix_rows(c))
+
+
+def test_many_groups():
+    """More groups than a wave looks through at once, some of them empty."""
+    rng = np.random.default_rng(17)
+    R = 90
+    begin = np.sort(np.concatenate([[0], rng.integers(0, R + 1, 150), [R]]))
+    c = prefix_case(rng, R, 2, begin, list(rng.integers(0, 40, 151)), [0] * 45 + [5] * 45, 16, "fp16")
+    announce("prefix, many groups")
+    out, lse = run_prefix(c)
+    check(out, lse, c["q"], c["kv"], prefix_rows(c))
+
+
+def test_an_empty_cache():
+    rng = np.random.default_rng(18)
+    q, idx = rand(rng, (2, 16, 576), "bf16").cuda(), np.zeros((2, 70), np.int32)
+    kv = torch.empty(0, 576, dtype=torch.bfloat16, device="cuda")
+    announce("no cache")
+    out, lse = sparse(q, kv, idx)
+    assert not host(out.float()).any() and np.isneginf(host(lse)).all()
+    w = torch.full((2, 70), 3.0, device="cuda")
+    B.attention_weights(q, kv, dev(idx), lse, w, SCALE)
+    assert not host(w).any()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+def test_scores_that_keep_rising(t):
+    """Every tile has a token far above all before it, so that sums and results are scaled again and again; some heads'
+    scores fall instead."""
+    rng = np.random.default_rng(19)
+    n, H = 700, 40
+    announce("rising", t)
+    q, kv = rand(rng, (2, H, 576), t, 0.02), rand(rng, (n, 576), t)
+    kv[:, 575] = (torch.arange(n) // 7).to(kv.dtype)       # whole numbers up to 100
+    q[:, :, 575] = 4.0
+    q[:, 30:, 575] = -4.0
+    q, kv = q.cuda(), kv.cuda()
+    idx = np.stack([np.arange(n), rng.permutation(n)]).astype(np.int32)
+    out, lse = sparse(q, kv, idx, scale=1.0)
+    check(out, lse, q, kv, [r for _, r in oa.listed_rows(idx, 1, n)], scale=1.0)
+
+
+def test_a_cache_behind_32_bits_full():
+    """Rows on either side of 2^31 and 2^32 bytes, in a cache of 4.6 GB; only the listed ones are numbers."""
+    rng = np.random.default_rng(20)
+    n, R, H, k, page = 4000000, 3, 20, 300, 64
+    marks = [0, (1 << 31) // 1152, (1 << 32) // 1152, n - 2]
+    rows = np.unique(np.concatenate([rng.integers(0, n, 1500)] + [np.arange(max(m - 3, 0), min(m + 2, n)) for m in marks]))
+    announce("4.6 GB")
+    q, small = rand(rng, (R, H, 576), "bf16").cuda(), rand(rng, (len(rows), 576), "bf16").cuda()
+    kv = torch.empty(n, 576, dtype=torch.bfloat16, device="cuda")
+    kv.fill_(float("nan"))
+    kv[torch.from_numpy(rows).cuda()] = small
+    at = np.stack([rng.permutation(len(rows))[:k] for _ in range(R)])
+    near = [r for m in marks for r in range(max(m - 3, 0), m + 2) if r < n]
+    at[:, :len(near)] = np.searchsorted(rows, near)
+    idx = rows[at].astype(np.int32)
+    idx[0, 30], idx[1, 31] = -1, n                         # none, and one row behind the end
+    listed = [a[(i >= 0) & (i < n)] for a, i in zip(at, idx)]
+    out, lse = sparse(q, kv, idx)
+    check(out, lse, q, small, listed)
+    w = torch.empty(R, k, device="cuda")
+    B.attention_weights(q, kv, dev(idx), lse, w, SCALE)
+    places = [np.flatnonzero((i >= 0) & (i < n)) for i in idx]
+    want = oa.token_weights(f64(q), f64(small), places, listed, f64(lse), SCALE, k)
+    _, want_lse, _, terms = oa.attention(f64(q), f64(small), listed, SCALE)
+    assert (np.abs(host(w) - want) <= want * score_error(terms, want_lse).max() + 1e-30).all()
+    # pages: the last one and the one around 2^32 bytes
+    pages = np.array([n // page - 1, (1 << 32) // 1152 // page, 3], np.int32)
+    paged = np.concatenate([np.arange(p * page, (p + 1) * page) for p in pages])
+    dense = rand(rng, (len(paged), 576), "bf16").cuda()
+    kv[torch.from_numpy(paged).cuda()] = dense
+    out, lse = torch.empty_like(out), torch.empty_like(lse)
+    ws = workspace(B.prefix_attention_workspace_bytes(R, H, 1, 128, 64))
+    B.prefix_attention(q, kv, out, SCALE, dev(np.array([0, 2], np.int32)), dev(np.array([120], np.int32)), dev(pages[None, :2].copy()),
+                       dev(np.array([64, 10, 33], np.int32)), dev(np.full((3, 1), pages[2])), page, 128, 64, ws, lse=lse)
+    own = 128 + np.arange(64)
+    check(out, lse, q, dense, [np.concatenate([np.arange(120), own]), np.concatenate([np.arange(120), own[:10]]), own[:33]])
+
+
+def test_two_graphs_of_one_workspace():
+    """Captured apart, replayed in turn on one stream."""
+    rng = np.random.default_rng(21)
+    R, H, k, n = 2, 16, 500, 900
+    q, kv = rand(rng, (R, H, 576), "bf16").cuda(), rand(rng, (n, 576), "bf16").cuda()
+    ws = workspace(B.sparse_attention_workspace_bytes(R, H, k))
+    st = torch.cuda.Stream()
+    sets = []
+    for _ in range(2):
+        idx, out, lse = dev(lists(rng, R, k, n)), torch.empty(R, H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(R, H, device="cuda")
+        torch.cuda.synchronize()
+        g = B.CapturedGraph(lambda s: B.sparse_attention(q, kv, idx, out, SCALE, ws, lse=lse, stream=s), st)
+        sets.append((g, idx, out, lse))
+    for i in range(3):
+        announce("two graphs", i)
+        q.copy_(rand(rng, (R, H, 576), "bf16"))
+        torch.cuda.synchronize()
+        for g, *_ in sets:
+            g.launch(st)
+        torch.cuda.synchronize()
+        for _, idx, out, lse in sets:
+            check(out, lse, q, kv, [r for _, r in oa.listed_rows(host(idx), 1, n)])
+    for g, *_ in sets:
+        g.close()

@@ -150,3 +150,34 @@ def test_pool_step_evicts_the_smallest_mass():
             assert np.array_equal(getattr(got, name), getattr(want_state, name)), name
     finally:
         p.close()
+
+
+@pytest.mark.parametrize("n,block", [(1023, 16), (1024, 16), (1025, 64), (2048, 256), (4097, 512), (9000, 1024), (9000, 4096),
+                                     (2049, 16), (8193, 16)])
+def test_blocks_around_a_waves_span(n, block):
+    """Lengths around what a wave takes, blocks around it and above, and 129, 512 and 513 blocks of a row."""
+    rng = np.random.default_rng(n + block)
+    scores = np.round(8 * rng.standard_normal((5, n))).astype(np.float32)           # many ties
+    length = [n, n - 1, max(0, n - block), n // 2 + 1, min(n, 1024)]
+    announce("blocks, spans", n, block)
+    for k, first, last in ((1, 0, 0), (3, 0, 1), (7, 2, 0), (100, 0, 0)):
+        got = block_topk(scores, length, block, k, first, last, ld_pad=1)
+        assert np.array_equal(got, oa.block_topk(scores, length, block, k, first, last)), k
+
+
+@pytest.mark.parametrize("n,entries", [(700, 30000), (3000, 5), (40000, 20000), (200000, 9000)])
+def test_weigh_either_way(n, entries):
+    """Few entries and many, few slots and many: searched for in one launch, or added up in memory."""
+    rng = np.random.default_rng(n)
+    announce("weigh", n, entries)
+    mass, free = rng.random(n).astype(np.float32), (rng.random(n) < 0.3).astype(np.uint8)
+    slot = rng.integers(-1, n + 1, entries + 3).astype(np.int32)
+    w = rng.random(entries + 3).astype(np.float32)
+    fresh = rng.integers(-1, n + 1, 1300).astype(np.int32)
+    for a in (0, 3):                                       # arrays that begin and end anywhere
+        s, x = dev(slot)[a:a + entries], dev(w)[a:a + entries]
+        m, p = dev(mass), torch.empty(n, dtype=torch.int32, device="cuda")
+        ws = torch.full((B.pool_weigh_workspace_bytes(n),), 0x5A, dtype=torch.uint8, device="cuda")
+        B.pool_weigh(dev(free), p, m, s, x, ws, decay=0.75, fresh=dev(fresh))
+        want_m, want_p = oa.weigh(mass, free, slot[a:a + entries], w[a:a + entries], np.float32(0.75), fresh)
+        assert np.array_equal(host(m).view(np.int32), want_m.view(np.int32)) and np.array_equal(host(p), want_p)
