@@ -19,6 +19,11 @@
 // step of the type each, which in a sum of many is what the result's own rounding is); scores, sums,
 // maxima and the results are fp32.
 //
+// What bounds it: the matrix core.  With 64 queries a tile's products take 1092 cycles of a SIMD (580 for the scores, 512
+// for the sums) of about 1830 that pass; the adding waves' reads, loads and products one after the other are the
+// longest chain (1630).  Measured on MI355X: 2048 rows x 128 heads x 2048 tokens 1.20 ms = 975 TFLOP/s (a library
+// product of 8192^3 1570), 64 x 16 in two groups behind 32768 107 us, 8 x 128 x 2048 22.8 us, 1 x 16 x 2048 13.3 us.
+//
 // A chunk's result goes straight to the outputs where it is the only one, otherwise unnormalised to
 // the workspace with its maximum and sum, and join_kernel adds the chunks up.
 #include <algorithm>

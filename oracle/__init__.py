@@ -23,7 +23,9 @@ prefetch (what the page fixes about the threshold prefetch: the eligible
 tokens, the bound in proportion to the context, the contract a prefetched pool
 satisfies, and one valid outcome).  In front of the scores: pages (page tables
 and slot maps of a paged cache), blockfp8 (FP8 in blocks of 128 and the scaled
-product), heads (norms and rotation of query and key heads).
+product), heads (norms and rotation of query and key heads).  Behind the
+selection: attention (over listed latent rows and shared prefixes, token
+weights, blocks by score, masses of the pool's slots).
 
 Readings of points the page leaves open are listed in each module's docstring.
 Parity status of every function is stated in its docstring ("pinned by ...").
