@@ -3,19 +3,19 @@
 //
 //   w[r][t] = sum_h exp(scale * q[r][h] . row_t - lse[r][h])
 //
-// A workgroup takes 128 tokens of one query row, 32 a wave, whose 576 values stay in registers, and goes through
+// A workgroup takes 64 or 128 tokens of one query row, a quarter a wave, whose 576 values stay in registers, and goes through
 // the heads in tiles of 16 that it stages in LDS: each cache row is read once for all heads, and the sum
 // over the heads ends in the workgroup.  The product runs on the matrix core as in attention.hip; its
 // result's columns are heads, so a lane adds up its own head's weights and the 16 lanes are joined at the end.
-// Measured on MI355X: 64 rows x 128 heads x 2048 tokens 44 us = 3.4 TB/s of rows (a copy reads and writes 4.8), 1 x 16 x
-// 2048 7.1 us; a workgroup's rows are read before its products, which other workgroups' reads lie under.
+// Measured on MI355X: 64 rows x 16 heads x 2048 tokens 27 us = 5.6 TB/s of rows, what reading them takes; 64 x 128 x 2048 44
+// us, where the heads' reads from LDS (1 KB for two products) bound it; 1 x 16 x 2048 5.0 us.
 #include <algorithm>
 
 #include "latent.cuh"
 
 namespace echo {
 
-constexpr int KSTEPS = LATENT / 32, TT = 2, WAVES = 4, WG_TOKENS = WAVES * TT * 16;
+constexpr int KSTEPS = LATENT / 32, WAVES = 4;
 
 struct WeightArgs {
   LatentArgs a;
@@ -48,8 +48,8 @@ ECHO_DEV void stage_heads(const uint8_t *q, int64_t head_bytes, int32_t ht, int3
 
 typedef v4f v4f_any __attribute__((aligned(4)));
 
-template <typename T>
-__global__ __launch_bounds__(WAVES * 64) void weights_kernel(WeightArgs x) {
+template <typename T, int TT>                              // 16 TT tokens a wave
+__global__ __launch_bounds__(WAVES * 64, TT == 1 ? 4 : 2) void weights_kernel(WeightArgs x) {
   typedef typename Mma<T>::x8 x8;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][QSTAGE];
   const int wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(WAVES * 64) void weights_kernel(WeightArgs x) {
   const int32_t r = static_cast<int32_t>(blockIdx.x / x.chunks), c = static_cast<int32_t>(blockIdx.x % x.chunks);
   const Tokens src = x.a.tokens(r);
   const uint8_t *q = reinterpret_cast<const uint8_t *>(x.a.q + r * x.a.q_row);
-  const int32_t tiles = (x.a.n_heads + 15) >> 4, t0 = c * WG_TOKENS + wv * TT * 16;
+  const int32_t tiles = (x.a.n_heads + 15) >> 4, t0 = (c * WAVES + wv) * TT * 16;
   stage_heads(q, x.a.q_head * 2, 0, x.a.n_heads, lds[0], wv);
   x8 k[TT][KSTEPS];
   uint32_t real[TT];
@@ -213,9 +213,17 @@ __global__ __launch_bounds__(256) void weigh_kernel(const uint64_t *__restrict__
   if (i < n) weigh(acc[i], i, gpu_free, priority, mass, decay);
 }
 
+// 16 tokens a wave have more waves on a SIMD and more workgroups, 32 read the heads from LDS half as often, which is what
+// many heads of many rows wait for.  Measured on MI355X, 2048 tokens a row (us, 16 and 32): 16 heads of 1 row 5.0 and 7.1, of 256
+// rows 95.8 and 97.7; 128 heads of 8 rows 12.2 and 14.1, of 64 rows 47.7 and 44.6.
 template <typename T>
-int launch_weights(const WeightArgs &x, hipStream_t st) {
-  weights_kernel<T><<<static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(x.chunks), WAVES * 64, 0, st>>>(x);
+int launch_weights(WeightArgs x, hipStream_t st) {
+  const auto chunks = [&](int tt) { return (x.a.n_tok + WAVES * tt * 16 - 1) / (WAVES * tt * 16); };
+  const bool few = x.a.n_heads <= 32 || static_cast<int64_t>(x.a.n_rows) * chunks(2) <= 512;
+  x.chunks = chunks(few ? 1 : 2);
+  const uint32_t grid = static_cast<uint32_t>(x.a.n_rows) * static_cast<uint32_t>(x.chunks);
+  if (few) weights_kernel<T, 1><<<grid, WAVES * 64, 0, st>>>(x);
+  else weights_kernel<T, 2><<<grid, WAVES * 64, 0, st>>>(x);
   return check_launch("attention weights");
 }
 
@@ -234,8 +242,7 @@ extern "C" int echo_attention_weights(const echo_latent_args *a, const float *ls
   if (!lse || !w) return fail(ECHO_EINVAL, "%s: NULL pointer", fn);
   if (reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(w) % 4) return fail(ECHO_EINVAL, "%s: an array is not aligned to its type", fn);
   x.lse = lse; x.w = w; x.w_ld = w_stride;
-  x.chunks = (x.a.n_tok + WG_TOKENS - 1) / WG_TOKENS;
-  if (static_cast<int64_t>(a->n_rows) * x.chunks >= 1 << 24) return fail(ECHO_EUNSUPPORTED, "%s: more rows and tokens than a launch holds", fn);
+  if (static_cast<int64_t>(a->n_rows) * ((x.a.n_tok + 63ll) / 64) >= 1 << 24) return fail(ECHO_EUNSUPPORTED, "%s: more rows and tokens than a launch holds", fn);
   return a->type == ECHO_BF16 ? launch_weights<bf16_t>(x, S(stream)) : launch_weights<fp16_t>(x, S(stream));
 }
 

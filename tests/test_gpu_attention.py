@@ -194,6 +194,23 @@ def test_weights_of_tokens(t, R, H, k, block):
             assert abs(got[r, :k * block].sum() - H) <= 1e-4 * H
 
 
+@pytest.mark.parametrize("t,R,H,k", [("bf16", 40, 33, 1700), ("fp16", 300, 40, 130), ("bf16", 600, 20, 70)])
+def test_weights_of_many_rows_full(t, R, H, k):
+    rng = np.random.default_rng(R + H)
+    announce("weights, many rows", t, R, H, k)
+    n = 3000
+    q, kv, idx = rand(rng, (R, H, 576), t).cuda(), rand(rng, (n, 576), t).cuda(), lists(rng, R, k, n)
+    idx[1], idx[2, 1:] = -1, -1
+    out, lse = sparse(q, kv, idx)
+    w = torch.full((R, k), -7.0, device="cuda")
+    B.attention_weights(q, kv, dev(idx), lse, w, SCALE)
+    listed = oa.listed_rows(idx, 1, n)
+    places, rows = [p for p, _ in listed], [r for _, r in listed]
+    want = oa.token_weights(f64(q), f64(kv), places, rows, f64(lse), SCALE, k)
+    _, want_lse, _, terms = oa.attention(f64(q), f64(kv), rows, SCALE)
+    assert (np.abs(host(w) - want) <= want * score_error(terms, want_lse).max() + 1e-30).all()
+
+
 # ---------------------------------------------------------------- shared prefixes
 def prefix_case(rng, R, H, groups, prefix, own, page, t):
     """groups: (first row, last row) pairs as a begin list; prefix lengths and own lengths given."""
