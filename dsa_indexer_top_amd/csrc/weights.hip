@@ -132,12 +132,15 @@ constexpr int64_t MAX_ENTRIES = 1 << 21;                   // 2^21 * 1024 * 2^32
 ECHO_DEV unsigned long long units(float w) {               // a NaN counts as 0
   return static_cast<unsigned long long>(rintf(fminf(fmaxf(w, 0.f), WEIGHT_MAX) * 0x1p32f));
 }
-ECHO_DEV void weigh(uint64_t a, int32_t i, const uint8_t *__restrict__ gpu_free, int32_t *__restrict__ priority, float *__restrict__ mass, float decay) {
+ECHO_DEV float weighed(uint64_t a, float mass, float decay) {
 #pragma clang fp contract(off)
-  const float old = a & FRESH ? 0.f : fmaxf(mass[i], 0.f) * decay;
-  const float m = old + static_cast<float>(a & ~FRESH) * 0x1p-32f;
+  const float old = a & FRESH ? 0.f : fmaxf(mass, 0.f) * decay;
+  return old + static_cast<float>(a & ~FRESH) * 0x1p-32f;
+}
+ECHO_DEV void weigh(uint64_t a, int32_t i, const uint8_t *__restrict__ gpu_free, int32_t *__restrict__ priority, float *__restrict__ mass, float decay) {
   const bool is_free = gpu_free[i] != 0;
-  mass[i] = is_free ? 0.f : m;
+  const float m = is_free ? 0.f : weighed(a, mass[i], decay);
+  mass[i] = m;
   priority[i] = is_free ? -1 : __float_as_int(m);
 }
 
@@ -190,9 +193,12 @@ __global__ __launch_bounds__(SEARCH) void weigh_search_kernel(const int32_t *__r
 }
 
 // Three launches, the sums in global memory.
+typedef uint64_t u64x4_any __attribute__((ext_vector_type(4), aligned(8)));
 __global__ __launch_bounds__(256) void weigh_clear_kernel(uint64_t *acc, int32_t n) {
-  const int32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n) acc[i] = 0;
+  const int32_t i = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (i + 4 <= n) *reinterpret_cast<u64x4_any *>(acc + i) = u64x4_any{0, 0, 0, 0};
+  else
+    for (int32_t e = i; e < n; ++e) acc[e] = 0;
 }
 
 __global__ __launch_bounds__(256) void weigh_add_kernel(const int32_t *__restrict__ slot, const float *__restrict__ w, int32_t n,
@@ -207,10 +213,27 @@ __global__ __launch_bounds__(256) void weigh_add_kernel(const int32_t *__restric
   }
 }
 
+// Four slots a thread.
+typedef uint8_t u8x4_any __attribute__((ext_vector_type(4), aligned(1)));
 __global__ __launch_bounds__(256) void weigh_kernel(const uint64_t *__restrict__ acc, const uint8_t *__restrict__ gpu_free,
                                                     int32_t *__restrict__ priority, float *__restrict__ mass, float decay, int32_t n) {
-  const int32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n) weigh(acc[i], i, gpu_free, priority, mass, decay);
+  const int32_t i = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (i + 4 <= n) {
+    const u64x4_any a = *reinterpret_cast<const u64x4_any *>(acc + i);
+    const u8x4_any f = *reinterpret_cast<const u8x4_any *>(gpu_free + i);
+    const f32x4_any m = *reinterpret_cast<const f32x4_any *>(mass + i);
+    f32x4_any to;
+    i32x4_any prio;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      to[e] = f[e] ? 0.f : weighed(a[e], m[e], decay);
+      prio[e] = f[e] ? -1 : __float_as_int(to[e]);
+    }
+    *reinterpret_cast<f32x4_any *>(mass + i) = to;
+    *reinterpret_cast<i32x4_any *>(priority + i) = prio;
+  } else {
+    for (int32_t e = i; e < n; ++e) weigh(acc[e], e, gpu_free, priority, mass, decay);
+  }
 }
 
 // 16 tokens a wave have more waves on a SIMD and more workgroups, 32 read the heads from LDS half as often, which is what
@@ -270,10 +293,10 @@ extern "C" int echo_pool_weigh(const uint8_t *gpu_free, int32_t *gpu_priority, f
                                                                    gpu_free, gpu_priority, mass, decay, n_gpu, per);
     return check_launch("pool weigh");
   }
-  weigh_clear_kernel<<<(n_gpu + 255) / 256, 256, 0, st>>>(static_cast<uint64_t *>(ws), n_gpu);
+  weigh_clear_kernel<<<(n_gpu + 1023) / 1024, 256, 0, st>>>(static_cast<uint64_t *>(ws), n_gpu);
   const uint32_t n = static_cast<uint32_t>(n_entries + n_fresh);
   weigh_add_kernel<<<(n + 255) / 256, 256, 0, st>>>(slot, w, static_cast<int32_t>(n_entries), fresh, static_cast<int32_t>(n_fresh),
                                                       static_cast<unsigned long long *>(ws), n_gpu);
-  weigh_kernel<<<(n_gpu + 255) / 256, 256, 0, st>>>(static_cast<const uint64_t *>(ws), gpu_free, gpu_priority, mass, decay, n_gpu);
+  weigh_kernel<<<(n_gpu + 1023) / 1024, 256, 0, st>>>(static_cast<const uint64_t *>(ws), gpu_free, gpu_priority, mass, decay, n_gpu);
   return check_launch("pool weigh");
 }
