@@ -462,3 +462,21 @@ def test_two_graphs_of_one_workspace():
             check(out, lse, q, kv, [r for _, r in oa.listed_rows(host(idx), 1, n)])
     for g, *_ in sets:
         g.close()
+
+
+@pytest.mark.parametrize("begin", [[0, 4, 2], [-5, 2, 100], [4, 4, 0], [1 << 30, -(1 << 30), 3]])
+def test_groups_that_are_none(begin):
+    """Group bounds that are not ascending rows: whatever the rows get, nothing else is touched, and the next call is whole."""
+    rng = np.random.default_rng(23)
+    R, H = 4, 16
+    c = prefix_case(rng, R, H, [0, 2, 4], [150, 90], [20, 0, 40, 1], 16, "bf16")
+    out = torch.full((R + 2, H, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((R + 2, H), 3.0, device="cuda")
+    ws = workspace(B.prefix_attention_workspace_bytes(R, H, 2, 150, 40))
+    tables = [dev(c[x]) for x in ("plen", "ptab", "olen", "otab")]
+    announce("groups", begin)
+    for b in (np.asarray(begin, np.int32), c["begin"]):
+        B.prefix_attention(c["q"], c["kv"], out[1:-1], SCALE, dev(b), *tables, 16, 150, 40, ws, lse=lse[1:-1])
+        for x in (out, lse):
+            assert (host(x[0].float()) == 3).all() and (host(x[-1].float()) == 3).all()
+    check(out[1:-1], lse[1:-1], c["q"], c["kv"], prefix_rows(c))
