@@ -2,11 +2,10 @@
 // its tokens' scores; the row's first and last blocks may be kept whatever they score.
 //
 // Reading the scores is all there is to it: a wave takes 1024 of them at a time in four loads, and the
-// lanes of a block are joined with moves between lanes.  On MI355X 4096 rows of 65536 scores (up to 1.07 GB, by their
-// lengths 0.8) with blocks of 128 take 148 us with the selection, 4 rows of 8192 6.8 us, most of that two launches.
-// The maxima alone take 140 us = 5.7 TB/s; with one load a wave, as at first, they took 242.
-// The blocks' scores, a 16th of the row or less, are selected from by a wave a row, or, above 512, by the
-// exact top-k of topk.hip.
+// lanes of a block are joined with moves between lanes.  The blocks' scores, a 16th of the row or less, are selected
+// from by one wave, in the same launch where a workgroup takes a row, or, above 512, by the exact top-k of
+// topk.hip.  On MI355X 4096 rows of 65536 scores (0.8 GB by their lengths) with blocks of 128 take 139 us = 5.8 TB/s, 4 rows of
+// 8192 4.6 us, a launch.  One load a wave, as at first, took 242 us for the maxima alone.
 #include <algorithm>
 
 #include "float_types.cuh"
@@ -21,22 +20,12 @@ struct OpMaxF {
   }
 };
 
-// One wave per 1024 tokens of a row, or per block where blocks are larger; four loads on their way.
+// The blocks of 1024 tokens from u * 1024 on, or, where blocks are larger, block u, by one wave; four loads on their way.
 constexpr int SPAN = 1024;
-template <int G>                                           // lanes of a block, 64 for blocks of 256 and more
-__global__ __launch_bounds__(256) void block_max_kernel(const float *__restrict__ scores, int64_t ld, const int32_t *__restrict__ len,
-                                                        int64_t waves, int32_t per_row, int32_t max_len, int32_t block, int32_t n_blocks,
-                                                        int32_t n_first, int32_t n_last, float *__restrict__ pooled, int32_t *__restrict__ count) {
-  const int64_t wave = blockIdx.x * 4ll + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  if (wave >= waves) return;
-  const int32_t r = static_cast<int32_t>(wave / per_row), u = static_cast<int32_t>(wave - static_cast<int64_t>(r) * per_row);
-  const int32_t n = max(0, min(len[r], max_len)), l = lane_id();
-  const int32_t nb = static_cast<int32_t>((static_cast<int64_t>(n) + block - 1) / block);
-  if (u == 0 && l == 0) count[r] = nb;
-  const int32_t span = max(block, SPAN);
+template <int G, typename S>                               // lanes of a block, 64 for blocks of 256 and more
+ECHO_DEV void span_max(const float *row, int32_t n, int32_t block, int32_t u, const S &store) {
+  const int32_t span = max(block, SPAN), l = lane_id();
   const int64_t t0 = static_cast<int64_t>(u) * span;
-  if (t0 >= n) return;
-  const float *row = scores + r * ld;
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};             // of the four 256ths
   for (int64_t t = t0 + 4 * l; t < t0 + span; t += SPAN) {
     if (t - 4 * l + SPAN <= n) {
@@ -51,8 +40,6 @@ __global__ __launch_bounds__(256) void block_max_kernel(const float *__restrict_
         for (int64_t e = t + 256 * i; e < min<int64_t>(n, t + 256 * i + 4); ++e) m[i] = fmaxf(m[i], row[e]);
     }
   }
-  float *out = pooled + static_cast<int64_t>(r) * n_blocks;
-  const auto store = [&](int32_t b, float v) { if (b < nb) out[b] = b < n_first || b >= nb - n_last ? INFINITY : v; };
   if (G < 64) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -72,22 +59,20 @@ __global__ __launch_bounds__(256) void block_max_kernel(const float *__restrict_
   }
 }
 
-// The k highest of up to 64 V blocks' scores, a wave a row: the k-th highest key bit by bit, each bit a count of the
-// keys that are not below (a ballot for 64 of them, no waits), then the blocks above it and the first of those that equal it, in order.
+// The k highest of n <= 64 V blocks' scores by one wave: the k-th highest key bit by bit, each bit a count of the
+// keys that are not below (a ballot for 64 of them, no waits), then the blocks above it and the first of those that
+// equal it, in order.
 template <int V>
-__global__ __launch_bounds__(256) void block_select_kernel(const float *__restrict__ pooled, int32_t n_blocks, const int32_t *__restrict__ count,
-                                                           int32_t n_rows, int32_t k, int32_t *__restrict__ idx) {
-  const int32_t r = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), l = lane_id();
-  if (r >= n_rows) return;
-  const int32_t n = count[r];
-  const float *row = pooled + static_cast<int64_t>(r) * n_blocks;
+ECHO_DEV void select(const float *pooled, int32_t n, int32_t k, int32_t *out) {
+  const int32_t l = lane_id();
   uint32_t key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = 64 * v + l < n ? f32_key(row[64 * v + l]) : 0u;       // a score's key is above 0
+  for (int v = 0; v < V; ++v) key[v] = 64 * v + l < n ? f32_key(pooled[64 * v + l]) : 0u;    // a score's key is above 0
+  const auto number = [](uint64_t m) { return static_cast<int32_t>(__popcll(m)); };
   const auto at_least = [&](uint32_t x) {
     int32_t c = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) c += static_cast<int32_t>(__popcll(__ballot(key[v] >= x)));
+    for (int v = 0; v < V; ++v) c += number(__ballot(key[v] >= x));
     return c;
   };
   uint32_t least = 1;                                      // of the keys taken
@@ -102,8 +87,6 @@ __global__ __launch_bounds__(256) void block_select_kernel(const float *__restri
     if (have != k) ties = k - (least == ~0u ? 0 : at_least(least + 1));
   }
   const uint64_t below = (1ull << l) - 1;
-  const auto number = [](uint64_t m) { return static_cast<int32_t>(__popcll(m)); };
-  int32_t *out = idx + static_cast<int64_t>(r) * k;
   int32_t pos = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -115,6 +98,58 @@ __global__ __launch_bounds__(256) void block_select_kernel(const float *__restri
     pos += number(all);
   }
   for (int32_t j = pos + l; j < k; j += 64) out[j] = -1;
+}
+
+struct BlockArgs {
+  const float *scores;
+  int64_t ld;
+  const int32_t *len;
+  int32_t n_rows, max_len, block, n_blocks, n_first, n_last, k;
+  ECHO_DEV int32_t length(int32_t r) const { return max(0, min(len[r], max_len)); }
+  ECHO_DEV int32_t blocks(int32_t n) const { return static_cast<int32_t>((static_cast<int64_t>(n) + block - 1) / block); }
+  ECHO_DEV bool kept(int32_t b, int32_t nb) const { return b < n_first || b >= nb - n_last; }
+};
+
+// One launch: a workgroup a row, its blocks' scores in LDS, selected from by the first wave.
+constexpr int ROW_WAVES = 8, ROW_BLOCKS = 512;
+template <int G>
+__global__ __launch_bounds__(ROW_WAVES * 64) void block_row_kernel(BlockArgs x, int32_t *__restrict__ idx) {
+  __shared__ float pooled[ROW_BLOCKS];
+  const int32_t r = blockIdx.x, n = x.length(r), nb = x.blocks(n), span = max(x.block, SPAN);
+  const int32_t wv = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int32_t spans = static_cast<int32_t>((static_cast<int64_t>(n) + span - 1) / span);
+  for (int32_t u = wv; u < spans; u += ROW_WAVES)
+    span_max<G>(x.scores + r * x.ld, n, x.block, u, [&](int32_t b, float v) { if (b < nb) pooled[b] = x.kept(b, nb) ? INFINITY : v; });
+  __syncthreads();
+  if (wv) return;
+  int32_t *out = idx + static_cast<int64_t>(r) * x.k;
+  if (nb <= 128) select<2>(pooled, nb, x.k, out);
+  else select<ROW_BLOCKS / 64>(pooled, nb, x.k, out);
+}
+
+// Two launches: the blocks' scores to memory, a wave a span, then the selection, a wave a row or topk.hip's.
+template <int G>
+__global__ __launch_bounds__(256) void block_max_kernel(BlockArgs x, int64_t waves, int32_t per_row, float *__restrict__ pooled, int32_t *__restrict__ count) {
+  const int64_t wave = blockIdx.x * 4ll + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  if (wave >= waves) return;
+  const int32_t r = static_cast<int32_t>(wave / per_row), u = static_cast<int32_t>(wave - static_cast<int64_t>(r) * per_row);
+  const int32_t n = x.length(r), nb = x.blocks(n);
+  if (u == 0 && lane_id() == 0) count[r] = nb;
+  if (static_cast<int64_t>(u) * max(x.block, SPAN) >= n) return;
+  float *out = pooled + static_cast<int64_t>(r) * x.n_blocks;
+  span_max<G>(x.scores + r * x.ld, n, x.block, u, [&](int32_t b, float v) { if (b < nb) out[b] = x.kept(b, nb) ? INFINITY : v; });
+}
+__global__ __launch_bounds__(256) void block_select_kernel(const float *__restrict__ pooled, int32_t n_blocks, const int32_t *__restrict__ count,
+                                                           int32_t n_rows, int32_t k, int32_t *__restrict__ idx) {
+  const int32_t r = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  if (r < n_rows) select<ROW_BLOCKS / 64>(pooled + static_cast<int64_t>(r) * n_blocks, count[r], k, idx + static_cast<int64_t>(r) * k);
+}
+
+template <int G>
+int launch(const BlockArgs &x, bool one, int64_t waves, int32_t per_row, float *pooled, int32_t *count, int32_t *idx, hipStream_t st) {
+  if (one) block_row_kernel<G><<<x.n_rows, ROW_WAVES * 64, 0, st>>>(x, idx);
+  else block_max_kernel<G><<<static_cast<uint32_t>((waves + 3) / 4), 256, 0, st>>>(x, waves, per_row, pooled, count);
+  return check_launch("block maxima");
 }
 
 }  // namespace echo
@@ -149,25 +184,17 @@ extern "C" int echo_block_topk(const float *scores, int64_t ld, const int32_t *l
   if (reinterpret_cast<uintptr_t>(ws) % 4) return fail(ECHO_EINVAL, "%s: the workspace is not aligned to its type", fn);
   float *pooled = static_cast<float *>(ws);
   int32_t *count = reinterpret_cast<int32_t *>(pooled + static_cast<int64_t>(n_rows) * n_blocks);
-  const uint32_t grid = static_cast<uint32_t>((waves + 3) / 4);
   const hipStream_t st = S(stream);
-#define RUN(G) block_max_kernel<G><<<grid, 256, 0, st>>>(scores, ld, len, waves, per_row, max_len, block, n_blocks, n_first, n_last, pooled, count)
-  switch (block) {
-    case 16: RUN(4); break;
-    case 32: RUN(8); break;
-    case 64: RUN(16); break;
-    case 128: RUN(32); break;
-    default: RUN(64); break;
-  }
-#undef RUN
-  const int rc = check_launch("block maxima");
-  if (rc != ECHO_OK) return rc;
-#define RUN(V) block_select_kernel<V><<<(n_rows + 3) / 4, 256, 0, st>>>(pooled, n_blocks, count, n_rows, k, idx)
-  // Measured on MI355X, both launches (us, and with topk.hip's): 128 blocks of 1 row 6.7 and 13.8; 512 blocks of 1 row 9.0 and 14.4, of
-  // 4096 rows 148 and 195; 1024 blocks of 1 row 16.4 and 15.0, 2048 of 64 rows 29 and 22.5.
-  if (n_blocks <= 128) RUN(2);
-  else if (n_blocks <= 512) RUN(8);
-  else return launch_topk_rows(pooled, n_blocks, count, n_rows, n_blocks, k, nullptr, idx, st);
-#undef RUN
+  const BlockArgs x = {scores, ld, len, n_rows, max_len, block, n_blocks, n_first, n_last, k};
+  // One launch for rows that a workgroup reads fast enough, or as many rows as fill the card.  Measured on MI355X (us, in
+  // one launch and in two): 4 rows of 8192 4.6 and 7.1, 1 of 32768 7.7 and 9.2, 256 of 65536 15.7 and 19.0, 4096 of 65536 139 and
+  // 148; 64 of 65536 13.8 and 13.1, 4096 of 8192 27.4 and 26.2.
+  const bool one = n_blocks <= ROW_BLOCKS && (max_len <= 65536 || n_rows >= 512);
+  const auto go = block == 16 ? launch<4> : block == 32 ? launch<8> : block == 64 ? launch<16> : block == 128 ? launch<32> : launch<64>;
+  const int rc = go(x, one, waves, per_row, pooled, count, idx, st);
+  if (rc != ECHO_OK || one) return rc;
+  // 512 blocks of 1 row 9.0 us, 14.4 with topk.hip's; 1024 16.4 and 15.0, 2048 of 64 rows 29 and 22.5.
+  if (n_blocks > ROW_BLOCKS) return launch_topk_rows(pooled, n_blocks, count, n_rows, n_blocks, k, nullptr, idx, st);
+  block_select_kernel<<<(n_rows + 3) / 4, 256, 0, st>>>(pooled, n_blocks, count, n_rows, k, idx);
   return check_launch("block selection");
 }

@@ -181,3 +181,14 @@ def test_weigh_either_way(n, entries):
         B.pool_weigh(dev(free), p, m, s, x, ws, decay=0.75, fresh=dev(fresh))
         want_m, want_p = oa.weigh(mass, free, slot[a:a + entries], w[a:a + entries], np.float32(0.75), fresh)
         assert np.array_equal(host(m).view(np.int32), want_m.view(np.int32)) and np.array_equal(host(p), want_p)
+
+
+@pytest.mark.parametrize("R,n,block,k", [(3, 70000, 256, 20), (2, 66000, 4096, 5), (520, 66000, 1024, 9), (2, 65536, 128, 600)])
+def test_long_rows_full(R, n, block, k):
+    """Few long rows in two launches, many in one, and more asked for than there are."""
+    rng = np.random.default_rng(n + R)
+    scores = np.round(50 * rng.standard_normal((R, n)).astype(np.float32))
+    length = rng.integers(0, n + 1, R)
+    length[0] = n
+    announce("long rows", R, n, block, k)
+    assert np.array_equal(block_topk(scores, length, block, k, 1, 2), oa.block_topk(scores, length, block, k, 1, 2))
