@@ -528,8 +528,8 @@ ECHO_DEV void attend(const AttArgs &x, const Work &w, Lds &lds) {
     const uint32_t u = static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, i)), v = static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, i));
     uint8_t *p = reinterpret_cast<uint8_t *>(static_cast<uint64_t>(v) << 32 | u) + 16 * l;
     if (w.q0 + at >= w.q1) break;
-    if (whole) {
-      *reinterpret_cast<u32x4 *>(p) = *reinterpret_cast<const u32x4 *>(lds.stage + at * OUT_ROW + 16 * l);
+    if (whole) {                                           // past the caches, which hold the rows (202 x 128 heads x 73 tokens 36.0 -> 34.6 us)
+      __builtin_nontemporal_store(*reinterpret_cast<const u32x4 *>(lds.stage + at * OUT_ROW + 16 * l), reinterpret_cast<u32x4 *>(p));
     } else {
       *reinterpret_cast<u32x4 *>(p) = *reinterpret_cast<const u32x4 *>(lds.stage + at * PART_ROW + 16 * l);
       *reinterpret_cast<u32x4 *>(p + 1024) = *reinterpret_cast<const u32x4 *>(lds.stage + at * PART_ROW + 1024 + 16 * l);
